@@ -307,6 +307,151 @@ int mfd_verify(const float *target_logits, int n_req, int B, int V, int L,
                int32_t *path_nodes, int32_t *out_tokens, int32_t *status, void *ws,
                size_t ws_bytes, mfd_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The target's attention over a paged key-value cache: the part of a round
+ * between mfd_build_tree and mfd_verify (project page, How it works, step 3,
+ * and Figure 2 (c): the target scores every node of the tree in one pass
+ * under the tree mask).  Per layer of the target:
+ *
+ *   mfd_kv_append       queries and keys of the tree's nodes get their norm
+ *                       and position rotation; keys and values go into the
+ *                       cache's pages, behind the context
+ *   mfd_tree_attention  the nodes attend to the context and, under the tree
+ *                       mask, to each other
+ *   mfd_kv_commit       after mfd_verify: the accepted path's entries move
+ *                       to where the next round's context ends
+ *
+ * N counts the rows of a request: the tree's B + 1 nodes, one new token
+ * (N = 1), or a stretch of a prompt.  Row n of request q sits at cache
+ * position ctx_len[q] + n; its rotation position is pos[q][n], which for a
+ * tree is the one mfd_build_tree emits.  n_nodes[q] <= N rows are live (NULL:
+ * all N); the others are neither read nor cached.
+ *
+ * Element types.  Queries and outputs are bf16 or fp16.  A cache holds the
+ * same type, or E4M3 with one power of two per (position, head) row of D
+ * values: e is the smallest integer >= -127 with max|x| <= 448 * 2^e, the row
+ * holds e4m3(x * 2^-e) (round to nearest even) and the byte e + 127.  A power
+ * of two makes the held value q * 2^e exact in bf16 (and in fp16 inside its
+ * range), so reading back rounds nothing.  A row with a NaN or an infinity
+ * gets the byte 255 and reads back as NaN in whole; a value that would round
+ * past the type's largest is held as the grid's next lower one. */
+enum { MFD_BF16 = 0, MFD_FP16 = 1, MFD_E4M3 = 2 };
+
+/* A paged cache.  This struct lives on the host and is read during the call;
+ * its pointers are device memory.  Entry (page g, head h, slot s) starts at
+ * element g * page_stride + h * head_stride + s * token_stride of k and of v,
+ * D contiguous elements; position p of request q is slot p % page_size of page
+ * block_table[q][p / page_size].  E4M3 caches also have k_exp and v_exp, uint8
+ * [n_pages][Hk][page_size] contiguous (NULL otherwise).
+ * Limits: page_size 16, 32, 64, 128 or 256; D % 16 == 0, 16 <= D <= 256;
+ * k, v and the strides in bytes multiples of 16; strides >= D;
+ * max_pages * page_size < 2^31 - 65536.  A block table entry outside
+ * [0, n_pages), or a position past max_pages * page_size, sets MFD_ERR_INPUT
+ * in *status; nothing outside the cache is touched. */
+typedef struct {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+  const int32_t *block_table; /* [n_req][max_pages] */
+  int32_t dtype;              /* MFD_BF16, MFD_FP16 or MFD_E4M3 */
+  int32_t n_pages, page_size, max_pages;
+  int32_t Hk, D;
+  int64_t page_stride, head_stride, token_stride; /* elements */
+} mfd_kv_cache;
+
+/* Rotation phases.  Angle i of position p is p * inv_freq[i]; it is taken as
+ * p * phase[i] modulo 2^64, phase[i] = inv_freq[i] / (2 pi) in units of 2^-64
+ * turns, so a far position loses no precision.  Host only: inv_freq and phase
+ * are host arrays of n; the caller copies phase to the device.  Errors:
+ * INVALID_ARG (NULL, n < 1, a frequency that is negative or not finite). */
+int mfd_rope_phases(const double *inv_freq, int n, uint64_t *phase);
+
+/* Norm and rotation of queries and keys, each head's row of D:
+ *   y = x / sqrt(mean(x^2) + eps) * w      (fp32; w NULL: y = x)
+ * then the first rot_dim elements turn by their angles: pairs (i, i + rot_dim
+ * / 2), or (2i, 2i + 1) with `interleaved`: (u, v) -> (u cos - v sin, v cos + u
+ * sin); one rounding to the output's type at the end.
+ *   q, k      [T][Hq][D], [T][Hk][D] of `dtype` (MFD_BF16 or MFD_FP16); tokens
+ *             q_stride, k_stride elements apart (a multiple of 8, at least
+ *             heads * D), heads contiguous; 16-byte aligned
+ *   q_w, k_w  [D] of `dtype`, 16-byte aligned, or NULL (no norm)
+ *   phase     uint64 [rot_dim / 2] from mfd_rope_phases, or NULL with rot_dim 0
+ *   pos       int32 [T]
+ *   q_out, k_out  [T][Hq][D], [T][Hk][D] contiguous; may be q, k themselves
+ *             where those are contiguous
+ * rot_dim even, 0 <= rot_dim <= D; eps >= 0.  Errors: INVALID_ARG, UNSUPPORTED
+ * (D as for a cache, Hq or Hk > 1024), CUDA. */
+int mfd_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int dtype, int T, int Hq,
+                     int Hk, int D, const void *q_w, const void *k_w, float eps, const uint64_t *phase, int rot_dim,
+                     int interleaved, const int32_t *pos, void *q_out, void *k_out, int32_t *status,
+                     mfd_stream_t stream);
+
+/* mfd_qk_norm_rope of N rows per request with the keys, and the values as they
+ * are, written into the cache at positions ctx_len[q] + n (one pass, one
+ * launch).  q, k, v: [n_req * N] tokens, strided as above; pos int32
+ * [n_req][N]; ctx_len, n_nodes int32 [n_req] (n_nodes may be NULL); q_out
+ * [n_req][N][Hq][D], zero past n_nodes.  Hq may be 0 with q and q_out NULL: the
+ * cache write alone.  Hk, D and the cache's type come from `cache`, whose type
+ * is `dtype` or MFD_E4M3.  Keys are quantised from fp32.  The pages of live
+ * rows must be distinct.  Device errors (MFD_ERR_INPUT): n_nodes outside [0,
+ * N], ctx_len < 0, a position or page outside the cache; that request's rows,
+ * or that row's entry, are then not written. */
+int mfd_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                  int dtype, int n_req, int N, int Hq, const void *q_w, const void *k_w, float eps,
+                  const uint64_t *phase, int rot_dim, int interleaved, const int32_t *pos, const int32_t *ctx_len,
+                  const int32_t *n_nodes, void *q_out, const mfd_kv_cache *cache, int32_t *status,
+                  mfd_stream_t stream);
+
+/* Reads a stretch of every request back: positions start[q] .. start[q] +
+ * length[q] - 1 to k_out, v_out [n_req][L_max][Hk][D] of `dtype` (MFD_BF16 or
+ * MFD_FP16; the cache's type, or either from MFD_E4M3), zero past length[q].
+ * start, length int32 [n_req].  Device errors (MFD_ERR_INPUT): start < 0,
+ * length outside [0, L_max], a position or page outside the cache; such
+ * entries are written as zeros. */
+int mfd_kv_read(const mfd_kv_cache *cache, int n_req, int L_max, const int32_t *start, const int32_t *length,
+                int dtype, void *k_out, void *v_out, int32_t *status, mfd_stream_t stream);
+
+/* Keeps the accepted path: entry ctx_len[q] + path_nodes[q][j] moves to
+ * ctx_len[q] + j for j = 1..accept_len[q] (node 0, the root, stays), in place,
+ * and new_len[q] = ctx_len[q] + accept_len[q] + 1.  accept_len and path_nodes
+ * [n_req][L + 1] as mfd_verify writes them; n_nodes int32 [n_req] as the
+ * append's.  new_len may be ctx_len.  Device errors (MFD_ERR_INPUT): accept_len
+ * outside [0, L], a path that does not start at node 0, does not increase or
+ * leaves [0, n_nodes), a position or page outside the cache; that request's
+ * entries stay and its new_len is ctx_len.  1 <= L <= 16. */
+int mfd_kv_commit(const mfd_kv_cache *cache, int n_req, int L, const int32_t *ctx_len, const int32_t *accept_len,
+                  const int32_t *path_nodes, const int32_t *n_nodes, int32_t *new_len, int32_t *status,
+                  mfd_stream_t stream);
+
+/* Attention of N rows per request over the paged cache (the rows' own entries
+ * are in it: mfd_kv_append).  Row n of request q, query head h, reads key head
+ * h / (Hq / Hk) at every position t that it sees:
+ *   t < ctx_len[q], or t = ctx_len[q] + j, j < n_nodes[q], with bit j of
+ *   mask[q][n] set (mask NULL: j <= n)
+ *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t)
+ * A row that sees nothing, or past n_nodes, gets zeros and lse -inf.  What a
+ * row does not see does not reach it, infinities and NaN included.
+ *   q     [n_req * N] tokens of [Hq][D], q_stride elements apart (as above),
+ *         `dtype` MFD_BF16 or MFD_FP16; the cache's type, or any over MFD_E4M3
+ *   mask  uint32 [n_req][N][ceil(N / 32)] from mfd_build_tree, or NULL (causal)
+ *   scale finite, > 0
+ *   out   [n_req][N][Hq][D] of `dtype`, 16-byte aligned; lse fp32
+ *         [n_req][N][Hq] (natural log) or NULL
+ *   ws    mfd_tree_attention_workspace_bytes(n_req, N, Hq, Hk, D), 256-byte
+ *         aligned; needs no zeroing and keeps nothing between calls
+ * Scores, softmax statistics and sums are fp32; a row's weights are rounded to
+ * `dtype` for the product with the values.  The split over the cache's length
+ * follows the lengths on the device, so a captured call may be replayed with
+ * other lengths.  Results do not change from run to run.
+ * Limits: n_req <= 1024, N <= 4096, Hq % Hk == 0, Hq <= 1024, N * (Hq / Hk) <=
+ * 65536.  Device errors (MFD_ERR_INPUT): ctx_len < 0, n_nodes outside [0, N],
+ * positions or pages outside the cache (values clamped, results not to be
+ * trusted); MFD_ERR_TIMEOUT as for every bounded wait. */
+size_t mfd_tree_attention_workspace_bytes(int n_req, int N, int Hq, int Hk, int D);
+int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, int N, int Hq,
+                       const mfd_kv_cache *cache, const int32_t *ctx_len, const int32_t *n_nodes,
+                       const uint32_t *mask, float scale, void *out, float *lse, int32_t *status, void *ws,
+                       size_t ws_bytes, mfd_stream_t stream);
+
 /* Tree analytics: what a tree spends its budget on (project page "Multi-Future
  * Drafting", TL;DR and Abstract: chimeras -- prefixes spliced from different
  * futures that the target never produces; How it works, step 1, and "What the

@@ -4,12 +4,14 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstring>
 #include <map>
 #include <mutex>
 #include <tuple>
 
 #include "../../include/mfd.h"
+#include "kvcache.h"
 #include "lmhead.h"
 
 namespace {
@@ -671,6 +673,253 @@ int mfd_verify_withheld_test(const float *target_logits, int n_req, int B, int V
   if (wait_limit_ns < 1000ull || wait_limit_ns > 100000000ull) return MFD_ERR_INVALID_ARG;
   return verify_call(target_logits, n_req, B, V, L, parent, token, n_nodes, temperature, seed, accept_len,
                      path_nodes, out_tokens, status, ws, ws_bytes, stream, wait_limit_ns, 1);
+}
+
+}  // extern "C"
+
+// ------------------------------------------- attention over a paged cache
+namespace {
+
+// mfd_kv_cache to the kernels' view, with its limits checked.
+int cache_view(const mfd_kv_cache *c, mfd::CacheView *out) {
+  if (!c || !c->k || !c->v || !c->block_table) return MFD_ERR_INVALID_ARG;
+  if (c->dtype != MFD_BF16 && c->dtype != MFD_FP16 && c->dtype != MFD_E4M3) return MFD_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->Hk < 1 || c->D < 1) return MFD_ERR_INVALID_ARG;
+  const bool e4m3 = c->dtype == MFD_E4M3;
+  if (e4m3 && (!c->k_exp || !c->v_exp)) return MFD_ERR_INVALID_ARG;
+  const int64_t esz = e4m3 ? 1 : 2;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->block_table, 4)) return MFD_ERR_INVALID_ARG;
+  if (c->D % 16 != 0 || c->D > 256 || c->Hk > 1024) return MFD_ERR_UNSUPPORTED;
+  const int64_t strides[3] = {c->page_stride, c->head_stride, c->token_stride};
+  for (int64_t s : strides) {
+    if (s < c->D || s * esz % 16 != 0) return MFD_ERR_INVALID_ARG;
+    if (s * esz >= ((int64_t)1 << 40)) return MFD_ERR_UNSUPPORTED;  // a tensor map's stride
+  }
+  int shift = 4;
+  while (shift < 8 && (1 << shift) < c->page_size) ++shift;
+  if ((1 << shift) != c->page_size) return MFD_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31) - 65536) return MFD_ERR_UNSUPPORTED;
+  out->k = c->k;
+  out->v = c->v;
+  out->k_exp = e4m3 ? c->k_exp : nullptr;
+  out->v_exp = e4m3 ? c->v_exp : nullptr;
+  out->table = c->block_table;
+  out->dtype = c->dtype;
+  out->n_pages = c->n_pages;
+  out->ps_shift = shift;
+  out->max_pages = c->max_pages;
+  out->Hk = c->Hk;
+  out->D = c->D;
+  out->page_stride = c->page_stride;
+  out->head_stride = c->head_stride;
+  out->token_stride = c->token_stride;
+  return MFD_OK;
+}
+
+int need_sm103() {
+  DeviceInfo d;
+  const int rc = current_device_info(&d);
+  if (rc != MFD_OK) return rc;
+  return is_sm103(d) ? MFD_OK : MFD_ERR_UNSUPPORTED;
+}
+
+// A [tokens][heads][D] tensor of 16-bit elements with its token stride.
+bool rows_ok(const void *p, int64_t stride, int heads, int D) {
+  return p && aligned(p, 16) && stride >= (int64_t)heads * D && stride % 8 == 0 && stride < ((int64_t)1 << 40);
+}
+
+// What the norm and rotation of mfd_qk_norm_rope and mfd_kv_append share.
+int norm_rope_args(int dtype, int D, const void *q_w, const void *k_w, float eps, const uint64_t *phase, int rot_dim,
+                   const int32_t *pos, const int32_t *status) {
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (!pos || !status || D < 1) return MFD_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return MFD_ERR_INVALID_ARG;
+  if ((q_w && !aligned(q_w, 16)) || (k_w && !aligned(k_w, 16))) return MFD_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0 || (rot_dim > 0 && !phase)) return MFD_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 256) return MFD_ERR_UNSUPPORTED;
+  return MFD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mfd_rope_phases(const double *inv_freq, int n, uint64_t *phase) {
+  if (!inv_freq || !phase || n < 1) return MFD_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!(inv_freq[i] >= 0.0) || !std::isfinite(inv_freq[i])) return MFD_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    const double turns = inv_freq[i] / 6.283185307179586476925;
+    const double part = turns - std::floor(turns);  // in [0, 1), at most 1 - 2^-53
+    phase[i] = static_cast<uint64_t>(std::ldexp(part, 64));
+  }
+  return MFD_OK;
+}
+
+int mfd_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int dtype, int T, int Hq,
+                     int Hk, int D, const void *q_w, const void *k_w, float eps, const uint64_t *phase, int rot_dim,
+                     int interleaved, const int32_t *pos, void *q_out, void *k_out, int32_t *status,
+                     mfd_stream_t stream) {
+  if (T < 1 || Hq < 1 || Hk < 1) return MFD_ERR_INVALID_ARG;
+  int rc = norm_rope_args(dtype, D, q_w, k_w, eps, phase, rot_dim, pos, status);
+  if (rc != MFD_OK) return rc;
+  if (!rows_ok(q, q_stride, Hq, D) || !rows_ok(k, k_stride, Hk, D)) return MFD_ERR_INVALID_ARG;
+  if (!q_out || !k_out || !aligned(q_out, 16) || !aligned(k_out, 16)) return MFD_ERR_INVALID_ARG;
+  if (Hq > 1024 || Hk > 1024) return MFD_ERR_UNSUPPORTED;
+  if ((rc = need_sm103()) != MFD_OK) return rc;
+  mfd::AppendLaunch A = {};
+  A.q = q;
+  A.k = k;
+  A.q_stride = q_stride;
+  A.k_stride = k_stride;
+  A.dtype = dtype;
+  A.n_req = 1;
+  A.N = T;
+  A.Hq = Hq;
+  A.Hk = Hk;
+  A.D = D;
+  A.q_w = q_w;
+  A.k_w = k_w;
+  A.eps = eps;
+  A.phase = phase;
+  A.rot_dim = rot_dim;
+  A.interleaved = interleaved != 0;
+  A.pos = pos;
+  A.q_out = q_out;
+  A.k_out = k_out;
+  A.status = status;
+  return cuda_status(mfd::launch_kv_append(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                  int dtype, int n_req, int N, int Hq, const void *q_w, const void *k_w, float eps,
+                  const uint64_t *phase, int rot_dim, int interleaved, const int32_t *pos, const int32_t *ctx_len,
+                  const int32_t *n_nodes, void *q_out, const mfd_kv_cache *cache, int32_t *status,
+                  mfd_stream_t stream) {
+  mfd::CacheView cv;
+  int rc = cache_view(cache, &cv);
+  if (rc != MFD_OK) return rc;
+  if (n_req < 1 || N < 1 || Hq < 0 || !ctx_len) return MFD_ERR_INVALID_ARG;
+  if ((rc = norm_rope_args(dtype, cv.D, q_w, k_w, eps, phase, rot_dim, pos, status)) != MFD_OK) return rc;
+  if (cv.dtype != dtype && cv.dtype != MFD_E4M3) return MFD_ERR_INVALID_ARG;
+  if (Hq > 0 && (!rows_ok(q, q_stride, Hq, cv.D) || !q_out || !aligned(q_out, 16))) return MFD_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride, cv.Hk, cv.D) || !rows_ok(v, v_stride, cv.Hk, cv.D)) return MFD_ERR_INVALID_ARG;
+  if (Hq > 1024 || (int64_t)n_req * N >= ((int64_t)1 << 31) - 1) return MFD_ERR_UNSUPPORTED;
+  if ((rc = need_sm103()) != MFD_OK) return rc;
+  mfd::AppendLaunch A = {};
+  A.q = q;
+  A.k = k;
+  A.v = v;
+  A.q_stride = q_stride;
+  A.k_stride = k_stride;
+  A.v_stride = v_stride;
+  A.dtype = dtype;
+  A.n_req = n_req;
+  A.N = N;
+  A.Hq = Hq;
+  A.Hk = cv.Hk;
+  A.D = cv.D;
+  A.q_w = Hq ? q_w : nullptr;
+  A.k_w = k_w;
+  A.eps = eps;
+  A.phase = phase;
+  A.rot_dim = rot_dim;
+  A.interleaved = interleaved != 0;
+  A.pos = pos;
+  A.ctx_len = ctx_len;
+  A.n_nodes = n_nodes;
+  A.q_out = q_out;
+  A.cache = &cv;
+  A.status = status;
+  return cuda_status(mfd::launch_kv_append(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_kv_read(const mfd_kv_cache *cache, int n_req, int L_max, const int32_t *start, const int32_t *length,
+                int dtype, void *k_out, void *v_out, int32_t *status, mfd_stream_t stream) {
+  mfd::CacheView cv;
+  int rc = cache_view(cache, &cv);
+  if (rc != MFD_OK) return rc;
+  if (n_req < 1 || L_max < 1 || !start || !length || !k_out || !v_out || !status) return MFD_ERR_INVALID_ARG;
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (cv.dtype != MFD_E4M3 && cv.dtype != dtype) return MFD_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return MFD_ERR_INVALID_ARG;
+  if (n_req > 65535 || (int64_t)L_max * cv.Hk >= ((int64_t)1 << 33)) return MFD_ERR_UNSUPPORTED;
+  if ((rc = need_sm103()) != MFD_OK) return rc;
+  mfd::KvReadLaunch A;
+  A.cache = cv;
+  A.n_req = n_req;
+  A.L_max = L_max;
+  A.dtype = dtype;
+  A.start = start;
+  A.length = length;
+  A.k_out = k_out;
+  A.v_out = v_out;
+  A.status = status;
+  return cuda_status(mfd::launch_kv_read(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_kv_commit(const mfd_kv_cache *cache, int n_req, int L, const int32_t *ctx_len, const int32_t *accept_len,
+                  const int32_t *path_nodes, const int32_t *n_nodes, int32_t *new_len, int32_t *status,
+                  mfd_stream_t stream) {
+  mfd::CacheView cv;
+  int rc = cache_view(cache, &cv);
+  if (rc != MFD_OK) return rc;
+  if (n_req < 1 || L < 1 || !ctx_len || !accept_len || !path_nodes || !n_nodes || !new_len || !status)
+    return MFD_ERR_INVALID_ARG;
+  if (L > 16) return MFD_ERR_UNSUPPORTED;
+  if ((rc = need_sm103()) != MFD_OK) return rc;
+  mfd::KvCommitLaunch A;
+  A.cache = cv;
+  A.n_req = n_req;
+  A.L = L;
+  A.ctx_len = ctx_len;
+  A.accept_len = accept_len;
+  A.path = path_nodes;
+  A.n_nodes = n_nodes;
+  A.new_len = new_len;
+  A.status = status;
+  return cuda_status(mfd::launch_kv_commit(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mfd_tree_attention_workspace_bytes(int n_req, int N, int Hq, int Hk, int D) {
+  if (n_req < 1 || n_req > 1024 || N < 1 || N > 4096 || Hq < 1 || Hk < 1 || Hq > 1024 || Hq % Hk != 0 ||
+      (int64_t)N * (Hq / Hk) > 65536 || D < 16 || D > 256 || D % 16 != 0)
+    return 0;
+  return 256;
+}
+
+int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, int N, int Hq,
+                       const mfd_kv_cache *cache, const int32_t *ctx_len, const int32_t *n_nodes,
+                       const uint32_t *mask, float scale, void *out, float *lse, int32_t *status, void *ws,
+                       size_t ws_bytes, mfd_stream_t stream) {
+  mfd::CacheView cv;
+  int rc = cache_view(cache, &cv);
+  if (rc != MFD_OK) return rc;
+  if (n_req < 1 || N < 1 || Hq < 1 || !ctx_len || !out || !status) return MFD_ERR_INVALID_ARG;
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (cv.dtype != dtype && cv.dtype != MFD_E4M3) return MFD_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_stride, Hq, cv.D) || !aligned(out, 16)) return MFD_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return MFD_ERR_INVALID_ARG;
+  const size_t need = mfd_tree_attention_workspace_bytes(n_req, N, Hq, cv.Hk, cv.D);
+  if (need == 0) return MFD_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < need || !aligned(ws, 256)) return MFD_ERR_WORKSPACE;
+  if ((rc = need_sm103()) != MFD_OK) return rc;
+  mfd::AttentionLaunch A;
+  A.q = q;
+  A.q_stride = q_stride;
+  A.dtype = dtype;
+  A.n_req = n_req;
+  A.N = N;
+  A.Hq = Hq;
+  A.cache = cv;
+  A.ctx_len = ctx_len;
+  A.n_nodes = n_nodes;
+  A.mask = mask;
+  A.scale = scale;
+  A.out = out;
+  A.lse = lse;
+  A.status = status;
+  return cuda_status(mfd::launch_tree_attention(A, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -39,8 +39,22 @@ EXPORTS = ("mfd_status_string", "mfd_workspace_size", "mfd_lmhead_topk", "mfd_lm
            "mfd_logits_topk_noalloc",
            "mfd_build_tree", "mfd_verify", "mfd_verify_withheld_test", "mfd_lmhead_withheld_test", "mfd_mfdd_modes",
            "mfd_lmhead_packed_fp8_bytes", "mfd_lmhead_pack_fp8", "mfd_fp8_quantize_rows",
-           "mfd_lmhead_fp8_workspace_bytes", "mfd_lmhead_topk_fp8", "mfd_tree_analytics")
+           "mfd_lmhead_fp8_workspace_bytes", "mfd_lmhead_topk_fp8", "mfd_tree_analytics",
+           "mfd_rope_phases", "mfd_qk_norm_rope", "mfd_kv_append", "mfd_kv_read", "mfd_kv_commit",
+           "mfd_tree_attention_workspace_bytes", "mfd_tree_attention")
 NOALLOC_SCRATCH_BYTES = 4 << 20
+
+MFD_BF16, MFD_FP16, MFD_E4M3 = 0, 1, 2
+_DTYPE = {torch.bfloat16: MFD_BF16, torch.float16: MFD_FP16, torch.float8_e4m3fn: MFD_E4M3}
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """mfd_kv_cache of include/mfd.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 _lock = threading.Lock()
 _lib = None
@@ -120,6 +134,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.mfd_lmhead_topk_fp8.restype = I
         lib.mfd_tree_analytics.argtypes = [P, P, P, P, I, I, I, P, I, P, I, P, P, P, P, P, P, SZ, P]
         lib.mfd_tree_analytics.restype = I
+        I64, F, C = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(_KvCacheStruct)
+        lib.mfd_rope_phases.argtypes = [P, I, P]
+        lib.mfd_rope_phases.restype = I
+        lib.mfd_qk_norm_rope.argtypes = [P, I64, P, I64, I, I, I, I, I, P, P, F, P, I, I, P, P, P, P, P]
+        lib.mfd_qk_norm_rope.restype = I
+        lib.mfd_kv_append.argtypes = [P, I64, P, I64, P, I64, I, I, I, I, P, P, F, P, I, I, P, P, P, P, C, P, P]
+        lib.mfd_kv_append.restype = I
+        lib.mfd_kv_read.argtypes = [C, I, I, P, P, I, P, P, P, P]
+        lib.mfd_kv_read.restype = I
+        lib.mfd_kv_commit.argtypes = [C, I, I, P, P, P, P, P, P, P]
+        lib.mfd_kv_commit.restype = I
+        lib.mfd_tree_attention_workspace_bytes.argtypes = [I] * 5
+        lib.mfd_tree_attention_workspace_bytes.restype = SZ
+        lib.mfd_tree_attention.argtypes = [P, I64, I, I, I, I, C, P, P, P, F, P, P, P, P, SZ, P]
+        lib.mfd_tree_attention.restype = I
         _libs[p] = lib
         if path is None:
             _lib = lib
@@ -347,6 +376,181 @@ def mfd_verify_withheld_test(target_logits, n_req, B, V, L, parent, token, n_nod
                                          _p(out_tokens), _p(status), _p(ws), ws.numel() * ws.element_size(),
                                          int(wait_limit_ns), _s(stream))
     _check(rc, "mfd_verify_withheld_test")
+
+
+# ---------------------------------------------------------------------------
+class KVCache:
+    """A paged key-value cache of one layer (mfd_kv_cache): k and v
+    [n_pages, Hk, page_size, D] views of bf16, fp16 or float8_e4m3fn storage
+    (E4M3 with k_exp, v_exp uint8 [n_pages, Hk, page_size]), and block_table
+    int32 [n_req, max_pages].  All are plain tensors the caller may fill; the
+    pages start uninitialised and the block table at zero."""
+
+    def __init__(self, n_pages: int, page_size: int, Hk: int, D: int, n_req: int, max_pages: int,
+                 dtype=torch.bfloat16, layout: str = "head", device="cuda"):
+        """layout: "head" keeps a head's slots of a page together ([n_pages,
+        Hk, page_size, D]), "token" a slot's heads ([n_pages, page_size, Hk,
+        D])."""
+        assert layout in ("head", "token")
+        kv = []
+        for _ in range(2):
+            if layout == "head":
+                kv.append(torch.empty((n_pages, Hk, page_size, D), dtype=dtype, device=device))
+            else:
+                kv.append(torch.empty((n_pages, page_size, Hk, D), dtype=dtype, device=device).transpose(1, 2))
+        exps = [torch.zeros((n_pages, Hk, page_size), dtype=torch.uint8, device=device)
+                if dtype == torch.float8_e4m3fn else None for _ in range(2)]
+        table = torch.zeros((n_req, max_pages), dtype=torch.int32, device=device)
+        self._set(kv[0], kv[1], table, exps[0], exps[1])
+
+    @classmethod
+    def from_tensors(cls, k, v, block_table, k_exp=None, v_exp=None) -> "KVCache":
+        """A cache over tensors the caller holds: k and v [n_pages, Hk,
+        page_size, D] with equal strides and contiguous D."""
+        self = cls.__new__(cls)
+        self._set(k, v, block_table, k_exp, v_exp)
+        return self
+
+    def _set(self, k, v, table, k_exp, v_exp):
+        assert k.shape == v.shape and k.dim() == 4 and k.dtype == v.dtype and k.dtype in _DTYPE
+        assert k.stride() == v.stride() and k.stride(3) == 1, "k and v: equal strides, contiguous rows"
+        assert table.dtype == torch.int32 and table.dim() == 2
+        if k.dtype == torch.float8_e4m3fn:
+            for e in (k_exp, v_exp):
+                assert e is not None and e.dtype == torch.uint8 and e.shape == k.shape[:3], "E4M3: row exponents"
+        else:
+            assert k_exp is None and v_exp is None, "row exponents belong to an E4M3 cache"
+        self.k, self.v, self.block_table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
+        self.n_pages, self.Hk, self.page_size, self.D = k.shape
+        self.n_req, self.max_pages = table.shape
+        for t in (k, v):
+            assert t.is_cuda, "device tensors"
+        # a dimension of one element has no stride of its own
+        st = [k.stride(i) if k.shape[i] > 1 else self.D for i in range(3)]
+        self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _p(k_exp), _p(v_exp), _p(table), _DTYPE[k.dtype],
+                                 self.n_pages, self.page_size, self.max_pages, self.Hk, self.D, st[0], st[1], st[2])
+
+
+def rope_phases(theta: float, rot_dim: int, inv_freq=None, device="cuda"):
+    """The phases of mfd_rope_phases on the device (int64 holding the 64-bit
+    words), for inv_freq[i] = theta ** (-2 i / rot_dim) or the given sequence
+    of rot_dim / 2 frequencies."""
+    n = rot_dim // 2
+    f = [float(theta) ** (-2.0 * i / rot_dim) for i in range(n)] if inv_freq is None else [float(x) for x in inv_freq]
+    assert len(f) == n, "one frequency per pair"
+    src, dst = (ctypes.c_double * max(n, 1))(*f), (ctypes.c_int64 * max(n, 1))()
+    if n:
+        _check(load().mfd_rope_phases(ctypes.addressof(src), n, ctypes.addressof(dst)), "mfd_rope_phases")
+    return torch.tensor(list(dst)[:n], dtype=torch.int64, device=device)
+
+
+def _rows(t, heads, D):
+    """(pointer, token stride) of a [..., tokens, heads, D] tensor whose heads
+    are contiguous; all leading dimensions step by the token stride."""
+    assert isinstance(t, torch.Tensor) and t.is_cuda and t.dim() >= 3 and tuple(t.shape[-2:]) == (heads, D), \
+        "device tensor [..., tokens, heads, D]"
+    assert t.stride(-1) == 1 and (heads == 1 or t.stride(-2) == D), "contiguous heads"
+    n, st = t.shape[-3], t.stride(-3)
+    if n == 1:  # one token each: the stride is that of the dimension before, if it has one
+        st = t.stride(-4) if t.dim() > 3 and t.shape[-4] > 1 else heads * D
+    for i in range(t.dim() - 4, -1, -1):
+        assert t.shape[i] == 1 or t.stride(i) == n * st, "tokens at one stride"
+        n *= t.shape[i]
+    return t.data_ptr(), st
+
+
+def mfd_qk_norm_rope(q, k, q_w, k_w, eps, phase, rot_dim, interleaved, pos, q_out, k_out, status,
+                     stream=None) -> None:
+    """Per-head norm (q_w, k_w [D], or None) and rotation of q [.., T, Hq, D]
+    and k [.., T, Hk, D] at positions pos (int32, one per token)."""
+    Hq, D = q.shape[-2:]
+    Hk = k.shape[-2]
+    assert q.dtype == k.dtype == q_out.dtype == k_out.dtype and pos.dtype == torch.int32
+    assert q.shape[:-2] == k.shape[:-2] and q_out.shape == q.shape and k_out.shape == k.shape
+    T = pos.numel()
+    assert q.numel() == T * Hq * D, "one position per token"
+    for w in (q_w, k_w):
+        assert w is None or (w.dtype == q.dtype and w.numel() == D), "norm weights [D] of q's type"
+    assert phase is None or phase.numel() >= rot_dim // 2
+    (qp, qs), (kp, ks) = _rows(q, Hq, D), _rows(k, Hk, D)
+    rc = load().mfd_qk_norm_rope(qp, qs, kp, ks, _DTYPE[q.dtype], T, Hq, Hk, D, _p(q_w), _p(k_w), eps,
+                                 _p(phase) if rot_dim else None, rot_dim, int(interleaved), _p(pos), _p(q_out),
+                                 _p(k_out), _p(status), _s(stream))
+    _check(rc, "mfd_qk_norm_rope")
+
+
+def mfd_kv_append(q, k, v, q_w, k_w, eps, phase, rot_dim, interleaved, pos, ctx_len, n_nodes, q_out, cache, status,
+                  stream=None) -> None:
+    """Norm and rotation of q, k [n_req, N, heads, D], with k and v written
+    into `cache` (KVCache) at positions ctx_len[q] + n.  q and q_out may be
+    None (the cache write alone), and n_nodes (all N rows live)."""
+    n_req, N, Hk, D = k.shape
+    assert v.shape == k.shape and v.dtype == k.dtype and (Hk, D) == (cache.Hk, cache.D)
+    assert n_req == cache.n_req and tuple(pos.shape) == (n_req, N) and pos.dtype == torch.int32
+    assert ctx_len.dtype == torch.int32 and ctx_len.numel() == n_req
+    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == n_req)
+    for w in (q_w, k_w):
+        assert w is None or (w.dtype == k.dtype and w.numel() == D), "norm weights [D] of k's type"
+    assert phase is None or phase.numel() >= rot_dim // 2
+    Hq, qp, qs = 0, None, 0
+    if q is not None:
+        Hq = q.shape[2]
+        assert tuple(q.shape) == (n_req, N, Hq, D) and q.dtype == k.dtype
+        assert q_out.shape == q.shape and q_out.dtype == q.dtype
+        qp, qs = _rows(q, Hq, D)
+    (kp, ks), (vp, vs) = _rows(k, Hk, D), _rows(v, Hk, D)
+    rc = load().mfd_kv_append(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hq, _p(q_w), _p(k_w), eps,
+                              _p(phase) if rot_dim else None, rot_dim, int(interleaved), _p(pos), _p(ctx_len),
+                              _p(n_nodes), _p(q_out) if q is not None else None, ctypes.byref(cache._c), _p(status),
+                              _s(stream))
+    _check(rc, "mfd_kv_append")
+
+
+def mfd_kv_read(cache, start, length, k_out, v_out, status, stream=None) -> None:
+    """Positions start[q] .. start[q] + length[q] - 1 of every request to
+    k_out, v_out [n_req, L_max, Hk, D], zero past length[q]."""
+    n_req, L_max, Hk, D = k_out.shape
+    assert v_out.shape == k_out.shape and v_out.dtype == k_out.dtype and (Hk, D) == (cache.Hk, cache.D)
+    assert n_req == cache.n_req
+    for t in (start, length):
+        assert t.dtype == torch.int32 and t.numel() == n_req
+    rc = load().mfd_kv_read(ctypes.byref(cache._c), n_req, L_max, _p(start), _p(length), _DTYPE[k_out.dtype],
+                            _p(k_out), _p(v_out), _p(status), _s(stream))
+    _check(rc, "mfd_kv_read")
+
+
+def mfd_kv_commit(cache, ctx_len, accept_len, path_nodes, n_nodes, new_len, status, stream=None) -> None:
+    """Moves the accepted path's entries (mfd_verify's accept_len and
+    path_nodes) behind the context; new_len may be ctx_len."""
+    n_req, L1 = path_nodes.shape
+    assert n_req == cache.n_req
+    for t in (ctx_len, accept_len, n_nodes, new_len):
+        assert t.dtype == torch.int32 and t.numel() == n_req
+    assert path_nodes.dtype == torch.int32
+    rc = load().mfd_kv_commit(ctypes.byref(cache._c), n_req, L1 - 1, _p(ctx_len), _p(accept_len), _p(path_nodes),
+                              _p(n_nodes), _p(new_len), _p(status), _s(stream))
+    _check(rc, "mfd_kv_commit")
+
+
+def mfd_tree_attention_workspace_bytes(n_req: int, N: int, Hq: int, Hk: int, D: int) -> int:
+    return int(load().mfd_tree_attention_workspace_bytes(n_req, N, Hq, Hk, D))
+
+
+def mfd_tree_attention(q, cache, ctx_len, n_nodes, mask, scale, out, lse, status, ws, stream=None) -> None:
+    """Attention of q [n_req, N, Hq, D] over `cache` under the tree mask
+    (int32 words [n_req, N, ceil(N / 32)]; None: causal) into out (q's shape)
+    and lse (fp32 [n_req, N, Hq], or None)."""
+    n_req, N, Hq, D = q.shape
+    assert n_req == cache.n_req and D == cache.D and out.shape == q.shape and out.dtype == q.dtype
+    assert ctx_len.dtype == torch.int32 and ctx_len.numel() == n_req
+    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == n_req)
+    assert mask is None or (mask.dtype == torch.int32 and tuple(mask.shape) == (n_req, N, (N + 31) // 32))
+    assert lse is None or (lse.dtype == torch.float32 and lse.numel() == n_req * N * Hq)
+    qp, qs = _rows(q, Hq, D)
+    rc = load().mfd_tree_attention(qp, qs, _DTYPE[q.dtype], n_req, N, Hq, ctypes.byref(cache._c), _p(ctx_len),
+                                   _p(n_nodes), _p(mask), scale, _p(out), _p(lse), _p(status), _p(ws),
+                                   ws.numel() * ws.element_size(), _s(stream))
+    _check(rc, "mfd_tree_attention")
 
 
 # ---------------------------------------------------------------------------
