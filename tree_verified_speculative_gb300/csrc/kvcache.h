@@ -57,6 +57,9 @@ struct KvCommitLaunch {
 cudaError_t launch_kv_commit(const KvCommitLaunch &A, cudaStream_t stream);
 
 // attention.cu
+constexpr int ATTENTION_MAX_CTAS = 152;  // GB300's SMs: scratch is sized without asking the device
+size_t attention_part_bytes(int M, int D);
+int attention_box_rows(int page_size, int D);  // positions of a tensor map's box
 struct AttentionLaunch {
   const void *q;
   int64_t q_stride;
@@ -68,6 +71,9 @@ struct AttentionLaunch {
   void *out;
   float *lse;
   int32_t *status;
+  const CUtensorMap *map_k, *map_v;
+  int n_sm;
+  void *ws;
 };
 cudaError_t launch_tree_attention(const AttentionLaunch &A, cudaStream_t stream);
 

@@ -716,6 +716,44 @@ int cache_view(const mfd_kv_cache *c, mfd::CacheView *out) {
   return MFD_OK;
 }
 
+using KvMapKey = std::tuple<int, const void *, int, int, int, int, int, int64_t, int64_t, int64_t, int>;
+std::map<KvMapKey, CUtensorMap> g_kv_maps;
+
+// Keys or values as a 4-D tensor (D, slot, head, page).  A 16-bit cache's box
+// is 64 columns x `rows` slots of one head and page with the 128-byte swizzle
+// (columns past D read as zero); an E4M3 one's is D columns x `rows` slots as
+// they are.
+int kv_map(const void *ptr, const mfd::CacheView &c, int rows, CUtensorMap *out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MFD_ERR_CUDA;
+  const bool e4m3 = c.dtype == MFD_E4M3;
+  const int esz = e4m3 ? 1 : 2;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const KvMapKey key{dev, ptr, c.dtype, c.D, 1 << c.ps_shift, c.Hk, c.n_pages, c.token_stride, c.head_stride, c.page_stride, rows};
+  auto it = g_kv_maps.find(key);
+  if (it == g_kv_maps.end()) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return MFD_ERR_CUDA;
+    CUtensorMap m;
+    std::memset(&m, 0, sizeof m);
+    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)1 << c.ps_shift, (cuuint64_t)c.Hk, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)(c.token_stride * esz), (cuuint64_t)(c.head_stride * esz),
+                                   (cuuint64_t)(c.page_stride * esz)};
+    const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? c.D : 64), (cuuint32_t)rows, 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(&m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : c.dtype == MFD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return MFD_ERR_CUDA;
+    if (g_kv_maps.size() > 4096) g_kv_maps.clear();
+    it = g_kv_maps.emplace(key, m).first;
+  }
+  *out = it->second;
+  return MFD_OK;
+}
+
 int need_sm103() {
   DeviceInfo d;
   const int rc = current_device_info(&d);
@@ -885,7 +923,7 @@ size_t mfd_tree_attention_workspace_bytes(int n_req, int N, int Hq, int Hk, int 
   if (n_req < 1 || n_req > 1024 || N < 1 || N > 4096 || Hq < 1 || Hk < 1 || Hq > 1024 || Hq % Hk != 0 ||
       (int64_t)N * (Hq / Hk) > 65536 || D < 16 || D > 256 || D % 16 != 0)
     return 0;
-  return 256;
+  return align256(mfd::attention_part_bytes(N * (Hq / Hk), D));
 }
 
 int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, int N, int Hq,
@@ -903,8 +941,17 @@ int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, in
   const size_t need = mfd_tree_attention_workspace_bytes(n_req, N, Hq, cv.Hk, cv.D);
   if (need == 0) return MFD_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MFD_ERR_WORKSPACE;
-  if ((rc = need_sm103()) != MFD_OK) return rc;
+  DeviceInfo d;
+  if ((rc = current_device_info(&d)) != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
+  CUtensorMap mk, mv;
+  const int rows = mfd::attention_box_rows(1 << cv.ps_shift, cv.D);
+  if ((rc = kv_map(cv.k, cv, rows, &mk)) != MFD_OK || (rc = kv_map(cv.v, cv, rows, &mv)) != MFD_OK) return rc;
   mfd::AttentionLaunch A;
+  A.map_k = &mk;
+  A.map_v = &mv;
+  A.n_sm = d.n_sm;
+  A.ws = ws;
   A.q = q;
   A.q_stride = q_stride;
   A.dtype = dtype;
