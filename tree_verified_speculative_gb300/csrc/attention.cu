@@ -39,14 +39,18 @@
 // past the end and values that are not finite, which a product would spread
 // to rows that do not see them (0 * NaN); a cleared value's node is noted and
 // added back for the rows that do see it.
+#include <atomic>
+
 #include "kvcache.h"
 #include "mfd_device.cuh"
 
 namespace mfd {
 namespace {
 
-constexpr int BM = 128;
+constexpr int BM = 128;  // rows of a tile
+constexpr int BN = 128;  // key positions of a tile
 constexpr int MAX_N = 4096;
+constexpr int SEG_RING = 4;  // entries of a CTA's list of work in flight
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
@@ -72,20 +76,28 @@ template <int DP_, bool E4M3_>
 struct Shape {
   static constexpr int DP = DP_;                       // head width, padded to 64, 128 or 256
   static constexpr int NS = DP == 256 ? 1 : 2;         // streams
-  static constexpr int BN = DP == 256 ? 64 : 128;      // key positions of a tile
-  static constexpr int NB = DP / 64;                   // 64-column blocks of 128-byte rows
+  static constexpr int UC = DP == 64 ? 64 : 128;       // columns of a unit, what one stage holds of a tile
+  static constexpr int NU = DP / UC;                   // units of a tile
+  static constexpr int NB = UC / 64;                   // 64-column blocks of 128-byte rows
   static constexpr int Q_TILE = BM * DP * 2;
-  static constexpr int STAGE = BN * DP * 2;
-  static constexpr int RAW = BN * DP;                  // an E4M3 tile as it is in the cache
+  static constexpr int STAGE = BN * UC * 2;
+  static constexpr int RAW = BN * UC;                  // an E4M3 unit as it is in the cache
   static constexpr int ST = E4M3_ ? (DP == 64 ? 4 : 3) : (DP == 64 ? 8 : 5);
   static constexpr int RST = E4M3_ ? (DP == 64 ? 6 : 4) : 0;
   static constexpr int THREADS = 128 * (2 + NS);
   static constexpr int HELP_WARP = 4 + 4 * NS;
-  static constexpr int TM_S = 0;                       // S accumulators; P over them
-  static constexpr int TM_O = 256;
-  static constexpr int CODES = E4M3_ ? 2 * 8 * 128 : 0;
-  static constexpr int BARS = 2 * ST + ST + 2 * (RST ? RST : 1) + 2 + 2 + 2 + 1 + 1;
-  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + CODES + MAX_N / 8 + BARS * 8 + 64;
+  // Registers a thread: at launch, and after the warpgroups have shared them
+  // out anew; the shares together are what the launch has (64K, 63K).
+  static constexpr int REGS = NS == 2 ? 128 : 168;
+  static constexpr int REGS_LOAD = NS == 2 ? 48 : 104;
+  static constexpr int REGS_HELP = NS == 2 ? 80 : 168;
+  static constexpr int REGS_SOFTMAX = NS == 2 ? 192 : 232;
+  static_assert(REGS_LOAD + REGS_HELP + NS * REGS_SOFTMAX == (2 + NS) * REGS, "a larger sum would wait forever");
+  static constexpr int TM_S = 0;                       // two S accumulators; P over them
+  static constexpr int TM_O = 2 * BN;
+  static constexpr int POWERS = E4M3_ ? 2 * 4 * BN * 2 : 0;  // [k, v][tile mod 4][position], 16 bits
+  static constexpr int BARS = 3 * ST + 2 * (RST ? RST : 1) + 8 + 2 * SEG_RING;
+  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + POWERS + MAX_N / 8 + BARS * 8 + SEG_RING * 40 + 32;
 };
 
 // ------------------------------------------------------------------ line of work
@@ -106,7 +118,7 @@ struct Item {
   int cost;    // places on the line: a step per row tile and key tile, and one for its start and end
 };
 
-template <int NS, int BN>
+template <int NS>
 __device__ __forceinline__ Item item_of(const Params &p, int ctx, int nn, int pair) {
   Item it;
   const int live = nn * p.G, first = pair * NS * BM;
@@ -121,85 +133,28 @@ __device__ __forceinline__ Item item_of(const Params &p, int ctx, int nn, int pa
   return it;
 }
 
-template <int NS, int BN>
+template <int NS>
 __device__ __forceinline__ int64_t head_cost(const Params &p, int ctx, int nn) {
   if (p.mask) {
     const int live = nn * p.G;
     return (int64_t)((live + BM - 1) / BM) * (nn ? (ctx + nn + BN - 1) / BN : 0) + p.n_pair;
   }
   int64_t c = 0;
-  for (int i = 0; i < p.n_pair; ++i) c += item_of<NS, BN>(p, ctx, nn, i).cost;
+  for (int i = 0; i < p.n_pair; ++i) c += item_of<NS>(p, ctx, nn, i).cost;
   return c;
 }
 
+// Where the line's place x falls: CTA c of n has [C c / n, C (c + 1) / n).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // non-negative; mostly 32 bits
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t border(int64_t total, int c, int n) { return divide(total * c, n); }
+__device__ __forceinline__ int cta_of(int64_t total, int64_t x, int n) { return (int)divide((x + 1) * n - 1, total); }
+
 // First key tile at or after place z of an item.
 __device__ __forceinline__ int tile_at(const Item &it, int z) {
-  return z >= it.cost ? it.tiles : (int)((int64_t)z * it.tiles / it.cost);
+  return z >= it.cost ? it.tiles : (int)divide((int64_t)z * it.tiles, it.cost);
 }
-
-// A CTA's stretch of one item.
-struct Segment {
-  int q, h, pair;
-  int ctx, nn;
-  Item it;
-  int t0, t1;  // key tiles
-  bool head;   // starts at the item's start
-};
-
-// Walks a CTA's stretch [x, x1) of the line.  Every role walks it by itself.
-template <int NS, int BN>
-struct Walk {
-  int64_t x, x1;
-  int q, h, pair, z;
-  int ctx, nn;
-
-  __device__ __forceinline__ void start(const Params &p, int64_t x_, int64_t x1_, int q0, int64_t into) {
-    x = x_;
-    x1 = x1_;
-    q = q0;
-    h = pair = z = 0;
-    if (x >= x1) return;
-    lengths(p, q, ctx, nn);
-    const int64_t hc = head_cost<NS, BN>(p, ctx, nn);
-    h = (int)(into / hc);
-    int64_t rest = into - h * hc;
-    for (;;) {
-      const int c = item_of<NS, BN>(p, ctx, nn, pair).cost;
-      if (rest < c) break;
-      rest -= c;
-      ++pair;
-    }
-    z = (int)rest;
-  }
-  __device__ __forceinline__ bool next(const Params &p, Segment &s) {
-    if (x >= x1) return false;
-    s.q = q;
-    s.h = h;
-    s.pair = pair;
-    s.ctx = ctx;
-    s.nn = nn;
-    s.it = item_of<NS, BN>(p, ctx, nn, pair);
-    const int64_t left = x1 - x;
-    const int end = left < s.it.cost - z ? z + (int)left : s.it.cost;
-    s.t0 = tile_at(s.it, z);
-    s.t1 = tile_at(s.it, end);
-    s.head = z == 0;
-    x += end - z;
-    z = 0;
-    if (end == s.it.cost && ++pair == p.n_pair) {
-      pair = 0;
-      if (++h == p.cv.Hk) {
-        h = 0;
-        if (++q < p.n_req) lengths(p, q, ctx, nn);
-      }
-    }
-    return true;
-  }
-};
-
-// Where the line's place x falls: CTA c of n has [C c / n, C (c + 1) / n).
-__device__ __forceinline__ int64_t border(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int cta_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
 
 // ------------------------------------------------------------------ primitives
 
@@ -211,6 +166,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
+// 16 bytes global -> shared without a register; cp_async_wait waits for all of the thread's.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
@@ -225,14 +185,47 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands, fp32 accumulate.
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// One lane of the warp; the branch it guards runs in uniform registers, which
+// is where the MMA takes its operands from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// Operand descriptors of 128-byte swizzled rows in shared memory (8-row groups
+// 1024 bytes apart: stride byte offset; version 1; swizzle mode 128 bytes).
+// Low word: address >> 4, and at bit 16 the leading byte offset >> 4: unused
+// (1) where the contraction runs along the rows (queries, keys), the distance
+// of 64-column blocks where it runs down them (values).
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) { return (saddr >> 4) | ((lead >> 4) << 16); }
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulate.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
       : "memory");
 }
 
@@ -283,20 +276,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Operand descriptor of a [tokens][64 columns] block array as an operand whose
-// contiguous dimension is not the contraction (the values: contraction over
-// tokens).  128-byte swizzle; 64-column blocks `block_bytes` apart (leading
-// byte offset), 8-token groups 1024 bytes apart (stride byte offset).
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(block_bytes >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 // Instruction descriptor, kind::f16, fp32 accumulator: operand type code at
 // bits 7 and 10 (0 fp16, 1 bf16), bit 16 set when B's contraction is not its
 // contiguous dimension, N >> 3 at bit 17, M >> 4 at bit 24.
@@ -318,6 +297,28 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Bits of two 16-bit elements whose exponent is all ones (NaN, infinity).
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w);
@@ -330,46 +331,65 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
   return ((w & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
 }
 
-// Four E4M3 bytes to four 16-bit values times 2^e (code = e + 127, not NaN).
+// E4M3 to the operand type.  power(code): a 16-bit number that scales a row's
+// values as widen4 takes them, NaN for a row that reads back as NaN; `wide`
+// says that 2^e has no such number and widen4_wide is to be used.
 template <typename T>
 struct Widen;
 // bf16: the byte's exponent and mantissa bits moved to bf16's places read as
 // the value times 2^-120 (biases 7 and 127), subnormals included; one exact
-// multiplication puts both powers right, or two where 2^(e + 120) has no bf16.
+// multiplication by 2^(e + 120) puts both right.
 template <>
 struct Widen<__nv_bfloat16> {
-  __nv_bfloat162 f1, f2;
-  bool two;
-  __device__ __forceinline__ explicit Widen(int code) {
-    two = code > 134;
-    const uint32_t a = two ? 247u << 7 : (uint32_t)(code + 120) << 7, b = (uint32_t)code << 7;
-    const uint32_t aa = a | (a << 16), bb = b | (b << 16);
-    f1 = *reinterpret_cast<const __nv_bfloat162 *>(&aa);
-    f2 = *reinterpret_cast<const __nv_bfloat162 *>(&bb);
+  static constexpr uint16_t NONE = 0x7FFF;
+  static __device__ __forceinline__ uint16_t power(int code, bool &wide) {
+    if (code == EXP_NAN) return NONE;
+    wide |= code > 134;
+    return (uint16_t)((code > 134 ? 254 : code + 120) << 7);
   }
-  __device__ __forceinline__ uint2 operator()(uint32_t x) const {
-    uint2 o;
-    uint32_t y = __byte_perm(x, 0, 0x1404);
-    y = (y & 0x80008000u) | ((y & 0x7F007F00u) >> 4);
-    __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f1);
-    uint32_t w = __byte_perm(x, 0, 0x3424);
-    w = (w & 0x80008000u) | ((w & 0x7F007F00u) >> 4);
-    __nv_bfloat162 u = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w), f1);
-    if (two) {
-      v = __hmul2(v, f2);
-      u = __hmul2(u, f2);
-    }
-    o.x = *reinterpret_cast<const uint32_t *>(&v);
-    o.y = *reinterpret_cast<const uint32_t *>(&u);
-    return o;
+  static __device__ __forceinline__ __nv_bfloat162 moved(uint32_t x, uint32_t pick) {
+    const uint32_t y = __byte_perm(x, 0, pick);
+    const uint32_t z = (y & 0x80008000u) | ((y >> 4) & 0x07F007F0u);
+    return *reinterpret_cast<const __nv_bfloat162 *>(&z);
+  }
+  static __device__ __forceinline__ uint2 widen4(uint32_t x, uint32_t power2) {
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&power2);
+    const __nv_bfloat162 a = __hmul2(moved(x, 0x1404), f), b = __hmul2(moved(x, 0x3424), f);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+  }
+  // power2 = 2^127 here; the rest, 2^(e - 7), in a second multiplication
+  static __device__ __forceinline__ uint2 widen4_wide(uint32_t x, int code) {
+    const uint32_t w = (uint32_t)(code > 134 ? 254 : code + 120) << 7, r = (uint32_t)(code > 134 ? code - 7 : 127) << 7;
+    uint2 o = widen4(x, w | (w << 16));
+    const uint32_t rr = r | (r << 16);
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&rr);
+    const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o.x), f),
+                         b = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o.y), f);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
   }
 };
-// fp16: E4M3 converts exactly; the power is applied in fp32.
+// fp16: E4M3 converts exactly; the power has a number from 2^-24 to 2^15.
 template <>
 struct Widen<__half> {
-  float s;
-  __device__ __forceinline__ explicit Widen(int code) { s = e4m3_scale(code); }
-  __device__ __forceinline__ uint2 operator()(uint32_t x) const {
+  static constexpr uint16_t NONE = 0x7FFF;
+  static __device__ __forceinline__ uint16_t power(int code, bool &wide) {
+    if (code == EXP_NAN) return NONE;
+    wide |= code < 103 || code > 142;
+    return code < 103 ? 1 : code < 113 ? (uint16_t)(1u << (code - 103)) : code > 142 ? 0x7800 : (uint16_t)((code - 112) << 10);
+  }
+  static __device__ __forceinline__ uint32_t two(uint32_t bytes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)bytes, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  }
+  static __device__ __forceinline__ uint2 widen4(uint32_t x, uint32_t power2) {
+    const __half2 f = *reinterpret_cast<const __half2 *>(&power2);
+    const uint32_t lo = two(x & 0xFFFFu), hi = two(x >> 16);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f),
+                  b = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+  }
+  static __device__ __forceinline__ uint2 widen4_wide(uint32_t x, int code) {
+    const float s = e4m3_scale(code);
     const float2 a = e4m3x2_float(x & 0xFFFFu), b = e4m3x2_float(x >> 16);
     return make_uint2(pack2<__half>(a.x * s, a.y * s), pack2<__half>(b.x * s, b.y * s));
   }
@@ -393,36 +413,262 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t *row, int W32, int 
 
 // ------------------------------------------------------------------ kernel
 
+// One entry of a CTA's list of work; q < 0 ends it.
+struct Segment {
+  int q, h, pair;
+  int ctx, nn;
+  int active, tiles;  // of the item
+  int t0, t1;         // its key tiles in this stretch
+  int head;           // the stretch has the item's start
+};
+// How long a role waits for its next entry: longer than the list's own waits,
+// so that either every role gets an entry or none does.
+constexpr unsigned long long SEG_LIMIT_NS = 4 * kWaitLimitNs;
+
+__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0 && globaltimer() - t0 > limit_ns) return false;
+  }
+}
+
+// The CTA's stretch of the line, entry by entry, by one warp: the requests'
+// costs are summed by its lanes, the entries written by its first.
+template <int NS>
+struct Scheduler {
+  int64_t x, x1, into;
+  int q0;
+
+  __device__ __forceinline__ void start(const Params &p, int lane) {
+    int64_t total = 0;
+    for (int b = 0; b < p.n_req; b += 32) {
+      int ctx, nn;
+      int64_t c = 0;
+      if (b + lane < p.n_req) {
+        if (!lengths(p, b + lane, ctx, nn) && blockIdx.x == 0) report(p.status, MFD_ERR_INPUT);
+        c = p.cv.Hk * head_cost<NS>(p, ctx, nn);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      total += c;
+    }
+    x = border(total, blockIdx.x, gridDim.x);
+    x1 = border(total, blockIdx.x + 1, gridDim.x);
+    q0 = 0;
+    into = 0;
+    int64_t before = 0;
+    if (x < x1)
+      for (int b = 0; b < p.n_req; b += 32) {
+        int ctx, nn;
+        int64_t own = 0;
+        if (b + lane < p.n_req) {
+          lengths(p, b + lane, ctx, nn);
+          own = p.cv.Hk * head_cost<NS>(p, ctx, nn);
+        }
+        int64_t run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += up;
+        }
+        const int64_t lo = before + run - own;
+        const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && lo <= x && x < lo + own);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          q0 = b + l;
+          into = x - __shfl_sync(0xffffffffu, lo, l);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, run, 31);
+      }
+  }
+  // by one lane
+  __device__ __forceinline__ void emit(const Params &p, Segment *ring, uint64_t *seg_full, uint64_t *seg_empty) {
+    uint32_t n = 0;
+    int q = q0, h = 0, pair = 0, z = 0, ctx = 0, nn = 0;
+    if (x < x1) {
+      lengths(p, q, ctx, nn);
+      const int64_t hc = head_cost<NS>(p, ctx, nn);
+      h = (int)divide(into, hc);
+      int64_t rest = into - h * hc;
+      for (;;) {
+        const int c = item_of<NS>(p, ctx, nn, pair).cost;
+        if (rest < c) break;
+        rest -= c;
+        ++pair;
+      }
+      z = (int)rest;
+    }
+    for (bool more = true; more; ++n) {
+      const int st = n % SEG_RING;
+      if (!wait_limit(&seg_empty[st], ((n / SEG_RING) & 1u) ^ 1u, 2 * kWaitLimitNs)) {
+        report(p.status, MFD_ERR_TIMEOUT);
+        return;
+      }
+      Segment s;
+      s.q = -1;
+      more = x < x1;
+      if (more) {
+        const Item it = item_of<NS>(p, ctx, nn, pair);
+        const int64_t left = x1 - x;
+        const int end = left < it.cost - z ? z + (int)left : it.cost;
+        s.q = q;
+        s.h = h;
+        s.pair = pair;
+        s.ctx = ctx;
+        s.nn = nn;
+        s.active = it.active;
+        s.tiles = it.tiles;
+        s.t0 = tile_at(it, z);
+        s.t1 = tile_at(it, end);
+        s.head = z == 0;
+        x += end - z;
+        z = 0;
+        if (end == it.cost && ++pair == p.n_pair) {
+          pair = 0;
+          if (++h == p.cv.Hk) {
+            h = 0;
+            if (++q < p.n_req) lengths(p, q, ctx, nn);
+          }
+        }
+      }
+      ring[st] = s;
+      mbar_arrive(&seg_full[st]);
+    }
+  }
+};
+
+// Adds back what the helpers took out of the values' product: for every noted
+// node from lo to hi - 1 that this row sees, the values that are not finite
+// (all NaN where an E4M3 row reads back as NaN), columns d .. d + 15.
+template <typename T, bool E4M3>
+__device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, int lo, int hi, int node,
+                                      const uint32_t *mask_row, const uint32_t *bad, int d, float (&f)[16]) {
+  const CacheView &cv = p.cv;
+  for (int j = lo; j < hi; ++j) {
+    if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
+    const bool sees = mask_row ? (__ldg(mask_row + (j >> 5)) >> (j & 31)) & 1u : j <= node;
+    if (!sees) continue;
+    const int pos = ctx + j;
+    const int page = __ldg(cv.table + (size_t)q * cv.max_pages + (pos >> cv.ps_shift));
+    if (page < 0 || page >= cv.n_pages) continue;
+    const int64_t e = page * cv.page_stride + h * cv.head_stride +
+                      (int64_t)(pos & ((1 << cv.ps_shift) - 1)) * cv.token_stride;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (E4M3) {
+        f[k] = __int_as_float(0x7FFFFFFF);
+      } else {
+        const uint32_t w = static_cast<const uint16_t *>(cv.v)[e + d + k];
+        if (nonfinite2<T>(w)) f[k] += unpack2<T>(w).x;
+      }
+    }
+  }
+}
+
+// One E4M3 unit (128 positions x UC columns, columns from c0 of the head) to
+// the swizzled operand, by 128 threads: a thread's chunks of 16 columns are at
+// one column, 128 / (UC / 16) positions apart.  All chunks are loaded before
+// the first is converted.
+template <typename T, int DP>
+__device__ __forceinline__ void widen_unit(const Params &p, const uint8_t *src, uint8_t *dst, const uint16_t *power,
+                                           int ht, int c0) {
+  constexpr int UC = DP == 64 ? 64 : 128;
+  constexpr int C = UC / 16, PER = 128 / C, K = BN / PER;  // 8 or 4 chunks a thread
+  const int wide = min(p.cv.D, UC);
+  const int ch = ht % C, tok0 = ht / C;
+  const bool have = c0 + ch * 16 < p.cv.D;
+  const int c2 = (ch & 3) * 2;
+  // lanes of neighbouring blocks write their two chunks in opposite order (other banks)
+  const int sw = (ch >> 2) & 1;
+  uint4 x[K];
+  uint32_t pw[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    pw[k] = power[tok0 + k * PER];
+    x[k] = *reinterpret_cast<const uint4 *>(src + (tok0 + k * PER) * wide + (have ? ch * 16 : 0));
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int tok = tok0 + k * PER;
+    // power 0: no row, whatever the bytes are
+    const uint32_t keep = have && pw[k] ? 0xFFFFFFFFu : 0u, pp = pw[k] * 0x10001u;
+    const uint2 a = Widen<T>::widen4(x[k].x & keep, pp), b = Widen<T>::widen4(x[k].y & keep, pp),
+                c = Widen<T>::widen4(x[k].z & keep, pp), d = Widen<T>::widen4(x[k].w & keep, pp);
+    uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok * 128;
+    const int x7 = tok & 7;
+    *reinterpret_cast<uint4 *>(row + (((c2 + sw) ^ x7) << 4)) =
+        make_uint4(sw ? c.x : a.x, sw ? c.y : a.y, sw ? d.x : b.x, sw ? d.y : b.y);
+    *reinterpret_cast<uint4 *>(row + (((c2 + 1 - sw) ^ x7) << 4)) =
+        make_uint4(sw ? a.x : c.x, sw ? a.y : c.y, sw ? b.x : d.x, sw ? b.y : d.y);
+  }
+}
+
+// The same thread's chunks again, for a unit in which some row's power of two
+// has no number of the operand type: those rows, with the power applied exactly.
+template <typename T, int DP>
+__device__ __noinline__ void widen_unit_wide(const Params &p, int q, int h, int len, const uint8_t *src, uint8_t *dst,
+                                             int base, bool is_v, int ht, int c0) {
+  constexpr int UC = DP == 64 ? 64 : 128;
+  constexpr int C = UC / 16, PER = 128 / C, K = BN / PER;
+  const CacheView &cv = p.cv;
+  const int wide = min(cv.D, UC);
+  const int ch = ht % C;
+  if (c0 + ch * 16 >= cv.D) return;
+  for (int k = 0; k < K; ++k) {
+    const int tok = ht / C + k * PER, t = base + tok;
+    if (t >= len) break;
+    const int page = __ldg(cv.table + (size_t)q * cv.max_pages + (t >> cv.ps_shift));
+    if (page < 0 || page >= cv.n_pages) continue;
+    const int code = (is_v ? cv.v_exp : cv.k_exp)[(((int64_t)page * cv.Hk + h) << cv.ps_shift) +
+                                                  (t & ((1 << cv.ps_shift) - 1))];
+    bool odd = false;
+    Widen<T>::power(code, odd);
+    if (!odd) continue;
+    const uint4 x = *reinterpret_cast<const uint4 *>(src + tok * wide + ch * 16);
+    const uint2 a = Widen<T>::widen4_wide(x.x, code), b = Widen<T>::widen4_wide(x.y, code),
+                c = Widen<T>::widen4_wide(x.z, code), d = Widen<T>::widen4_wide(x.w, code);
+    uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok * 128;
+    const int c2 = (ch & 3) * 2, x7 = tok & 7;
+    *reinterpret_cast<uint4 *>(row + ((c2 ^ x7) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4 *>(row + (((c2 + 1) ^ x7) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+  }
+}
+
 template <typename T, int DP, bool E4M3>
 __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const Params p) {
   using SH = Shape<DP, E4M3>;
-  constexpr int NS = SH::NS, BN = SH::BN, NB = SH::NB, ST = SH::ST, RST = SH::RST;
+  constexpr int NS = SH::NS, NU = SH::NU, NB = SH::NB, ST = SH::ST, RST = SH::RST;
   constexpr uint32_t RN = RST ? RST : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;
   uint8_t *sT = sQ + NS * SH::Q_TILE;
   uint8_t *sR = sT + ST * SH::STAGE;
-  uint8_t *sC = sR + RST * SH::RAW;  // exponent bytes [k, v][8 tiles][128]
-  uint32_t *bad = reinterpret_cast<uint32_t *>(sC + SH::CODES);
+  uint16_t *sC = reinterpret_cast<uint16_t *>(sR + RST * SH::RAW);  // E4M3 rows' powers
+  uint32_t *bad = reinterpret_cast<uint32_t *>(sC + SH::POWERS / 2);  // nodes with values taken out
   uint64_t *full = reinterpret_cast<uint64_t *>(bad + MAX_N / 32);
   uint64_t *empty = full + ST;
-  uint64_t *special = empty + ST;  // a tile the helpers go over before it is full
+  uint64_t *special = empty + ST;  // a unit the helpers go over before it is full
   uint64_t *raw_full = special + ST;
-  uint64_t *raw_empty = raw_full + (RST ? RST : 1);
-  uint64_t *s_full = raw_empty + (RST ? RST : 1);
+  uint64_t *raw_empty = raw_full + RN;
+  uint64_t *s_full = raw_empty + RN;
   uint64_t *p_full = s_full + 2;
   uint64_t *pv_done = p_full + 2;
   uint64_t *q_full = pv_done + 2;
   uint64_t *drain = q_full + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *seg_full = drain + 1;
+  uint64_t *seg_empty = seg_full + SEG_RING;
+  Segment *seg_ring = reinterpret_cast<Segment *>(seg_empty + SEG_RING);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(seg_ring + SEG_RING);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *never = abort_flag + 1;
-  volatile int *seg_done = never + 1;  // segments a softmax warpgroup has left [NS]
-  int *start_q = const_cast<int *>(seg_done) + 2;
-  volatile int *any_bad = start_q + 1;
-  int64_t *start_x = reinterpret_cast<int64_t *>(start_q + 2 + 1);  // [x, x1, into the request]
+  volatile int *seg_done = never + 1;  // segments a softmax warpgroup has left [2]
+  volatile int *any_bad = seg_done + 2;
+  uint32_t *wide_s = reinterpret_cast<uint32_t *>(const_cast<int *>(any_bad) + 1);  // E4M3: tiles with a power that has no number
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CacheView &cv = p.cv;
@@ -431,7 +677,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     if (tid == 0) report(p.status, MFD_ERR_CUDA);
     return;
   }
-  if (tid == 0) {
+  pdl_launch_dependents();
+  Scheduler<NS> sched;
+  if (warp == 0 && lane == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], E4M3 ? 4 : 1);
       mbar_init(&empty[i], 1);
@@ -446,12 +694,17 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < SEG_RING; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 6 + 4 * NS);
+    }
     mbar_init(q_full, 4 * NS);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *never = 0;
     seg_done[0] = seg_done[1] = 0;
     *any_bad = 0;
+    *wide_s = 0;
     fence_mbar_init();
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -460,54 +713,17 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // Where this CTA's stretch starts: the requests' costs, summed by warp 0
-  // (in the space of the first tile, before any load is issued).
-  int64_t *cost_s = reinterpret_cast<int64_t *>(sT);
-  for (int q = tid; q < p.n_req; q += SH::THREADS) {
-    int ctx, nn;
-    if (!lengths(p, q, ctx, nn) && blockIdx.x == 0) report(p.status, MFD_ERR_INPUT);
-    cost_s[q] = cv.Hk * head_cost<NS, BN>(p, ctx, nn);
-  }
-  block_sync();
-  if (warp == 0) {
-    int64_t total = 0;
-    for (int q = lane; q < p.n_req; q += 32) total += cost_s[q];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t x = border(total, blockIdx.x, gridDim.x), x1 = border(total, blockIdx.x + 1, gridDim.x);
-    if (lane == 0) {
-      start_x[0] = x;
-      start_x[1] = x1;
-    }
-    int64_t before = 0;
-    for (int q0 = 0; q0 < p.n_req; q0 += 32) {
-      const int64_t own = q0 + lane < p.n_req ? cost_s[q0 + lane] : 0;
-      int64_t run = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
-      }
-      const int64_t lo = before + run - own;
-      if (own > 0 && lo <= x && x < lo + own) {
-        *start_q = q0 + lane;
-        start_x[2] = x - lo;
-      }
-      before += __shfl_sync(0xffffffffu, run, 31);
-    }
-  }
-  fence_async_smem();  // the costs are read; TMA writes there next
+  if (warp == 2) sched.start(p, lane);
   tc_fence_before();
   block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Walk<NS, BN> walk;
-  walk.start(p, start_x[0], start_x[1], start_x[0] < start_x[1] ? *start_q : 0, start_x[2]);
   Segment s;
+  uint32_t seg_n = 0;
   bool ok = true;
-  // A wait that ran out, or was told to stop, ends the CTA: every role goes
-  // on through its loops without waiting or touching anything.
+  // A wait that ran out, or was told to stop, ends the CTA's work: every role
+  // goes on through its list without waiting or touching anything.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!ok) return;
     if (!mbar_wait(bar, parity, abort_flag)) {
@@ -515,6 +731,27 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       *abort_flag = 1;
       ok = false;
     }
+  };
+  // The next entry; `arrive`: the thread that says it has been read.
+  auto next_segment = [&](bool arrive) {
+    const int st = seg_n % SEG_RING;
+    if (!wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS)) return false;
+    s = seg_ring[st];
+    ++seg_n;
+    if (!arrive) return s.q >= 0;
+    mbar_arrive(&seg_empty[st]);
+    return s.q >= 0;
+  };
+  // The same for a warp.
+  auto next_segment_warp = [&]() {
+    const int st = seg_n % SEG_RING;
+    const bool got = wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS);
+    if (!__all_sync(0xffffffffu, got)) return false;
+    s = seg_ring[st];
+    ++seg_n;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[st]);
+    return s.q >= 0;
   };
   // The order in which a segment's tiles pass the ring: keys and values of
   // tile j as K0 V0 K1 V1 .. when both streams read every tile, K0 K1 V0 K2 V1 ..
@@ -528,7 +765,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   };
 
   if (warp < 4) {
-    if (NS == 2) regs_down<64>();
+    regs_down<SH::REGS_LOAD>();
     if (warp == 0) {
       // ------------------------------------------------------- loads
       // Keys and values of one token serve M rows of this CTA only, or of
@@ -536,11 +773,13 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       const uint64_t policy = p.n_pair > 1 ? policy_evict_normal() : policy_evict_first();
       const int ps = 1 << cv.ps_shift;
       const int rows = ps < BN ? ps : BN;  // of a box
-          uint32_t n = 0, special_par = 0, issued = 0, issued_special = 0, issued_par = 0;
-      while (walk.next(p, s)) {
+      uint32_t st = 0, par = 0;            // ring place and its phase
+      uint32_t special_par = 0, issued = 0, issued_special = 0, issued_par = 0;
+      while (next_segment_warp()) {
         const int nt = s.t1 - s.t0;
-        const bool shared = s.it.active == 2;
+        const bool shared = s.active == 2;
         const int len = s.ctx + s.nn;
+        const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
         for (int i = 0; i < 2 * nt; ++i) {
           const int o = order(nt, shared, i);
           const bool is_v = o < 0;
@@ -549,114 +788,118 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           const int some = (min(len - base, BN) + rows - 1) / rows;
           int page = 0;
           if (lane < some) {
-            page = __ldg(cv.table + (size_t)s.q * cv.max_pages + ((base + lane * rows) >> cv.ps_shift));
+            page = __ldg(table + ((base + lane * rows) >> cv.ps_shift));
             if (page < 0 || page >= cv.n_pages) {
               report(p.status, MFD_ERR_INPUT);
               page = cv.n_pages;  // outside the map: reads as zeros
             }
           }
-          if (E4M3) {
-            const int st = (int)(n % RN);
-            wait(&raw_empty[st], ((n / RN) & 1u) ^ 1u);
+          const int slot = (base + lane * rows) & (ps - 1);
+          const CUtensorMap *map = is_v ? &map_v : &map_k;
+#pragma unroll 1
+          for (int u = 0; u < NU; ++u) {
+            const bool sp = !E4M3 && is_v && base + BN > s.ctx;
+            uint64_t *bar = E4M3 ? &raw_full[st] : sp ? &special[st] : &full[st];
+            const int wide = E4M3 ? min(cv.D, SH::UC) : 128 * NB;
+            wait(E4M3 ? &raw_empty[st] : &empty[st], par ^ 1u);
             if (__all_sync(0xffffffffu, ok)) {
-              if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], (uint32_t)(some * rows * cv.D));
+              if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * rows * wide));
               __syncwarp();
-              if (lane < some)
-                tma_load_4d(sR + st * SH::RAW + lane * rows * cv.D, is_v ? &map_v : &map_k, 0,
-                            (base + lane * rows) & (ps - 1), s.h, page, &raw_full[st], policy);
-              issued |= 1u << st;
-              const uint32_t par = (n / RN) & 1u;
-              issued_par = (issued_par & ~(1u << st)) | (par << st);
-            }
-          } else {
-            const int st = (int)(n % ST);
-            wait(&empty[st], ((n / ST) & 1u) ^ 1u);
-            const bool sp = is_v && base + BN > s.ctx;
-            uint64_t *bar = sp ? &special[st] : &full[st];
-            if (__all_sync(0xffffffffu, ok)) {
-              if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * rows * 128 * NB));
-              __syncwarp();
-              if (lane < some)
+              if (lane < some) {
+                if (E4M3) {
+                  tma_load_4d(sR + st * SH::RAW + lane * rows * wide, map, u * SH::UC, slot, s.h, page, bar, policy);
+                } else {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                  tma_load_4d(sT + st * SH::STAGE + b * (BN * 128) + lane * rows * 128, is_v ? &map_v : &map_k, b * 64,
-                              (base + lane * rows) & (ps - 1), s.h, page, bar, policy);
+                  for (int b = 0; b < NB; ++b)
+                    tma_load_4d(sT + st * SH::STAGE + b * (BN * 128) + lane * rows * 128, map, u * SH::UC + b * 64, slot,
+                                s.h, page, bar, policy);
+                }
+              }
               issued |= 1u << st;
-              const uint32_t par = sp ? (special_par >> st) & 1u : (n / ST) & 1u;
-              issued_par = (issued_par & ~(1u << st)) | (par << st);
+              const uint32_t bp = sp ? (special_par >> st) & 1u : par;
+              issued_par = (issued_par & ~(1u << st)) | (bp << st);
               issued_special = (issued_special & ~(1u << st)) | ((sp ? 1u : 0u) << st);
               if (sp) special_par ^= 1u << st;
             }
+            if (++st == (E4M3 ? RN : ST)) {
+              st = 0;
+              par ^= 1u;
+            }
           }
-          ++n;
         }
       }
       // every load issued lands before the CTA may exit
       if (lane == 0)
-        for (int st = 0; st < (E4M3 ? RST : ST); ++st)
-          if ((issued >> st) & 1u)
-            mbar_wait(E4M3 ? &raw_full[st] : ((issued_special >> st) & 1u) ? &special[st] : &full[st],
-                      (issued_par >> st) & 1u, never);
+        for (uint32_t i = 0; i < (E4M3 ? RN : ST); ++i)
+          if ((issued >> i) & 1u)
+            mbar_wait(E4M3 ? &raw_full[i] : ((issued_special >> i) & 1u) ? &special[i] : &full[i],
+                      (issued_par >> i) & 1u, never);
       __syncwarp();
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (elect_one()) {
         // ----------------------------------------------------- MMAs
-        constexpr uint32_t id_s = idesc_16<T>(BM, BN, false), id_o = idesc_16<T>(BM, DP, true);
-        const int k_steps = (cv.D + 15) / 16;
-        uint32_t n = 0;  // ring position
-        uint32_t seg = 0, p_par = 0;
-        while (walk.next(p, s)) {
+        constexpr uint32_t id_s = idesc_16<T>(BM, BN, false), id_o = idesc_16<T>(BM, SH::UC, true);
+        uint32_t st = 0, par = 0;  // ring place and its phase
+        uint32_t q_par = 0, p_par = 0;
+        while (next_segment(true)) {
           const int nt = s.t1 - s.t0;
           if (nt == 0) continue;
-          const bool shared = s.it.active == 2;
+          const bool shared = s.active == 2;
           const int steps = shared ? 2 * nt : nt;
-          wait(q_full, seg & 1u);
-          ++seg;
+          wait(q_full, q_par);
+          q_par ^= 1u;
           uint32_t kst = 0, vst = 0;
+          auto take = [&]() {
+            const uint32_t now = st;
+            wait(&full[st], par);
+            if (++st == ST) {
+              st = 0;
+              par ^= 1u;
+            }
+            return now;
+          };
           auto scores = [&](int i) {
-            if (!shared || !(i & 1)) {
-              kst = n % ST;
-              wait(&full[kst], (n / ST) & 1u);
-              ++n;
-            }
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t qa = smem_u32(sQ) + (shared ? (uint32_t)(i & 1) * SH::Q_TILE : 0u);
-            const uint32_t ka = smem_u32(sT) + kst * SH::STAGE;
             const uint32_t d = tmem + SH::TM_S + (uint32_t)(i & 1) * BN;
-            for (int k = 0; k < k_steps; ++k) {
-              const uint64_t ad = smem_desc_sw128(qa + (uint32_t)(k >> 2) * (BM * 128) + (uint32_t)(k & 3) * 32);
-              const uint64_t bd = smem_desc_sw128(ka + (uint32_t)(k >> 2) * (BN * 128) + (uint32_t)(k & 3) * 32);
-              tc_mma_f16(d, ad, bd, id_s, k != 0);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              if (!shared || !(i & 1)) kst = take();
+              if (!ok) continue;
+              tc_fence_after();
+              const uint32_t qa =
+                  desc_lo(smem_u32(sQ) + (shared ? (uint32_t)(i & 1) * SH::Q_TILE : 0u) + u * (NB * BM * 128), 16);
+              const uint32_t ka = desc_lo(smem_u32(sT) + kst * SH::STAGE, 16);
+              const int k_steps = min(cv.D - u * SH::UC, SH::UC) / 16;
+#pragma unroll
+              for (int k = 0; k < SH::UC / 16; ++k)
+                if (k < k_steps)
+                  mma_ss(d, qa + (k >> 2) * (BM * 128 >> 4) + (k & 3) * 2, ka + (k >> 2) * (BN * 128 >> 4) + (k & 3) * 2,
+                         id_s, u != 0 || k != 0);
+              if (!shared || (i & 1)) tc_commit(&empty[kst]);
             }
-            tc_commit(&s_full[i & 1]);
-            if (!shared || (i & 1)) tc_commit(&empty[kst]);
+            if (ok) tc_commit(&s_full[i & 1]);
           };
           auto values = [&](int i) {
             wait(&p_full[i & 1], (p_par >> (i & 1)) & 1u);
             p_par ^= 1u << (i & 1);
-            if (!shared || !(i & 1)) {
-              vst = n % ST;
-              wait(&full[vst], (n / ST) & 1u);
-              ++n;
-            }
-            if (!ok) return;
-            tc_fence_after();
             const int acc = NS == 2 ? i & 1 : 0;
-            const uint32_t va = smem_u32(sT) + vst * SH::STAGE;
-            const uint32_t d = tmem + SH::TM_O + (uint32_t)acc * DP;
             const uint32_t a = tmem + SH::TM_S + (uint32_t)(i & 1) * BN;
+            const bool more = NS == 2 ? i >= 2 : i >= 1;
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              tc_mma_f16_ta(d, a + k * 8, smem_desc_sw128_mn(va + k * 2048, BN * 128), id_o,
-                            (NS == 2 ? i >= 2 : i >= 1) || k != 0);
-            tc_commit(&pv_done[acc]);
-            if (!shared || (i & 1)) tc_commit(&empty[vst]);
+            for (int u = 0; u < NU; ++u) {
+              if (!shared || !(i & 1)) vst = take();
+              if (!ok) continue;
+              tc_fence_after();
+              const uint32_t va = desc_lo(smem_u32(sT) + vst * SH::STAGE, BN * 128);
+              const uint32_t d = tmem + SH::TM_O + (uint32_t)(acc * DP + u * SH::UC);
+#pragma unroll
+              for (int k = 0; k < BN / 16; ++k) mma_ts(d, a + k * 8, va + k * (2048 >> 4), id_o, more || k != 0);
+              if (!shared || (i & 1)) tc_commit(&empty[vst]);
+            }
+            if (ok) tc_commit(&pv_done[acc]);
           };
-          scores(0);
-          if (steps > 1) scores(1);
-          for (int i = 0; i < steps; ++i) {
-            values(i);
+          // one place each in the code for scores and values
+          for (int i = -2; i < steps; ++i) {
+            if (i >= 0) values(i);
             if (i + 2 < steps) scores(i + 2);
           }
         }
@@ -664,31 +907,53 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         mbar_wait(drain, 0, never);
       }
       __syncwarp();
+    } else if (warp == 2) {
+      if (lane == 0) sched.emit(p, seg_ring, seg_full, seg_empty);
+      __syncwarp();
     }
   } else if (warp < SH::HELP_WARP) {
     // --------------------------------------------------------- softmax
-    if (NS == 2) regs_up<192>();
+    regs_up<SH::REGS_SOFTMAX>();
     const int ws = NS == 2 ? (warp - 4) >> 2 : 0;  // stream
     const int wq = warp & 3;                       // the warp's lanes of tensor memory
     const int r = wq * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t o_base = lane_base + SH::TM_O + (uint32_t)ws * DP;
     uint32_t s_par = 0, pv_n = 0;
     // alternating streams exchange (m, l) in the space of the second Q tile
     float2 *ml_s = reinterpret_cast<float2 *>(sQ + (NS - 1) * SH::Q_TILE);
-    while (walk.next(p, s)) {
+    while (next_segment_warp()) {
       const int nt = s.t1 - s.t0;
-      const bool shared = s.it.active == 2;
+      const bool shared = s.active == 2;
       const int live = s.nn * p.G;
       const int rt = shared ? ws : 0;                     // row tile of the group
-      const int row = (s.pair * NS + rt) * BM + r;        // this thread's row
+      const int row0 = (s.pair * NS + rt) * BM;
+      const int row = row0 + r;                           // this thread's row
       const int node = row / p.G, g = row - node * p.G;
       const bool row_live = row < live && nt > 0;
-      const bool warp_live = (s.pair * NS + rt) * BM + wq * 32 < live && nt > 0;
+      const bool warp_live = row0 + wq * 32 < live && nt > 0;
 
+      // queries: 16-byte chunks to the swizzled tile; rows that are not live
+      // stay as they are (a row's scores reach no other row)
+      if (nt > 0) {
+        constexpr int C = DP / 8, STEP = 128 / C;
+        const int base_row = shared || NS == 1 ? 0 : ws * (BM / 2);  // alternating: half the rows each
+        const int have = min(shared || NS == 1 ? BM : BM / 2, live - row0 - base_row);  // rows to load
+        const int ch = r % C;
+        const uint32_t dst = smem_u32(sQ + rt * SH::Q_TILE) + (ch >> 3) * (BM * 128);
+        const uint16_t *src = p.q + (int64_t)s.q * p.N * p.q_stride + (int64_t)s.h * p.G * cv.D + ch * 8;
+        if (ch * 8 < cv.D)
+#pragma unroll 2
+          for (int i = r / C; i < have; i += STEP) {
+            const int rr = base_row + i;
+            const int n1 = (row0 + rr) / p.G, g1 = row0 + rr - n1 * p.G;
+            cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), src + n1 * p.q_stride + g1 * cv.D);
+          }
+      }
       // rows past n_nodes, once per item
       if (s.head) {
         const int zrow = (s.pair * NS + ws) * BM + r;
-        if (zrow < p.M && zrow >= (s.it.tiles ? live : 0)) {
+        if (zrow < p.M && zrow >= (s.tiles ? live : 0)) {
           const int zn = zrow / p.G, zg = zrow - zn * p.G;
           const int64_t at = ((int64_t)s.q * p.N + zn) * p.Hq + s.h * p.G + zg;
           for (int d = 0; d < cv.D; d += 8) *reinterpret_cast<uint4 *>(p.out + at * cv.D + d) = make_uint4(0, 0, 0, 0);
@@ -696,27 +961,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         }
       }
       if (nt == 0) continue;
-
-      // queries: 16-byte chunks to the swizzled tile; rows that are not live
-      // stay as they are (a row's scores reach no other row)
-      {
-        constexpr int C = DP / 8;
-        const int tiles_rows = shared || NS == 1 ? BM : BM / 2;  // alternating: half the rows each
-        const int row_first = shared || NS == 1 ? 0 : ws * (BM / 2);
-        uint8_t *dst = sQ + rt * SH::Q_TILE;
-        const int t128 = wq * 32 + lane;
-        const int ch = t128 % C;
-        for (int i = t128 / C; i < tiles_rows; i += 128 / C) {
-          const int rr = row_first + i, grow = (s.pair * NS + rt) * BM + rr;
-          if (grow >= live) break;
-          const int n1 = grow / p.G, g1 = grow - n1 * p.G;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (ch * 8 < cv.D)
-            x = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)s.q * p.N + n1) * p.q_stride +
-                                                      (int64_t)(s.h * p.G + g1) * cv.D + ch * 8));
-          *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (BM * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = x;
-        }
-      }
+      cp_async_wait();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -768,35 +1013,39 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             if (done) {
               wait(&pv_done[ws], (pv_n - 1u) & 1u);
               tc_fence_after();
-              const uint32_t oa = lane_base + SH::TM_O + (uint32_t)ws * DP;
 #pragma unroll 1
               for (int d = 0; d < DP; d += 16) {
                 uint32_t o[16];
-                tmem_ld16(oa + d, o);
+                tmem_ld16(o_base + d, o);
                 tmem_wait_ld();
                 tie16(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                tmem_st16(oa + d, o);
+                tmem_st16(o_base + d, o);
               }
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t cc = pair(p.c, p.c), mm = pair(-mz, -mz);
+          uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll
           for (int part = 0; part < BN / 32; ++part) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float a = ex2(fmaf(__uint_as_float(xr[32 * part + 2 * k]), p.c, -mz));
-              const float b = ex2(fmaf(__uint_as_float(xr[32 * part + 2 * k + 1]), p.c, -mz));
-              sum[(2 * k) & 3] += a;
-              sum[(2 * k + 1) & 3] += b;
+              const int e = 32 * part + 2 * k;
+              const float2 y = unpair(fma2(pair(__uint_as_float(xr[e]), __uint_as_float(xr[e + 1])), cc, mm));
+              const float a = ex2(y.x), b = ex2(y.y);
+              if (k & 1)
+                sum1 = add2(sum1, pair(a, b));
+              else
+                sum0 = add2(sum0, pair(a, b));
               pk[k] = pack2<T>(a, b);
             }
             tmem_st16(sa + 16 * part, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 sum = unpair(add2(sum0, sum1));
+          l += sum.x + sum.y;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -831,136 +1080,152 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           }
         }
       }
-      const bool whole = s.t0 == 0 && s.t1 == s.it.tiles;
+      const bool whole = s.t0 == 0 && s.t1 == s.tiles;
       if (ok && (!alternating || ws == 0) && warp_live) {
         const bool two = alternating && steps > 1;
-        const uint32_t oa = lane_base + SH::TM_O + (uint32_t)(alternating ? 0 : ws) * DP;
-        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          a0 *= inv;
+          a1 *= inv;
+        }
         const int64_t at = row_live ? ((int64_t)s.q * p.N + node) * p.Hq + s.h * p.G + g : 0;
-        const int prow = rt * BM + r;
-        const int slot = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
+        const int part = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
         const bool fix = p.N > 1 && s.t1 * BN > s.ctx && *any_bad;
-        // the values' place, for those added back
-        const int hstart = s.h;
+        uint16_t *out = p.out + at * cv.D;
+        float4 *po = p.part_o + (int64_t)part * (cv.D / 4) * p.part_rows + rt * BM + r;
 #pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-          if (d >= cv.D) break;
-          uint32_t o[32], o1[32];
-          tmem_ld32(oa + d, o);
-          if (two) tmem_ld32(oa + DP + d, o1);
+        for (int d = 0; d < cv.D; d += 16) {
+          uint32_t o[16], o1[16];
+          tmem_ld16(o_base + d, o);
+          if (two) tmem_ld16(o_base + DP + d, o1);
           tmem_wait_ld();
-          tie32(o);
-          if (two) tie32(o1);
-          float f[32];
+          tie16(o);
+          float f[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float x = __uint_as_float(o[k]);
-            if (alternating) {
-              x *= a0;
-              if (two) x = fmaf(__uint_as_float(o1[k]), a1, x);
-            }
-            f[k] = x * inv;
-          }
-          if (fix && row_live) {
-            const int lo = max(0, s.t0 * BN - s.ctx), hi = min(s.nn, s.t1 * BN - s.ctx);
-            for (int j = lo; j < hi; ++j) {
-              if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
-              const bool sees = mask_row ? (__ldg(mask_row + (j >> 5)) >> (j & 31)) & 1u : j <= node;
-              if (!sees) continue;
-              const int pos = s.ctx + j;
-              const int page = __ldg(cv.table + (size_t)s.q * cv.max_pages + (pos >> cv.ps_shift));
-              if (page < 0 || page >= cv.n_pages) continue;
-              const int64_t e = page * cv.page_stride + hstart * cv.head_stride +
-                                (int64_t)(pos & ((1 << cv.ps_shift) - 1)) * cv.token_stride;
+          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[k]) * a0;
+          if (two) {
+            tie16(o1);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                if (d + k < cv.D) {
-                  if (E4M3) {
-                    f[k] = __int_as_float(0x7FFFFFFF);
-                  } else {
-                    const uint32_t w = static_cast<const uint16_t *>(cv.v)[e + d + k];
-                    if (nonfinite2<T>(w)) f[k] += unpack2<T>(w).x;
-                  }
-                }
-              }
-            }
+            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(o1[k]), a1, f[k]);
           }
+          if (fix && row_live) add_back<T, E4M3>(p, s.q, s.h, s.ctx, max(0, s.t0 * BN - s.ctx), min(s.nn, s.t1 * BN - s.ctx), node, mask_row,
+                              bad, d, f);
           if (row_live) {
             if (whole) {
+              float y[8];
 #pragma unroll
-              for (int k = 0; k < 32; k += 8)
-                if (d + k < cv.D) {
-                  float y[8];
+              for (int e = 0; e < 8; ++e) y[e] = f[e];
+              *reinterpret_cast<uint4 *>(out + d) = pack8<T>(y);
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = f[k + e];
-                  *reinterpret_cast<uint4 *>(p.out + at * cv.D + d + k) = pack8<T>(y);
-                }
+              for (int e = 0; e < 8; ++e) y[e] = f[8 + e];
+              *reinterpret_cast<uint4 *>(out + d + 8) = pack8<T>(y);
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                if (d + k < cv.D)
-                  p.part_o[((int64_t)slot * (cv.D / 4) + (d + k) / 4) * p.part_rows + prow] =
-                      make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+              for (int k = 0; k < 16; k += 4)
+                po[(int64_t)((d + k) >> 2) * p.part_rows] = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
             }
           }
         }
         if (row_live) {
-          if (whole) {
-            if (p.lse) p.lse[at] = m == -INFINITY && l == 0.f ? -INFINITY : m * LN2 + logf(l);
-          } else {
-            p.part_ml[(int64_t)slot * p.part_rows + prow] = make_float2(m, l);
-          }
+          if (!whole)
+            p.part_ml[(int64_t)part * p.part_rows + rt * BM + r] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[at] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
         }
       }
       tc_fence_before();
       if (alternating) named_sync(1, 256);  // the first stream has read the second's O and (m, l)
       tc_fence_after();
-      if (ws == 0)
-        named_sync(2, 128);
-      else
-        named_sync(3, 128);
-      if (r == 0) {
-        __threadfence_block();
-        seg_done[ws] = seg_done[ws] + 1;
+      if (p.N > 1) {  // the noted nodes are read: the helpers may clear them
+        if (ws == 0)
+          named_sync(2, 128);
+        else
+          named_sync(3, 128);
+        if (r == 0) {
+          __threadfence_block();
+          seg_done[ws] = seg_done[ws] + 1;
+        }
       }
     }
   } else {
     // --------------------------------------------------------- helpers
-    if (NS == 2) regs_down<64>();
+    if (SH::REGS_HELP < SH::REGS) regs_down<SH::REGS_HELP>();
     const int ht = tid - SH::HELP_WARP * 32;
-    uint32_t n = 0, special_par = 0;
+    uint32_t st = 0, par = 0, rs = 0, rpar = 0;  // places in the rings and their phases
+    uint32_t special_par = 0;
     int seg = 0;
-    while (walk.next(p, s)) {
+    while (next_segment_warp()) {
       const int nt = s.t1 - s.t0;
       if (nt == 0) continue;
-      const bool shared = s.it.active == 2;
+      const bool shared = s.active == 2;
       const int len = s.ctx + s.nn;
       // one row per request: every key before the end is seen
       const bool note = p.N > 1;
       bool clean = false;  // the bad-node bits are this segment's
-      // exponent bytes of position t (keys, values)
-      auto codes = [&](int t, int &ck, int &cvv) {
-        ck = cvv = 0;
-        if (ht < BN && t < len) {
-          const int page = __ldg(cv.table + (size_t)s.q * cv.max_pages + (t >> cv.ps_shift));
-          if (page >= 0 && page < cv.n_pages) {
-            const int64_t e = (((int64_t)page * cv.Hk + s.h) << cv.ps_shift) + (t & ((1 << cv.ps_shift) - 1));
-            ck = __ldg(cv.k_exp + e);
-            cvv = __ldg(cv.v_exp + e);
+      // The bits serve the previous segment until its rows are out.
+      auto clear_bad = [&]() {
+        if (ok) {
+          const unsigned long long t0 = globaltimer();
+          for (uint32_t it = 1;; ++it) {
+            if (seg_done[0] >= seg && (NS == 1 || seg_done[1] >= seg)) break;
+            if ((it & 15u) == 0 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
+              if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            __nanosleep(64);
           }
+        }
+        named_sync(4, 128);
+        for (int k = ht; k < MAX_N / 32; k += 128) bad[k] = 0;
+        if (ht == 0) *any_bad = 0;
+        named_sync(4, 128);
+      };
+      // E4M3: a position's two exponent bytes, by the thread of that position:
+      // its page is looked up four tiles ahead, the bytes loaded three ahead
+      // and written as powers two ahead.
+      const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
+      auto page_at = [&](int j) {
+        const int t = (s.t0 + j) * BN + ht;
+        return j < nt && t < len ? __ldg(table + (t >> cv.ps_shift)) : -1;
+      };
+      auto codes = [&](int j, int page, int &ck, int &cvv) {
+        const int t = (s.t0 + j) * BN + ht;
+        ck = cvv = -1;
+        if (page >= 0 && page < cv.n_pages) {
+          const int64_t e = (((int64_t)page * cv.Hk + s.h) << cv.ps_shift) + (t & ((1 << cv.ps_shift) - 1));
+          ck = __ldg(cv.k_exp + e);
+          cvv = __ldg(cv.v_exp + e);
         }
       };
       auto put_codes = [&](int j, int ck, int cvv) {
-        if (ht < BN) {
-          sC[(j & 7) * 128 + ht] = (uint8_t)ck;
-          sC[1024 + (j & 7) * 128 + ht] = (uint8_t)cvv;
+        const int t = (s.t0 + j) * BN + ht;
+        bool wk = false, wv = false;
+        uint16_t pk = ck < 0 ? 0 : Widen<T>::power(ck, wk), pv = cvv < 0 ? 0 : Widen<T>::power(cvv, wv);
+        if (cvv == EXP_NAN && note && t >= s.ctx) {
+          // a NaN that some rows do not see: out of the product, added back later
+          pv = 0;
+          atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
+          *any_bad = 1;
         }
+        sC[(j & 3) * BN + ht] = pk;
+        sC[4 * BN + (j & 3) * BN + ht] = pv;
+        if (wk) atomicOr(wide_s, 1u << (j & 7));
+        if (wv) atomicOr(wide_s, 256u << (j & 7));
       };
+      int ck = -1, cvv = -1, pg = -1;
       if (E4M3) {
-        named_sync(4, 128);  // every helper is done with the last segment's bytes
+        if (note && s.t1 * BN > s.ctx) clear_bad();
+        named_sync(4, 128);  // every helper is done with the last segment's powers
+        if (ht == 0) *wide_s = 0;
+        const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
+        pg = page_at(3);
         int ck0, cv0, ck1, cv1;
-        codes(s.t0 * BN + ht, ck0, cv0);
-        codes((s.t0 + 1) * BN + ht, ck1, cv1);
+        codes(0, p0, ck0, cv0);
+        codes(1, p1, ck1, cv1);
+        codes(2, p2, ck, cvv);
+        named_sync(4, 128);
         put_codes(0, ck0, cv0);
         put_codes(1, ck1, cv1);
       }
@@ -970,118 +1235,80 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int j = is_v ? -1 - o : o;
         const int base = (s.t0 + j) * BN;
         const bool sp = is_v && base + BN > s.ctx;
-        if (sp && note && !clean) {
-          // the bits still serve the previous segment until its rows are out
-          if (ok) {
-            const unsigned long long t0 = globaltimer();
-            for (uint32_t it = 1;; ++it) {
-              if (seg_done[0] >= seg && (NS == 1 || seg_done[1] >= seg)) break;
-              if ((it & 15u) == 0 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
-                if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
-                *abort_flag = 1;
-                ok = false;
-                break;
-              }
-              __nanosleep(64);
-            }
-          }
-          named_sync(4, 128);
-          for (int k = ht; k < MAX_N / 32; k += 128) bad[k] = 0;
-          if (ht == 0) *any_bad = 0;
-          named_sync(4, 128);
+        if (!E4M3 && sp && note && !clean) {
+          clear_bad();
           clean = true;
         }
-        const int st = (int)(n % ST);
-        if (E4M3) {
-          const int rs = (int)(n % RN);
-          int ck = 0, cvv = 0;
-          if (!is_v) {
-            named_sync(4, 128);  // this tile's exponent bytes are written
-            if (j + 2 < nt) codes(base + 2 * BN + ht, ck, cvv);
-          }
-          wait(&empty[st], ((n / ST) & 1u) ^ 1u);
-          wait(&raw_full[rs], (n / RN) & 1u);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            const uint8_t *src = sR + rs * SH::RAW;
-            uint8_t *dst = sT + st * SH::STAGE;
-            const uint8_t *code = sC + (is_v ? 1024 : 0) + (j & 7) * 128;
-            constexpr int C = DP / 16;
-#pragma unroll 4
-            for (int k = 0; k < BN * C / 128; ++k) {
-              const int idx = ht + 128 * k;
-              const int tok = idx / C, ch = idx % C;
-              uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-              const int t = base + tok;
-              if (ch * 16 < cv.D && t < len) {
-                const int cd = code[tok];
-                if (cd != EXP_NAN) {
-                  const uint4 x = *reinterpret_cast<const uint4 *>(src + tok * cv.D + ch * 16);
-                  const Widen<T> widen(cd);
-                  uint2 a = widen(x.x), b = widen(x.y);
-                  lo = make_uint4(a.x, a.y, b.x, b.y);
-                  a = widen(x.z);
-                  b = widen(x.w);
-                  hi = make_uint4(a.x, a.y, b.x, b.y);
-                } else if (sp && note && t >= s.ctx) {
-                  atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
-                  *any_bad = 1;
-                } else {
-                  lo = hi = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-                }
-              }
-              uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok * 128;
-              const int c2 = (ch & 3) * 2, x7 = tok & 7;
-              // neighbouring blocks' lanes write their two chunks in opposite order (other banks)
-              const bool sw = (ch >> 2) & 1;
-              *reinterpret_cast<uint4 *>(row + (((c2 + (sw ? 1 : 0)) ^ x7) << 4)) = sw ? hi : lo;
-              *reinterpret_cast<uint4 *>(row + (((c2 + (sw ? 0 : 1)) ^ x7) << 4)) = sw ? lo : hi;
-            }
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0 && ok) {
-            mbar_arrive(&raw_empty[rs]);
-            mbar_arrive(&full[st]);
-          }
-          if (!is_v && j + 2 < nt) put_codes(j + 2, ck, cvv);
-        } else if (sp) {
-          wait(&special[st], (special_par >> st) & 1u);
-          special_par ^= 1u << st;
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            uint8_t *dst = sT + st * SH::STAGE;
-            constexpr int C = DP / 8;
-#pragma unroll 4
-            for (int k = 0; k < BN * C / 128; ++k) {
-              const int idx = ht + 128 * k;
-              const int tok = idx / C, ch = idx % C;
-              const int t = base + tok;
-              uint4 *at = reinterpret_cast<uint4 *>(dst + (ch >> 3) * (BN * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-              if (t >= len) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if (note && t >= s.ctx) {
-                uint4 x = *at;
-                if (nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w)) {
-                  uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const uint32_t z = nonfinite2<T>(w[e]);
-                    if (z & 0x8000u) w[e] &= 0xFFFF0000u;
-                    if (z & 0x80000000u) w[e] &= 0x0000FFFFu;
-                  }
-                  *at = make_uint4(w[0], w[1], w[2], w[3]);
-                  atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
-                  *any_bad = 1;
-                }
-              }
-            }
-          }
-          fence_async_smem();
-          named_sync(4, 128);
-          if (ht == 0 && ok) mbar_arrive(&full[st]);
+        if (E4M3 && !is_v) {
+          if (ht == 0) atomicAnd(wide_s, ~(0x101u << ((j + 4) & 7)));
+          named_sync(4, 128);  // this tile's powers are written; the slot of tile j - 2 is free
+          put_codes(j + 2, ck, cvv);
+          codes(j + 3, pg, ck, cvv);
+          pg = page_at(j + 4);
         }
-        ++n;
+#pragma unroll 1
+        for (int u = 0; u < NU; ++u) {
+          if (E4M3) {
+            wait(&empty[st], par ^ 1u);
+            wait(&raw_full[rs], rpar);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              const bool slow = (*static_cast<volatile uint32_t *>(wide_s) >> ((j & 7) + (is_v ? 8 : 0))) & 1u;
+              widen_unit<T, DP>(p, sR + rs * SH::RAW, sT + st * SH::STAGE, sC + (is_v ? 4 * BN : 0) + (j & 3) * BN, ht,
+                                u * SH::UC);
+              if (slow)
+                widen_unit_wide<T, DP>(p, s.q, s.h, len, sR + rs * SH::RAW, sT + st * SH::STAGE, base, is_v, ht, u * SH::UC);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && ok) {
+              mbar_arrive(&raw_empty[rs]);
+              mbar_arrive(&full[st]);
+            }
+            if (++rs == RN) {
+              rs = 0;
+              rpar ^= 1u;
+            }
+          } else if (sp) {
+            wait(&special[st], (special_par >> st) & 1u);
+            special_par ^= 1u << st;
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              uint8_t *dst = sT + st * SH::STAGE;
+              constexpr int C = SH::UC / 8, PER = 128 / C;
+              const int ch = ht % C;
+#pragma unroll 4
+              for (int tok = ht / C; tok < BN; tok += PER) {
+                const int t = base + tok;
+                uint4 *at = reinterpret_cast<uint4 *>(dst + (ch >> 3) * (BN * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                if (t >= len) {
+                  *at = make_uint4(0, 0, 0, 0);
+                } else if (note && t >= s.ctx) {
+                  const uint4 x = *at;
+                  if (nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w)) {
+                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const uint32_t z = nonfinite2<T>(w[e]);
+                      if (z & 0x8000u) w[e] &= 0xFFFF0000u;
+                      if (z & 0x80000000u) w[e] &= 0x0000FFFFu;
+                    }
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
+                    *any_bad = 1;
+                  }
+                }
+              }
+            }
+            fence_async_smem();
+            named_sync(4, 128);
+            if (ht == 0 && ok) mbar_arrive(&full[st]);
+          }
+          if (++st == ST) {
+            st = 0;
+            par ^= 1u;
+          }
+        }
       }
       ++seg;
     }
@@ -1094,94 +1321,162 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
 
 // ------------------------------------------------------------------ join
 
-// Combines the parts of an item that borders cut: one block per (pair of an
-// item, request and head), a thread per row and 8 columns.
-template <typename T, int NS, int BN>
-__global__ void __launch_bounds__(256) join_kernel(const Params p, int n_cta) {
-  __shared__ int64_t sums[2];  // before this request, in all
-  const int pair = blockIdx.x, h = blockIdx.y, q = blockIdx.z, tid = threadIdx.x;
-  if (tid < 2) sums[tid] = 0;
-  block_sync();
-  int64_t before = 0, total = 0;
-  for (int i = tid; i < p.n_req; i += 256) {
+constexpr int JOIN_ROWS = 16;
+
+// Combines the parts of the items that borders cut.  Block (c, y): the item
+// whose first inner border is CTA c + 1's start, if there is one, and 16 of its
+// rows; first every part's weight 2^(m - max m) / sum for these rows, then a
+// thread for each row and 8 columns adds the parts up in their order.
+template <typename T, int NS>
+__global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p, int n_cta) {
+  __shared__ int64_t sums[3];  // the line's length, the request's start on it, the request
+  __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
+  __shared__ int slot_s[ATTENTION_MAX_CTAS];
+  __shared__ int64_t cost_s[1024];
+  const int tid = threadIdx.x, lane = tid & 31, threads = JOIN_ROWS * (p.cv.D / 8);
+  for (int i = tid; i < p.n_req; i += threads) {
     int ctx, nn;
     lengths(p, i, ctx, nn);
-    const int64_t c = p.cv.Hk * head_cost<NS, BN>(p, ctx, nn);
-    total += c;
-    if (i < q) before += c;
+    cost_s[i] = p.cv.Hk * head_cost<NS>(p, ctx, nn);
   }
-  if (total) atomicAdd(reinterpret_cast<unsigned long long *>(&sums[1]), (unsigned long long)total);
-  if (before) atomicAdd(reinterpret_cast<unsigned long long *>(&sums[0]), (unsigned long long)before);
   block_sync();
-  total = sums[1];
+  const int c = (int)blockIdx.x + 1;
+  if (tid < 32) {
+    int64_t total = 0;
+    for (int i = lane; i < p.n_req; i += 32) total += cost_s[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int64_t x = border(total, c, n_cta);
+    if (lane == 0) {
+      sums[0] = total;
+      int64_t before = 0;
+      int q = 0;
+      while (q < p.n_req - 1 && before + cost_s[q] <= x) before += cost_s[q++];
+      sums[1] = before;
+      sums[2] = q;
+    }
+  }
+  block_sync();
+  const int64_t total = sums[0], x = border(total, c, n_cta);
+  const int q = (int)sums[2];
   int ctx, nn;
   lengths(p, q, ctx, nn);
-  const Item it = item_of<NS, BN>(p, ctx, nn, pair);
-  if (it.tiles == 0) return;
-  int64_t u0 = sums[0] + h * head_cost<NS, BN>(p, ctx, nn);
-  for (int i = 0; i < pair; ++i) u0 += item_of<NS, BN>(p, ctx, nn, i).cost;
-  const int64_t u1 = u0 + it.cost;
-  const int c0 = cta_of(total, u0, n_cta), c1 = cta_of(total, u1 - 1, n_cta);
-  if (c0 == c1) return;
-  // a part's key tiles; returns its slot, or -1 if it holds none, -2 if all
-  auto slot_of = [&](int c) {
-    const int64_t lo = border(total, c, n_cta), hi = border(total, c + 1, n_cta);
-    const int a = (int)((lo > u0 ? lo : u0) - u0), b = (int)((hi < u1 ? hi : u1) - u0);
-    const int t0 = tile_at(it, a), t1 = tile_at(it, b);
-    if (t0 >= t1) return -1;
-    if (t0 == 0 && t1 == it.tiles) return -2;
-    return 2 * c + (t0 == 0 ? 1 : 0);
-  };
-  const int first = pair * NS * BM;
-  const int rows = min(nn * p.G - first, NS * BM);
-  const int C8 = p.cv.D / 8;
-  for (int i = tid; i < rows * C8; i += 256) {
-    const int r = i % rows, ch = i / rows;
-    float m = -INFINITY, l = 0.f, acc[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-    bool direct = false;
-    for (int c = c0; c <= c1; ++c) {
-      const int s = slot_of(c);
-      if (s == -1) continue;
-      if (s == -2) {
-        direct = true;
-        break;
-      }
-      const float2 ml = p.part_ml[(int64_t)s * p.part_rows + r];
-      const float4 a = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch) * p.part_rows + r];
-      const float4 b = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch + 1) * p.part_rows + r];
-      const float top = fmaxf(m, ml.x);
-      const float w0 = m == -INFINITY ? 0.f : ex2(m - top), w1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // this part's keys are not seen
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = (m == -INFINITY ? 0.f : acc[k] * w0) + x[k] * w1;
-      l = l * w0 + (ml.x == -INFINITY ? ml.y : ml.y * w1);
-      m = top;
-    }
-    if (direct) return;
-    const int node = (first + r) / p.G, g = first + r - node * p.G;
-    const int64_t at = ((int64_t)q * p.N + node) * p.Hq + h * p.G + g;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    float y[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = acc[k] * inv;
-    *reinterpret_cast<uint4 *>(p.out + at * p.cv.D + ch * 8) = pack8<T>(y);
-    if (p.lse && ch == 0) p.lse[at] = m == -INFINITY && l == 0.f ? -INFINITY : m * LN2 + logf(l);
+  const int64_t hc = head_cost<NS>(p, ctx, nn);
+  const int h = (int)divide(x - sums[1], hc);
+  int64_t u0 = sums[1] + h * hc;
+  int pr = 0;
+  Item it;
+  for (;; ++pr) {
+    it = item_of<NS>(p, ctx, nn, pr);
+    if (x < u0 + it.cost) break;
+    u0 += it.cost;
   }
+  const int64_t u1 = u0 + it.cost;
+  // Every block waits for the parts, also those with nothing to join: this grid
+  // must not end before the one it follows.
+  if (x == u0 || border(total, c - 1, n_cta) > u0 || it.tiles == 0) {  // not cut here, or another block's
+    pdl_wait();
+    return;
+  }
+  const int first = pr * NS * BM;
+  const int rows = min(nn * p.G - first, NS * BM);
+  const int row0 = (int)blockIdx.y * JOIN_ROWS;
+  const int c0 = c - 1, n_part = cta_of(total, u1 - 1, n_cta) - c0 + 1;
+  // each part's slot, or -1 if it holds no key tile; all tiles in one part: it wrote the result
+  bool direct = false;
+  for (int i = tid; i < n_part; i += threads) {
+    const int64_t lo = border(total, c0 + i, n_cta), hi = border(total, c0 + i + 1, n_cta);
+    const int t0 = tile_at(it, (int)((lo > u0 ? lo : u0) - u0)), t1 = tile_at(it, (int)((hi < u1 ? hi : u1) - u0));
+    slot_s[i] = t0 >= t1 ? -1 : 2 * (c0 + i) + (t0 == 0 ? 1 : 0);
+    direct |= t0 == 0 && t1 == it.tiles;
+  }
+  pdl_wait();
+  if (__syncthreads_or(direct) || row0 >= rows) return;
+  // weights: D / 8 threads (a power of two of them, at most 16) for each row
+  const int G = p.cv.D >= 128 ? 16 : p.cv.D >= 64 ? 8 : p.cv.D >= 32 ? 4 : 2;
+  if (tid < JOIN_ROWS * G) {
+    const int r = tid / G, j = tid % G, row = row0 + r;
+    const unsigned group = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane / G * G);
+    float m = -INFINITY;
+    for (int i = j; i < n_part; i += G)
+      if (slot_s[i] >= 0 && row < rows) m = fmaxf(m, p.part_ml[(int64_t)slot_s[i] * p.part_rows + row].x);
+    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, o));
+    float l = 0.f;
+    for (int i = j; i < n_part; i += G) {
+      float w = 0.f;
+      if (slot_s[i] >= 0 && row < rows) {
+        const float2 ml = p.part_ml[(int64_t)slot_s[i] * p.part_rows + row];
+        // a part whose keys are not seen has sum 0; one whose scores are NaN a NaN
+        w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : ex2(ml.x - m);
+        l += w * ml.y;
+      }
+      w_s[i][r] = w;
+    }
+    for (int o = G / 2; o > 0; o >>= 1) l += __shfl_xor_sync(group, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int i = j; i < n_part; i += G) w_s[i][r] *= inv;
+    if (row < rows && p.lse && j == 0) {
+      const int node = (first + row) / p.G, g = first + row - node * p.G;
+      p.lse[((int64_t)q * p.N + node) * p.Hq + h * p.G + g] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
+    }
+  }
+  __syncthreads();
+  const int r = tid % JOIN_ROWS, ch = tid / JOIN_ROWS, row = row0 + r;
+  if (row >= rows) return;
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n_part; ++i) {
+    const int s = slot_s[i];
+    const float w = w_s[i][r];
+    if (s < 0 || w == 0.f) continue;
+    const float4 a = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch) * p.part_rows + row];
+    const float4 b = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch + 1) * p.part_rows + row];
+    acc[0] = fmaf(w, a.x, acc[0]);
+    acc[1] = fmaf(w, a.y, acc[1]);
+    acc[2] = fmaf(w, a.z, acc[2]);
+    acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]);
+    acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]);
+    acc[7] = fmaf(w, b.w, acc[7]);
+  }
+  const int node = (first + row) / p.G, g = first + row - node * p.G;
+  *reinterpret_cast<uint4 *>(p.out + (((int64_t)q * p.N + node) * p.Hq + h * p.G + g) * p.cv.D + ch * 8) = pack8<T>(acc);
 }
 
 template <typename T, int DP, bool E4M3>
 cudaError_t launch_shape(const AttentionLaunch &A, const Params &p, int n_cta, cudaStream_t stream) {
   using SH = Shape<DP, E4M3>;
   static_assert(SH::SMEM <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, DP, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};  // devices this kernel is set up on
+  if (dev > 63 || !((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
+    if ((e = cudaFuncSetAttribute(attention_kernel<T, DP, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM)) !=
+        cudaSuccess)
+      return e;
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, attention_kernel<T, DP, E4M3>)) != cudaSuccess) return e;
+    if (a.numRegs != SH::REGS) return cudaErrorInvalidConfiguration;  // the shares would not add up
+    if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  }
   attention_kernel<T, DP, E4M3><<<n_cta, SH::THREADS, SH::SMEM, stream>>>(*A.map_k, *A.map_v, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  join_kernel<T, SH::NS, SH::BN><<<dim3(p.n_pair, p.cv.Hk, p.n_req), 256, 0, stream>>>(p, n_cta);
-  return cudaGetLastError();
+  // the join launches while the last CTAs run and waits for them before it reads their parts
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_cta - 1, (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
+  cfg.blockDim = dim3(JOIN_ROWS * (p.cv.D / 8));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, SH::NS>, p, n_cta);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, bool E4M3>
@@ -1200,9 +1495,8 @@ size_t attention_part_bytes(int M, int D) {
   // two parts at most for every CTA: of the item its stretch starts in, and of the one it ends in
   return (size_t)2 * ATTENTION_MAX_CTAS * part_rows(M, D) * ((size_t)D * 4 + 8);
 }
-int attention_box_rows(int page_size, int D) {
-  const int bn = D > 128 ? 64 : 128;
-  return page_size < bn ? page_size : bn;
+int attention_box_rows(int page_size) {
+  return page_size < BN ? page_size : BN;
 }
 
 cudaError_t launch_tree_attention(const AttentionLaunch &A, cudaStream_t stream) {

@@ -59,7 +59,7 @@ cudaError_t launch_kv_commit(const KvCommitLaunch &A, cudaStream_t stream);
 // attention.cu
 constexpr int ATTENTION_MAX_CTAS = 152;  // GB300's SMs: scratch is sized without asking the device
 size_t attention_part_bytes(int M, int D);
-int attention_box_rows(int page_size, int D);  // positions of a tensor map's box
+int attention_box_rows(int page_size);  // positions of a tensor map's box
 struct AttentionLaunch {
   const void *q;
   int64_t q_stride;

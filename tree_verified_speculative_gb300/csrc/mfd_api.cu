@@ -721,8 +721,8 @@ std::map<KvMapKey, CUtensorMap> g_kv_maps;
 
 // Keys or values as a 4-D tensor (D, slot, head, page).  A 16-bit cache's box
 // is 64 columns x `rows` slots of one head and page with the 128-byte swizzle
-// (columns past D read as zero); an E4M3 one's is D columns x `rows` slots as
-// they are.
+// (columns past D read as zero); an E4M3 one's is D or 128 columns x `rows`
+// slots as they are.
 int kv_map(const void *ptr, const mfd::CacheView &c, int rows, CUtensorMap *out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MFD_ERR_CUDA;
@@ -739,7 +739,7 @@ int kv_map(const void *ptr, const mfd::CacheView &c, int rows, CUtensorMap *out)
     const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)1 << c.ps_shift, (cuuint64_t)c.Hk, (cuuint64_t)c.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)(c.token_stride * esz), (cuuint64_t)(c.head_stride * esz),
                                    (cuuint64_t)(c.page_stride * esz)};
-    const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? c.D : 64), (cuuint32_t)rows, 1u, 1u};
+    const cuuint32_t box[4] = {(cuuint32_t)(!e4m3 ? 64 : c.D < 128 ? c.D : 128), (cuuint32_t)rows, 1u, 1u};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     const CUresult r = fn(&m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : c.dtype == MFD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
@@ -945,7 +945,7 @@ int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, in
   if ((rc = current_device_info(&d)) != MFD_OK) return rc;
   if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
   CUtensorMap mk, mv;
-  const int rows = mfd::attention_box_rows(1 << cv.ps_shift, cv.D);
+  const int rows = mfd::attention_box_rows(1 << cv.ps_shift);
   if ((rc = kv_map(cv.k, cv, rows, &mk)) != MFD_OK || (rc = kv_map(cv.v, cv, rows, &mv)) != MFD_OK) return rc;
   mfd::AttentionLaunch A;
   A.map_k = &mk;
