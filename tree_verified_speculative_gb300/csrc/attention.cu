@@ -86,18 +86,11 @@ struct Shape {
   static constexpr int RST = E4M3_ ? (DP == 64 ? 6 : 4) : 0;
   static constexpr int THREADS = 128 * (2 + NS);
   static constexpr int HELP_WARP = 4 + 4 * NS;
-  // Registers a thread: at launch, and after the warpgroups have shared them
-  // out anew; the shares together are what the launch has (64K, 63K).
-  static constexpr int REGS = NS == 2 ? 128 : 168;
-  static constexpr int REGS_LOAD = NS == 2 ? 48 : 104;
-  static constexpr int REGS_HELP = NS == 2 ? 80 : 168;
-  static constexpr int REGS_SOFTMAX = NS == 2 ? 192 : 232;
-  static_assert(REGS_LOAD + REGS_HELP + NS * REGS_SOFTMAX == (2 + NS) * REGS, "a larger sum would wait forever");
   static constexpr int TM_S = 0;                       // two S accumulators; P over them
   static constexpr int TM_O = 2 * BN;
   static constexpr int POWERS = E4M3_ ? 2 * 4 * BN * 2 : 0;  // [k, v][tile mod 4][position], 16 bits
-  static constexpr int BARS = 3 * ST + 2 * (RST ? RST : 1) + 8 + 2 * SEG_RING;
-  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + POWERS + MAX_N / 8 + BARS * 8 + SEG_RING * 40 + 32;
+  static constexpr int BARS = (E4M3_ ? 2 : 3) * ST + 2 * RST + 8 + 8 + 2 * SEG_RING;
+  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + POWERS + MAX_N / 8 + BARS * 8 + SEG_RING * 40 + 48;
 };
 
 // ------------------------------------------------------------------ line of work
@@ -170,21 +163,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-template <int R>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 // One lane of the warp; the branch it guards runs in uniform registers, which
 // is where the MMA takes its operands from.
 __device__ __forceinline__ bool elect_one() {
@@ -291,6 +278,11 @@ __device__ __forceinline__ constexpr uint32_t idesc_16<__half>(int M, int N, boo
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -331,67 +323,58 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
   return ((w & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
 }
 
-// E4M3 to the operand type.  power(code): a 16-bit number that scales a row's
-// values as widen4 takes them, NaN for a row that reads back as NaN; `wide`
-// says that 2^e has no such number and widen4_wide is to be used.
+// E4M3 to the operand type.  A row's power is a 16-bit number that scales its
+// values as widen4 takes them (NaN where the row reads back as NaN); `wide`
+// says that the power has no such number and widen4_wide is to be used.  Four
+// columns c0 .. c3 of a 32-bit word come out as (c1, c3), (c0, c2), which needs
+// no byte permutation: the queries are put in the same order, and the output's
+// columns are taken back from it.  The byte's exponent and mantissa bits are
+// moved to the type's places, subnormals included, which reads as the value
+// times 2^-120 in bf16 (biases 7 and 127) and 2^-8 in fp16 (7 and 15); one
+// multiplication by a power of two puts both right.
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+__device__ __forceinline__ uint32_t bits_of(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 template <typename T>
 struct Widen;
-// bf16: the byte's exponent and mantissa bits moved to bf16's places read as
-// the value times 2^-120 (biases 7 and 127), subnormals included; one exact
-// multiplication by 2^(e + 120) puts both right.
 template <>
 struct Widen<__nv_bfloat16> {
-  static constexpr uint16_t NONE = 0x7FFF;
   static __device__ __forceinline__ uint16_t power(int code, bool &wide) {
-    if (code == EXP_NAN) return NONE;
+    if (code == EXP_NAN) return 0x7FFF;
     wide |= code > 134;
     return (uint16_t)((code > 134 ? 254 : code + 120) << 7);
   }
-  static __device__ __forceinline__ __nv_bfloat162 moved(uint32_t x, uint32_t pick) {
-    const uint32_t y = __byte_perm(x, 0, pick);
-    const uint32_t z = (y & 0x80008000u) | ((y >> 4) & 0x07F007F0u);
-    return *reinterpret_cast<const __nv_bfloat162 *>(&z);
-  }
   static __device__ __forceinline__ uint2 widen4(uint32_t x, uint32_t power2) {
-    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&power2);
-    const __nv_bfloat162 a = __hmul2(moved(x, 0x1404), f), b = __hmul2(moved(x, 0x3424), f);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    const uint32_t hi = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+    const uint32_t lo = ((x * 256u) & 0x80008000u) | ((x * 16u) & 0x07F007F0u);
+    return make_uint2(bits_of(__hmul2(as_bf162(hi), as_bf162(power2))), bits_of(__hmul2(as_bf162(lo), as_bf162(power2))));
   }
-  // power2 = 2^127 here; the rest, 2^(e - 7), in a second multiplication
+  // 2^(e + 120) in two multiplications
   static __device__ __forceinline__ uint2 widen4_wide(uint32_t x, int code) {
-    const uint32_t w = (uint32_t)(code > 134 ? 254 : code + 120) << 7, r = (uint32_t)(code > 134 ? code - 7 : 127) << 7;
-    uint2 o = widen4(x, w | (w << 16));
-    const uint32_t rr = r | (r << 16);
-    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&rr);
-    const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o.x), f),
-                         b = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o.y), f);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    const uint32_t rest = (uint32_t)(code - 7) << 7;
+    const uint2 o = widen4(x, 0x7F007F00u);
+    const __nv_bfloat162 f = as_bf162(rest | (rest << 16));
+    return make_uint2(bits_of(__hmul2(as_bf162(o.x), f)), bits_of(__hmul2(as_bf162(o.y), f)));
   }
 };
-// fp16: E4M3 converts exactly; the power has a number from 2^-24 to 2^15.
 template <>
 struct Widen<__half> {
-  static constexpr uint16_t NONE = 0x7FFF;
+  // 2^(e + 8) from 2^-24 (code 95) to 2^15; nothing of a row with code 0 is left in fp16
   static __device__ __forceinline__ uint16_t power(int code, bool &wide) {
-    if (code == EXP_NAN) return NONE;
-    wide |= code < 103 || code > 142;
-    return code < 103 ? 1 : code < 113 ? (uint16_t)(1u << (code - 103)) : code > 142 ? 0x7800 : (uint16_t)((code - 112) << 10);
-  }
-  static __device__ __forceinline__ uint32_t two(uint32_t bytes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)bytes, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    if (code == EXP_NAN) return 0x7FFF;
+    wide |= (code > 0 && code < 95) || code > 134;
+    return code == 0 ? 0 : code < 95 ? 1 : code < 105 ? (uint16_t)(1u << (code - 95)) : code > 134 ? 0x7800 : (uint16_t)((code - 104) << 10);
   }
   static __device__ __forceinline__ uint2 widen4(uint32_t x, uint32_t power2) {
-    const __half2 f = *reinterpret_cast<const __half2 *>(&power2);
-    const uint32_t lo = two(x & 0xFFFFu), hi = two(x >> 16);
-    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f),
-                  b = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    const uint32_t hi = (x & 0x80008000u) | ((x >> 1) & 0x3F803F80u);
+    const uint32_t lo = ((x * 256u) & 0x80008000u) | ((x * 128u) & 0x3F803F80u);
+    return make_uint2(bits_of(__hmul2(as_half2(hi), as_half2(power2))), bits_of(__hmul2(as_half2(lo), as_half2(power2))));
   }
   static __device__ __forceinline__ uint2 widen4_wide(uint32_t x, int code) {
     const float s = e4m3_scale(code);
     const float2 a = e4m3x2_float(x & 0xFFFFu), b = e4m3x2_float(x >> 16);
-    return make_uint2(pack2<__half>(a.x * s, a.y * s), pack2<__half>(b.x * s, b.y * s));
+    return make_uint2(pack2<__half>(a.y * s, b.y * s), pack2<__half>(a.x * s, b.x * s));
   }
 };
 
@@ -425,12 +408,27 @@ struct Segment {
 // so that either every role gets an entry or none does.
 constexpr unsigned long long SEG_LIMIT_NS = 4 * kWaitLimitNs;
 
-__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+// A waiting warp is put to sleep for up to a microsecond at a time: a dozen
+// waiting warps that poll take the issue slots of those that work.
+__device__ __forceinline__ bool try_wait_sleep(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase with `parity`; false when the limit passes or *abort is set.
+__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
+                                           volatile int *abort) {
+  if (try_wait_sleep(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 0 && globaltimer() - t0 > limit_ns) return false;
+  for (;;) {
+    if (try_wait_sleep(bar, parity)) return true;
+    if (*abort || globaltimer() - t0 > limit_ns) return false;
   }
 }
 
@@ -485,7 +483,8 @@ struct Scheduler {
       }
   }
   // by one lane
-  __device__ __forceinline__ void emit(const Params &p, Segment *ring, uint64_t *seg_full, uint64_t *seg_empty) {
+  __device__ __forceinline__ void emit(const Params &p, Segment *ring, uint64_t *seg_full, uint64_t *seg_empty,
+                                       volatile int *never) {
     uint32_t n = 0;
     int q = q0, h = 0, pair = 0, z = 0, ctx = 0, nn = 0;
     if (x < x1) {
@@ -503,7 +502,7 @@ struct Scheduler {
     }
     for (bool more = true; more; ++n) {
       const int st = n % SEG_RING;
-      if (!wait_limit(&seg_empty[st], ((n / SEG_RING) & 1u) ^ 1u, 2 * kWaitLimitNs)) {
+      if (!wait_limit(&seg_empty[st], ((n / SEG_RING) & 1u) ^ 1u, 2 * kWaitLimitNs, never)) {
         report(p.status, MFD_ERR_TIMEOUT);
         return;
       }
@@ -570,8 +569,8 @@ __device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, in
 
 // One E4M3 unit (128 positions x UC columns, columns from c0 of the head) to
 // the swizzled operand, by 128 threads: a thread's chunks of 16 columns are at
-// one column, 128 / (UC / 16) positions apart.  All chunks are loaded before
-// the first is converted.
+// one column, 128 / (UC / 16) positions apart.  Two chunks at a time in a
+// rolled loop (see the softmax).
 template <typename T, int DP>
 __device__ __forceinline__ void widen_unit(const Params &p, const uint8_t *src, uint8_t *dst, const uint16_t *power,
                                            int ht, int c0) {
@@ -580,29 +579,35 @@ __device__ __forceinline__ void widen_unit(const Params &p, const uint8_t *src, 
   const int wide = min(p.cv.D, UC);
   const int ch = ht % C, tok0 = ht / C;
   const bool have = c0 + ch * 16 < p.cv.D;
-  const int c2 = (ch & 3) * 2;
-  // lanes of neighbouring blocks write their two chunks in opposite order (other banks)
-  const int sw = (ch >> 2) & 1;
-  uint4 x[K];
-  uint32_t pw[K];
+  // Which half of its chunk a lane reads and writes first: neighbouring blocks'
+  // lanes, and neighbouring positions', take opposite halves (other banks).
+  const int sw = UC == 128 ? ((ch >> 2) ^ tok0) & 1 : 0;
+  const uint8_t *at = src + tok0 * wide + (have ? ch * 16 : 0) + 8 * sw;
+  const int flip = 8 - 16 * sw;
+  // PER is a multiple of 8: the swizzle is the same for all of a thread's rows
+  uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok0 * 128;
+  const int o1 = (((ch & 3) * 2 + sw) ^ (tok0 & 7)) << 4, o2 = (((ch & 3) * 2 + 1 - sw) ^ (tok0 & 7)) << 4;
+  power += tok0;
+#pragma unroll 1
+  for (int k = 0; k < K; k += 2) {
+    uint2 x[2], y[2];
+    uint32_t pp[2];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    pw[k] = power[tok0 + k * PER];
-    x[k] = *reinterpret_cast<const uint4 *>(src + (tok0 + k * PER) * wide + (have ? ch * 16 : 0));
-  }
+    for (int e = 0; e < 2; ++e) {
+      pp[e] = have ? power[e * PER] * 0x10001u : 0u;  // 0: no row or column, whatever the (finite) bytes are
+      x[e] = *reinterpret_cast<const uint2 *>(at + e * PER * wide);
+      y[e] = *reinterpret_cast<const uint2 *>(at + e * PER * wide + flip);
+    }
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int tok = tok0 + k * PER;
-    // power 0: no row, whatever the bytes are
-    const uint32_t keep = have && pw[k] ? 0xFFFFFFFFu : 0u, pp = pw[k] * 0x10001u;
-    const uint2 a = Widen<T>::widen4(x[k].x & keep, pp), b = Widen<T>::widen4(x[k].y & keep, pp),
-                c = Widen<T>::widen4(x[k].z & keep, pp), d = Widen<T>::widen4(x[k].w & keep, pp);
-    uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok * 128;
-    const int x7 = tok & 7;
-    *reinterpret_cast<uint4 *>(row + (((c2 + sw) ^ x7) << 4)) =
-        make_uint4(sw ? c.x : a.x, sw ? c.y : a.y, sw ? d.x : b.x, sw ? d.y : b.y);
-    *reinterpret_cast<uint4 *>(row + (((c2 + 1 - sw) ^ x7) << 4)) =
-        make_uint4(sw ? a.x : c.x, sw ? a.y : c.y, sw ? b.x : d.x, sw ? b.y : d.y);
+    for (int e = 0; e < 2; ++e) {
+      const uint2 a = Widen<T>::widen4(x[e].x, pp[e]), b = Widen<T>::widen4(x[e].y, pp[e]);
+      *reinterpret_cast<uint4 *>(row + e * PER * 128 + o1) = make_uint4(a.x, a.y, b.x, b.y);
+      const uint2 c = Widen<T>::widen4(y[e].x, pp[e]), d = Widen<T>::widen4(y[e].y, pp[e]);
+      *reinterpret_cast<uint4 *>(row + e * PER * 128 + o2) = make_uint4(c.x, c.y, d.x, d.y);
+    }
+    at += 2 * PER * wide;
+    row += 2 * PER * 128;
+    power += 2 * PER;
   }
 }
 
@@ -652,15 +657,17 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   uint32_t *bad = reinterpret_cast<uint32_t *>(sC + SH::POWERS / 2);  // nodes with values taken out
   uint64_t *full = reinterpret_cast<uint64_t *>(bad + MAX_N / 32);
   uint64_t *empty = full + ST;
-  uint64_t *special = empty + ST;  // a unit the helpers go over before it is full
-  uint64_t *raw_full = special + ST;
-  uint64_t *raw_empty = raw_full + RN;
-  uint64_t *s_full = raw_empty + RN;
+  uint64_t *special = empty + ST;  // a unit the helpers go over before it is full (not E4M3)
+  uint64_t *raw_full = special + (E4M3 ? 0 : ST);
+  uint64_t *raw_empty = raw_full + RST;
+  uint64_t *s_full = raw_empty + RST;
   uint64_t *p_full = s_full + 2;
   uint64_t *pv_done = p_full + 2;
   uint64_t *q_full = pv_done + 2;
   uint64_t *drain = q_full + 1;
-  uint64_t *seg_full = drain + 1;
+  uint64_t *pow_full = drain + 1;
+  uint64_t *pow_empty = pow_full + 4;
+  uint64_t *seg_full = pow_empty + 4;
   uint64_t *seg_empty = seg_full + SEG_RING;
   Segment *seg_ring = reinterpret_cast<Segment *>(seg_empty + SEG_RING);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(seg_ring + SEG_RING);
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   volatile int *never = abort_flag + 1;
   volatile int *seg_done = never + 1;  // segments a softmax warpgroup has left [2]
   volatile int *any_bad = seg_done + 2;
-  uint32_t *wide_s = reinterpret_cast<uint32_t *>(const_cast<int *>(any_bad) + 1);  // E4M3: tiles with a power that has no number
+  volatile int *wide_s = any_bad + 1;  // E4M3: a tile with a power that has no number (1 keys, 2 values) [4]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CacheView &cv = p.cv;
@@ -683,7 +690,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], E4M3 ? 4 : 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&special[i], 1);
+      if (!E4M3) mbar_init(&special[i], 1);
     }
     for (int i = 0; i < RST; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -696,7 +703,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
     for (int i = 0; i < SEG_RING; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 6 + 4 * NS);
+      mbar_init(&seg_empty[i], (E4M3 ? 7 : 6) + 4 * NS);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&pow_full[i], 1);
+      mbar_init(&pow_empty[i], 4);
     }
     mbar_init(q_full, 4 * NS);
     mbar_init(drain, 1);
@@ -704,7 +715,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     *never = 0;
     seg_done[0] = seg_done[1] = 0;
     *any_bad = 0;
-    *wide_s = 0;
     fence_mbar_init();
     prefetch_tmap(&map_k);
     prefetch_tmap(&map_v);
@@ -726,7 +736,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   // goes on through its list without waiting or touching anything.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!ok) return;
-    if (!mbar_wait(bar, parity, abort_flag)) {
+    if (!wait_limit(bar, parity, kWaitLimitNs, abort_flag)) {
       if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
       *abort_flag = 1;
       ok = false;
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   // The next entry; `arrive`: the thread that says it has been read.
   auto next_segment = [&](bool arrive) {
     const int st = seg_n % SEG_RING;
-    if (!wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS)) return false;
+    if (!wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS, never)) return false;
     s = seg_ring[st];
     ++seg_n;
     if (!arrive) return s.q >= 0;
@@ -745,13 +755,29 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   // The same for a warp.
   auto next_segment_warp = [&]() {
     const int st = seg_n % SEG_RING;
-    const bool got = wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS);
+    const bool got = wait_limit(&seg_full[st], (seg_n / SEG_RING) & 1u, SEG_LIMIT_NS, never);
     if (!__all_sync(0xffffffffu, got)) return false;
     s = seg_ring[st];
     ++seg_n;
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[st]);
     return s.q >= 0;
+  };
+  // The noted nodes serve a segment until its rows are out: waits until the
+  // softmax warpgroups have left `seg` segments.
+  auto wait_rows_out = [&](int seg) {
+    if (!ok) return;
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+      if (seg_done[0] >= seg && (NS == 1 || seg_done[1] >= seg)) return;
+      if ((it & 15u) == 0 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
+        if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+        return;
+      }
+      __nanosleep(64);
+    }
   };
   // The order in which a segment's tiles pass the ring: keys and values of
   // tile j as K0 V0 K1 V1 .. when both streams read every tile, K0 K1 V0 K2 V1 ..
@@ -765,7 +791,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   };
 
   if (warp < 4) {
-    regs_down<SH::REGS_LOAD>();
     if (warp == 0) {
       // ------------------------------------------------------- loads
       // Keys and values of one token serve M rows of this CTA only, or of
@@ -908,12 +933,77 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       }
       __syncwarp();
     } else if (warp == 2) {
-      if (lane == 0) sched.emit(p, seg_ring, seg_full, seg_empty);
+      if (lane == 0) sched.emit(p, seg_ring, seg_full, seg_empty, never);
       __syncwarp();
+    } else if (E4M3) {
+      // ------------------------------------------------------- powers
+      // The exponent bytes of every tile's positions, four a lane, as powers
+      // for the helpers; pages are looked up one tile ahead.
+      uint32_t n = 0;
+      int seg = 0;
+      while (next_segment_warp()) {
+        const int nt = s.t1 - s.t0;
+        if (nt == 0) continue;
+        const int len = s.ctx + s.nn;
+        const bool note = p.N > 1;  // else every key before the end is seen
+        bool clean = false;
+        const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
+        auto page_at = [&](int t) { return t < min(len, s.t1 * BN) ? __ldg(table + (t >> cv.ps_shift)) : -1; };
+        int page[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) page[i] = page_at(s.t0 * BN + 32 * i + lane);
+        for (int j = 0; j < nt; ++j, ++n) {
+          const int base = (s.t0 + j) * BN, slot = n & 3;
+          int ck[4], cw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = base + 32 * i + lane;
+            ck[i] = cw[i] = -1;
+            if (page[i] >= 0 && page[i] < cv.n_pages) {
+              const int64_t e = (((int64_t)page[i] * cv.Hk + s.h) << cv.ps_shift) + (t & ((1 << cv.ps_shift) - 1));
+              ck[i] = __ldg(cv.k_exp + e);
+              cw[i] = __ldg(cv.v_exp + e);
+            }
+            page[i] = page_at(t + BN);
+          }
+          if (note && base + BN > s.ctx && !clean) {
+            wait_rows_out(seg);
+            for (int k = lane; k < MAX_N / 32; k += 32) bad[k] = 0;
+            if (lane == 0) *any_bad = 0;
+            __syncwarp();
+            clean = true;
+          }
+          wait(&pow_empty[slot], ((n >> 2) & 1u) ^ 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          bool wk = false, wv = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = base + 32 * i + lane;
+            const uint16_t pk = ck[i] < 0 ? 0 : Widen<T>::power(ck[i], wk);
+            uint16_t pv = cw[i] < 0 ? 0 : Widen<T>::power(cw[i], wv);
+            if (cw[i] == EXP_NAN && note && t >= s.ctx) {
+              // a NaN that some rows do not see: out of the product, added back later
+              pv = 0;
+              atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
+              *any_bad = 1;
+            }
+            if (ok) {
+              sC[slot * BN + 32 * i + lane] = pk;
+              sC[4 * BN + slot * BN + 32 * i + lane] = pv;
+            }
+          }
+          const int w = (__any_sync(0xffffffffu, wk) ? 1 : 0) | (__any_sync(0xffffffffu, wv) ? 2 : 0);
+          if (lane == 0 && ok) {
+            wide_s[slot] = w;
+            mbar_arrive(&pow_full[slot]);
+          }
+          __syncwarp();
+        }
+        ++seg;
+      }
     }
   } else if (warp < SH::HELP_WARP) {
     // --------------------------------------------------------- softmax
-    regs_up<SH::REGS_SOFTMAX>();
     const int ws = NS == 2 ? (warp - 4) >> 2 : 0;  // stream
     const int wq = warp & 3;                       // the warp's lanes of tensor memory
     const int r = wq * 32 + lane;
@@ -942,13 +1032,42 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int ch = r % C;
         const uint32_t dst = smem_u32(sQ + rt * SH::Q_TILE) + (ch >> 3) * (BM * 128);
         const uint16_t *src = p.q + (int64_t)s.q * p.N * p.q_stride + (int64_t)s.h * p.G * cv.D + ch * 8;
-        if (ch * 8 < cv.D)
-#pragma unroll 2
-          for (int i = r / C; i < have; i += STEP) {
-            const int rr = base_row + i;
-            const int n1 = (row0 + rr) / p.G, g1 = row0 + rr - n1 * p.G;
-            cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), src + n1 * p.q_stride + g1 * cv.D);
+        if (ch * 8 < cv.D && r / C < have) {
+          int i = r / C;
+          int n1 = (row0 + base_row + i) / p.G, g1 = row0 + base_row + i - n1 * p.G;
+          const int dn = STEP / p.G, dg = STEP - dn * p.G;
+#pragma unroll 1
+          for (; i < have; i += 4 * STEP) {
+            uint4 x[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int rr = base_row + i + b * STEP;
+              const uint16_t *at = src + n1 * p.q_stride + g1 * cv.D;
+              if (i + b * STEP < have) {
+                if (E4M3)
+                  x[b] = __ldg(reinterpret_cast<const uint4 *>(at));
+                else
+                  cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), at);
+              }
+              n1 += dn;
+              g1 += dg;
+              if (g1 >= p.G) {
+                g1 -= p.G;
+                ++n1;
+              }
+            }
+            if (E4M3) {  // in the widened keys' order
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const int rr = base_row + i + b * STEP;
+                if (i + b * STEP < have)
+                  st_shared16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                              make_uint4(__byte_perm(x[b].x, x[b].y, 0x7632), __byte_perm(x[b].x, x[b].y, 0x5410),
+                                         __byte_perm(x[b].z, x[b].w, 0x7632), __byte_perm(x[b].z, x[b].w, 0x5410)));
+              }
+            }
           }
+        }
       }
       // rows past n_nodes, once per item
       if (s.head) {
@@ -987,22 +1106,34 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         if (ok && warp_live) {
           tc_fence_after();
           const uint32_t sa = lane_base + SH::TM_S + (uint32_t)slot * BN;
-          uint32_t xr[BN];
+          // Both passes read the scores from tensor memory, 32 columns at a time
+          // in a rolled loop: 128 in registers took unrolled code for all of
+          // them, and the warps then waited for instructions (3.5 cycles an
+          // issue) more than for anything else.
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int part = 0; part < BN / 32; ++part) {
+            uint32_t x[32];
+            tmem_ld32(sa + 32 * part, x);
+            tmem_wait_ld();
+            tie32(x);
+            if (edge) {
+              const uint32_t w = part == 0 ? vis[0] : part == 1 ? vis[1] : part == 2 ? vis[2] : vis[3];
 #pragma unroll
-          for (int k = 0; k < BN / 32; ++k) tmem_ld32(sa + 32 * k, xr + 32 * k);
-          tmem_wait_ld();
+              for (int k = 0; k < 32; ++k) x[k] = (w >> k) & 1u ? x[k] : 0xFF800000u;
+              tmem_st16(sa + 32 * part, x);
+              tmem_st16(sa + 32 * part + 16, x + 16);
+            }
+            float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
-          for (int k = 0; k < BN / 32; ++k) tie32(xr + 32 * k);
-          if (edge) {
-#pragma unroll
-            for (int k = 0; k < BN; ++k) xr[k] = (vis[k >> 5] >> (k & 31)) & 1u ? xr[k] : 0xFF800000u;
+            for (int k = 2; k < 32; k += 4) {
+              t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+              if (k + 2 < 32) t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+            }
+            top = max3(top, t0, t1);
           }
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(xr[k]);
-#pragma unroll
-          for (int k = 4; k < BN; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(xr[k]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+          if (edge) tmem_wait_st();
+          top *= p.c;
           // move the maximum when it has grown by enough (or is the first)
           const bool move = row_live && top > m + MAX_GROWTH;
           if (__any_sync(0xffffffffu, move)) {
@@ -1028,13 +1159,15 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           const float mz = m == -INFINITY ? 0.f : m;
           const uint64_t cc = pair(p.c, p.c), mm = pair(-mz, -mz);
           uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
-#pragma unroll
+#pragma unroll 1
           for (int part = 0; part < BN / 32; ++part) {
-            uint32_t pk[16];
+            uint32_t x[32], pk[16];
+            tmem_ld32(sa + 32 * part, x);
+            tmem_wait_ld();
+            tie32(x);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const int e = 32 * part + 2 * k;
-              const float2 y = unpair(fma2(pair(__uint_as_float(xr[e]), __uint_as_float(xr[e + 1])), cc, mm));
+              const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, mm));
               const float a = ex2(y.x), b = ex2(y.y);
               if (k & 1)
                 sum1 = add2(sum1, pair(a, b));
@@ -1091,8 +1224,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int64_t at = row_live ? ((int64_t)s.q * p.N + node) * p.Hq + s.h * p.G + g : 0;
         const int part = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
         const bool fix = p.N > 1 && s.t1 * BN > s.ctx && *any_bad;
-        uint16_t *out = p.out + at * cv.D;
         float4 *po = p.part_o + (int64_t)part * (cv.D / 4) * p.part_rows + rt * BM + r;
+        uint16_t *out = p.out + at * cv.D;
 #pragma unroll 1
         for (int d = 0; d < cv.D; d += 16) {
           uint32_t o[16], o1[16];
@@ -1101,24 +1234,25 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           tmem_wait_ld();
           tie16(o);
           float f[16];
+          // E4M3: columns 4 i .. 4 i + 3 were widened in the order 1, 3, 0, 2
+          constexpr int FROM[4] = {E4M3 ? 2 : 0, E4M3 ? 0 : 1, E4M3 ? 3 : 2, E4M3 ? 1 : 3};
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[k]) * a0;
+          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[(k & ~3) + FROM[k & 3]]) * a0;
           if (two) {
             tie16(o1);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(o1[k]), a1, f[k]);
+            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(o1[(k & ~3) + FROM[k & 3]]), a1, f[k]);
           }
-          if (fix && row_live) add_back<T, E4M3>(p, s.q, s.h, s.ctx, max(0, s.t0 * BN - s.ctx), min(s.nn, s.t1 * BN - s.ctx), node, mask_row,
+          if (fix && row_live)
+            add_back<T, E4M3>(p, s.q, s.h, s.ctx, max(0, s.t0 * BN - s.ctx), min(s.nn, s.t1 * BN - s.ctx), node, mask_row,
                               bad, d, f);
           if (row_live) {
             if (whole) {
-              float y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = f[e];
-              *reinterpret_cast<uint4 *>(out + d) = pack8<T>(y);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = f[8 + e];
-              *reinterpret_cast<uint4 *>(out + d + 8) = pack8<T>(y);
+              for (int k = 0; k < 16; k += 8)
+                *reinterpret_cast<uint4 *>(out + d + k) =
+                    make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
+                               pack2<T>(f[k + 6], f[k + 7]));
             } else {
 #pragma unroll
               for (int k = 0; k < 16; k += 4)
@@ -1149,10 +1283,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
   } else {
     // --------------------------------------------------------- helpers
-    if (SH::REGS_HELP < SH::REGS) regs_down<SH::REGS_HELP>();
     const int ht = tid - SH::HELP_WARP * 32;
     uint32_t st = 0, par = 0, rs = 0, rpar = 0;  // places in the rings and their phases
-    uint32_t special_par = 0;
+    uint32_t special_par = 0, pow_n = 0;
     int seg = 0;
     while (next_segment_warp()) {
       const int nt = s.t1 - s.t0;
@@ -1162,73 +1295,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       // one row per request: every key before the end is seen
       const bool note = p.N > 1;
       bool clean = false;  // the bad-node bits are this segment's
-      // The bits serve the previous segment until its rows are out.
-      auto clear_bad = [&]() {
-        if (ok) {
-          const unsigned long long t0 = globaltimer();
-          for (uint32_t it = 1;; ++it) {
-            if (seg_done[0] >= seg && (NS == 1 || seg_done[1] >= seg)) break;
-            if ((it & 15u) == 0 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
-              if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-            __nanosleep(64);
-          }
-        }
-        named_sync(4, 128);
-        for (int k = ht; k < MAX_N / 32; k += 128) bad[k] = 0;
-        if (ht == 0) *any_bad = 0;
-        named_sync(4, 128);
-      };
-      // E4M3: a position's two exponent bytes, by the thread of that position:
-      // its page is looked up four tiles ahead, the bytes loaded three ahead
-      // and written as powers two ahead.
-      const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
-      auto page_at = [&](int j) {
-        const int t = (s.t0 + j) * BN + ht;
-        return j < nt && t < len ? __ldg(table + (t >> cv.ps_shift)) : -1;
-      };
-      auto codes = [&](int j, int page, int &ck, int &cvv) {
-        const int t = (s.t0 + j) * BN + ht;
-        ck = cvv = -1;
-        if (page >= 0 && page < cv.n_pages) {
-          const int64_t e = (((int64_t)page * cv.Hk + s.h) << cv.ps_shift) + (t & ((1 << cv.ps_shift) - 1));
-          ck = __ldg(cv.k_exp + e);
-          cvv = __ldg(cv.v_exp + e);
-        }
-      };
-      auto put_codes = [&](int j, int ck, int cvv) {
-        const int t = (s.t0 + j) * BN + ht;
-        bool wk = false, wv = false;
-        uint16_t pk = ck < 0 ? 0 : Widen<T>::power(ck, wk), pv = cvv < 0 ? 0 : Widen<T>::power(cvv, wv);
-        if (cvv == EXP_NAN && note && t >= s.ctx) {
-          // a NaN that some rows do not see: out of the product, added back later
-          pv = 0;
-          atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
-          *any_bad = 1;
-        }
-        sC[(j & 3) * BN + ht] = pk;
-        sC[4 * BN + (j & 3) * BN + ht] = pv;
-        if (wk) atomicOr(wide_s, 1u << (j & 7));
-        if (wv) atomicOr(wide_s, 256u << (j & 7));
-      };
-      int ck = -1, cvv = -1, pg = -1;
-      if (E4M3) {
-        if (note && s.t1 * BN > s.ctx) clear_bad();
-        named_sync(4, 128);  // every helper is done with the last segment's powers
-        if (ht == 0) *wide_s = 0;
-        const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
-        pg = page_at(3);
-        int ck0, cv0, ck1, cv1;
-        codes(0, p0, ck0, cv0);
-        codes(1, p1, ck1, cv1);
-        codes(2, p2, ck, cvv);
-        named_sync(4, 128);
-        put_codes(0, ck0, cv0);
-        put_codes(1, ck1, cv1);
-      }
       for (int i = 0; i < 2 * nt; ++i) {
         const int o = order(nt, shared, i);
         const bool is_v = o < 0;
@@ -1236,16 +1302,15 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int base = (s.t0 + j) * BN;
         const bool sp = is_v && base + BN > s.ctx;
         if (!E4M3 && sp && note && !clean) {
-          clear_bad();
+          wait_rows_out(seg);
+          named_sync(4, 128);
+          for (int k = ht; k < MAX_N / 32; k += 128) bad[k] = 0;
+          if (ht == 0) *any_bad = 0;
+          named_sync(4, 128);
           clean = true;
         }
-        if (E4M3 && !is_v) {
-          if (ht == 0) atomicAnd(wide_s, ~(0x101u << ((j + 4) & 7)));
-          named_sync(4, 128);  // this tile's powers are written; the slot of tile j - 2 is free
-          put_codes(j + 2, ck, cvv);
-          codes(j + 3, pg, ck, cvv);
-          pg = page_at(j + 4);
-        }
+        const uint32_t pn = pow_n + j;
+        if (E4M3 && !is_v) wait(&pow_full[pn & 3], (pn >> 2) & 1u);
 #pragma unroll 1
         for (int u = 0; u < NU; ++u) {
           if (E4M3) {
@@ -1253,10 +1318,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             wait(&raw_full[rs], rpar);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
-              const bool slow = (*static_cast<volatile uint32_t *>(wide_s) >> ((j & 7) + (is_v ? 8 : 0))) & 1u;
-              widen_unit<T, DP>(p, sR + rs * SH::RAW, sT + st * SH::STAGE, sC + (is_v ? 4 * BN : 0) + (j & 3) * BN, ht,
+              widen_unit<T, DP>(p, sR + rs * SH::RAW, sT + st * SH::STAGE, sC + (is_v ? 4 * BN : 0) + (pn & 3) * BN, ht,
                                 u * SH::UC);
-              if (slow)
+              if ((wide_s[pn & 3] >> (is_v ? 1 : 0)) & 1)
                 widen_unit_wide<T, DP>(p, s.q, s.h, len, sR + rs * SH::RAW, sT + st * SH::STAGE, base, is_v, ht, u * SH::UC);
             }
             fence_async_smem();
@@ -1264,6 +1328,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             if (lane == 0 && ok) {
               mbar_arrive(&raw_empty[rs]);
               mbar_arrive(&full[st]);
+              if (is_v && u == NU - 1) mbar_arrive(&pow_empty[pn & 3]);
             }
             if (++rs == RN) {
               rs = 0;
@@ -1311,6 +1376,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         }
       }
       ++seg;
+      pow_n += nt;
     }
   }
   tc_fence_before();
@@ -1458,9 +1524,6 @@ cudaError_t launch_shape(const AttentionLaunch &A, const Params &p, int n_cta, c
     if ((e = cudaFuncSetAttribute(attention_kernel<T, DP, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM)) !=
         cudaSuccess)
       return e;
-    cudaFuncAttributes a;
-    if ((e = cudaFuncGetAttributes(&a, attention_kernel<T, DP, E4M3>)) != cudaSuccess) return e;
-    if (a.numRegs != SH::REGS) return cudaErrorInvalidConfiguration;  // the shares would not add up
     if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   }
   attention_kernel<T, DP, E4M3><<<n_cta, SH::THREADS, SH::SMEM, stream>>>(*A.map_k, *A.map_v, p);
