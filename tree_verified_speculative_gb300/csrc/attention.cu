@@ -84,8 +84,10 @@ struct Shape {
   static constexpr int RAW = BN * UC;                  // an E4M3 unit as it is in the cache
   static constexpr int ST = E4M3_ ? (DP == 64 ? 4 : 3) : (DP == 64 ? 8 : 5);
   static constexpr int RST = E4M3_ ? (DP == 64 ? 6 : 4) : 0;
-  static constexpr int THREADS = 128 * (2 + NS);
+  static constexpr int HELPERS = E4M3_ ? 2 : 1;        // warpgroups that help
+  static constexpr int THREADS = 128 * (1 + NS + HELPERS);
   static constexpr int HELP_WARP = 4 + 4 * NS;
+  static constexpr int SW = 32;                        // score columns a softmax thread holds
   static constexpr int TM_S = 0;                       // two S accumulators; P over them
   static constexpr int TM_O = 2 * BN;
   static constexpr int POWERS = E4M3_ ? 2 * 4 * BN * 2 : 0;  // [k, v][tile mod 4][position], 16 bits
@@ -126,15 +128,90 @@ __device__ __forceinline__ Item item_of(const Params &p, int ctx, int nn, int pa
   return it;
 }
 
+// A key head's length on the line where it has one form for all of its items
+// (a tree mask, or one item): by one thread.
 template <int NS>
 __device__ __forceinline__ int64_t head_cost(const Params &p, int ctx, int nn) {
-  if (p.mask) {
-    const int live = nn * p.G;
-    return (int64_t)((live + BM - 1) / BM) * (nn ? (ctx + nn + BN - 1) / BN : 0) + p.n_pair;
+  if (p.n_pair == 1) return item_of<NS>(p, ctx, nn, 0).cost;
+  const int live = nn * p.G;
+  return (int64_t)((live + BM - 1) / BM) * (nn ? (ctx + nn + BN - 1) / BN : 0) + p.n_pair;
+}
+__device__ __forceinline__ bool one_form(const Params &p) { return p.mask || p.n_pair == 1; }
+__device__ __forceinline__ int64_t warp_total(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t warp_running(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
   }
+  return v;
+}
+// The same for any item lengths, by a warp, an item a lane at a time.
+template <int NS>
+__device__ __forceinline__ int64_t head_cost_warp(const Params &p, int ctx, int nn, int lane) {
+  if (one_form(p)) return head_cost<NS>(p, ctx, nn);
   int64_t c = 0;
-  for (int i = 0; i < p.n_pair; ++i) c += item_of<NS>(p, ctx, nn, i).cost;
-  return c;
+  for (int i = lane; i < p.n_pair; i += 32) c += item_of<NS>(p, ctx, nn, i).cost;
+  return warp_total(c);
+}
+// The line's length (all requests), by a warp; with `x` also the request whose
+// stretch holds place x and where that stretch starts.
+template <int NS>
+__device__ __forceinline__ int64_t line_walk(const Params &p, int lane, int64_t x, bool report_bad, int &q, int64_t &start) {
+  int64_t total = 0;
+  q = 0;
+  start = 0;
+  for (int b = 0; b < p.n_req; b += one_form(p) ? 32 : 1) {
+    int ctx, nn;
+    int64_t own = 0;
+    if (one_form(p)) {
+      if (b + lane < p.n_req) {
+        if (!lengths(p, b + lane, ctx, nn) && report_bad) report(p.status, MFD_ERR_INPUT);
+        own = p.cv.Hk * head_cost<NS>(p, ctx, nn);
+      }
+      if (x >= 0) {
+        const int64_t run = total + warp_running(own, lane), lo = run - own;
+        const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && lo <= x && x < run);
+        if (hit) {
+          q = b + __ffs(hit) - 1;
+          start = __shfl_sync(0xffffffffu, lo, __ffs(hit) - 1);
+        }
+        total = __shfl_sync(0xffffffffu, run, 31);
+      } else {
+        total += warp_total(own);
+      }
+    } else {
+      if (!lengths(p, b, ctx, nn) && report_bad && lane == 0) report(p.status, MFD_ERR_INPUT);
+      own = p.cv.Hk * head_cost_warp<NS>(p, ctx, nn, lane);
+      if (x >= total && x < total + own) {
+        q = b;
+        start = total;
+      }
+      total += own;
+    }
+  }
+  return total;
+}
+// The item of a head at `rest` places from the head's start, by a warp; `rest`
+// becomes the place inside the item.
+template <int NS>
+__device__ __forceinline__ int find_item(const Params &p, int ctx, int nn, int lane, int64_t &rest) {
+  for (int b = 0; b < p.n_pair; b += 32) {
+    const int64_t own = b + lane < p.n_pair ? item_of<NS>(p, ctx, nn, b + lane).cost : 0;
+    const int64_t run = warp_running(own, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && rest < run);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      rest -= __shfl_sync(0xffffffffu, run - own, l);
+      return b + l;
+    }
+    rest -= __shfl_sync(0xffffffffu, run, 31);
+  }
+  return 0;  // not reached: rest lies inside the head
 }
 
 // Where the line's place x falls: CTA c of n has [C c / n, C (c + 1) / n).
@@ -151,13 +228,16 @@ __device__ __forceinline__ int tile_at(const Item &it, int z) {
 
 // ------------------------------------------------------------------ primitives
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar,
-                                            uint64_t policy) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
       : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // 16 bytes global -> shared without a register; cp_async_wait waits for all of the thread's.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -165,6 +245,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_global16(void *dst, uint4 v) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -432,110 +515,90 @@ __device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsig
   }
 }
 
+// The order in which a segment's tiles pass the ring: keys and values as K0 V0
+// K1 V1 .. when both streams read every tile, K0 K1 V0 K2 V1 .. when they take
+// turns (a stream's scores are then two tiles ahead).  Step i of 2 n.
+struct Turn {
+  bool is_v;
+  int j;  // tile
+};
+__device__ __forceinline__ Turn turn_at(bool turns, int n, int i) {
+  if (!turns || n == 1) return {(i & 1) != 0, i >> 1};
+  if (i == 0) return {false, 0};
+  if (i == 2 * n - 1) return {true, n - 1};
+  return {(i & 1) == 0, (i & 1) ? (i + 1) >> 1 : (i - 2) >> 1};
+}
+
 // The CTA's stretch of the line, entry by entry, by one warp: the requests'
-// costs are summed by its lanes, the entries written by its first.
+// costs are summed by its lanes.
 template <int NS>
 struct Scheduler {
-  int64_t x, x1, into;
-  int q0;
+  int64_t x, x1;
+  int q, h, pair, z, ctx, nn;
+  uint32_t n;  // entries written
+  bool ended;
 
   __device__ __forceinline__ void start(const Params &p, int lane) {
-    int64_t total = 0;
-    for (int b = 0; b < p.n_req; b += 32) {
-      int ctx, nn;
-      int64_t c = 0;
-      if (b + lane < p.n_req) {
-        if (!lengths(p, b + lane, ctx, nn) && blockIdx.x == 0) report(p.status, MFD_ERR_INPUT);
-        c = p.cv.Hk * head_cost<NS>(p, ctx, nn);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-      total += c;
-    }
+    int64_t begin;
+    const int64_t total = line_walk<NS>(p, lane, -1, blockIdx.x == 0, q, begin);
     x = border(total, blockIdx.x, gridDim.x);
     x1 = border(total, blockIdx.x + 1, gridDim.x);
-    q0 = 0;
-    into = 0;
-    int64_t before = 0;
-    if (x < x1)
-      for (int b = 0; b < p.n_req; b += 32) {
-        int ctx, nn;
-        int64_t own = 0;
-        if (b + lane < p.n_req) {
-          lengths(p, b + lane, ctx, nn);
-          own = p.cv.Hk * head_cost<NS>(p, ctx, nn);
-        }
-        int64_t run = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += up;
-        }
-        const int64_t lo = before + run - own;
-        const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && lo <= x && x < lo + own);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          q0 = b + l;
-          into = x - __shfl_sync(0xffffffffu, lo, l);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, run, 31);
-      }
+    h = pair = z = ctx = nn = 0;
+    n = 0;
+    ended = false;
+    if (x >= x1) return;
+    line_walk<NS>(p, lane, x, false, q, begin);
+    lengths(p, q, ctx, nn);
+    const int64_t hc = head_cost_warp<NS>(p, ctx, nn, lane);
+    h = (int)divide(x - begin, hc);
+    int64_t rest = x - begin - h * hc;
+    pair = find_item<NS>(p, ctx, nn, lane, rest);
+    z = (int)rest;
   }
-  // by one lane
-  __device__ __forceinline__ void emit(const Params &p, Segment *ring, uint64_t *seg_full, uint64_t *seg_empty,
-                                       volatile int *never) {
-    uint32_t n = 0;
-    int q = q0, h = 0, pair = 0, z = 0, ctx = 0, nn = 0;
-    if (x < x1) {
-      lengths(p, q, ctx, nn);
-      const int64_t hc = head_cost<NS>(p, ctx, nn);
-      h = (int)divide(into, hc);
-      int64_t rest = into - h * hc;
-      for (;;) {
-        const int c = item_of<NS>(p, ctx, nn, pair).cost;
-        if (rest < c) break;
-        rest -= c;
-        ++pair;
-      }
-      z = (int)rest;
+  // The next entry, to the ring and to the caller; false at the end.
+  __device__ __forceinline__ bool next(const Params &p, Segment &s, int lane, Segment *ring, uint64_t *seg_full,
+                                       uint64_t *seg_empty, volatile int *never) {
+    if (ended) return false;
+    const int st = n % SEG_RING;
+    const bool room = wait_limit(&seg_empty[st], ((n / SEG_RING) & 1u) ^ 1u, 2 * kWaitLimitNs, never);
+    if (!__all_sync(0xffffffffu, room)) {  // never again: the others' waits run out together
+      if (lane == 0) report(p.status, MFD_ERR_TIMEOUT);
+      ended = true;
+      return false;
     }
-    for (bool more = true; more; ++n) {
-      const int st = n % SEG_RING;
-      if (!wait_limit(&seg_empty[st], ((n / SEG_RING) & 1u) ^ 1u, 2 * kWaitLimitNs, never)) {
-        report(p.status, MFD_ERR_TIMEOUT);
-        return;
-      }
-      Segment s;
-      s.q = -1;
-      more = x < x1;
-      if (more) {
-        const Item it = item_of<NS>(p, ctx, nn, pair);
-        const int64_t left = x1 - x;
-        const int end = left < it.cost - z ? z + (int)left : it.cost;
-        s.q = q;
-        s.h = h;
-        s.pair = pair;
-        s.ctx = ctx;
-        s.nn = nn;
-        s.active = it.active;
-        s.tiles = it.tiles;
-        s.t0 = tile_at(it, z);
-        s.t1 = tile_at(it, end);
-        s.head = z == 0;
-        x += end - z;
-        z = 0;
-        if (end == it.cost && ++pair == p.n_pair) {
-          pair = 0;
-          if (++h == p.cv.Hk) {
-            h = 0;
-            if (++q < p.n_req) lengths(p, q, ctx, nn);
-          }
+    ++n;
+    s.q = -1;
+    ended = x >= x1;
+    if (!ended) {
+      const Item it = item_of<NS>(p, ctx, nn, pair);
+      const int64_t left = x1 - x;
+      const int end = left < it.cost - z ? z + (int)left : it.cost;
+      s.q = q;
+      s.h = h;
+      s.pair = pair;
+      s.ctx = ctx;
+      s.nn = nn;
+      s.active = it.active;
+      s.tiles = it.tiles;
+      s.t0 = tile_at(it, z);
+      s.t1 = tile_at(it, end);
+      s.head = z == 0;
+      x += end - z;
+      z = 0;
+      if (end == it.cost && ++pair == p.n_pair) {
+        pair = 0;
+        if (++h == p.cv.Hk) {
+          h = 0;
+          if (++q < p.n_req) lengths(p, q, ctx, nn);
         }
       }
+    }
+    if (lane == 0) {
       ring[st] = s;
       mbar_arrive(&seg_full[st]);
     }
+    __syncwarp();
+    return !ended;
   }
 };
 
@@ -544,7 +607,7 @@ struct Scheduler {
 // (all NaN where an E4M3 row reads back as NaN), columns d .. d + 15.
 template <typename T, bool E4M3>
 __device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, int lo, int hi, int node,
-                                      const uint32_t *mask_row, const uint32_t *bad, int d, float (&f)[16]) {
+                                      const uint32_t *mask_row, const uint32_t *bad, int d, uint32_t (&f)[16]) {
   const CacheView &cv = p.cv;
   for (int j = lo; j < hi; ++j) {
     if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
@@ -558,10 +621,10 @@ __device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, in
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       if (E4M3) {
-        f[k] = __int_as_float(0x7FFFFFFF);
+        f[k] = 0x7FFFFFFFu;
       } else {
         const uint32_t w = static_cast<const uint16_t *>(cv.v)[e + d + k];
-        if (nonfinite2<T>(w)) f[k] += unpack2<T>(w).x;
+        if (nonfinite2<T>(w)) f[k] = __float_as_uint(__uint_as_float(f[k]) + unpack2<T>(w).x);
       }
     }
   }
@@ -703,11 +766,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
     for (int i = 0; i < SEG_RING; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], (E4M3 ? 7 : 6) + 4 * NS);
+      mbar_init(&seg_empty[i], 3 + 4 * (NS + SH::HELPERS));
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&pow_full[i], 1);
-      mbar_init(&pow_empty[i], 4);
+      mbar_init(&pow_empty[i], 8 * NU);  // four warps for each of a tile's units
     }
     mbar_init(q_full, 4 * NS);
     mbar_init(drain, 1);
@@ -779,83 +842,98 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       __nanosleep(64);
     }
   };
-  // The order in which a segment's tiles pass the ring: keys and values of
-  // tile j as K0 V0 K1 V1 .. when both streams read every tile, K0 K1 V0 K2 V1 ..
-  // when they take turns (a stream's scores are then two tiles ahead).  Step i
-  // of 2 n: returns the tile, negative (-1 - tile) for values.
-  auto order = [](int n, bool shared, int i) {
-    if (shared || n == 1) return (i & 1) ? -1 - (i >> 1) : i >> 1;
-    if (i == 0) return 0;
-    if (i == 2 * n - 1) return -1 - (n - 1);
-    return (i & 1) ? (i + 1) >> 1 : -1 - ((i - 2) >> 1);
-  };
-
   if (warp < 4) {
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
       // ------------------------------------------------------- loads
+      // Warp 0 the keys, warp 3 the values: one warp for both took longer over
+      // a tile (its pages, waits and copies, about 1.6 us a unit of small pages)
+      // than the rest of the SM.
+      const bool is_v = warp == 3;
+      const CUtensorMap *map = is_v ? &map_v : &map_k;
       // Keys and values of one token serve M rows of this CTA only, or of
       // neighbours too when there are more row tiles: then they stay in L2.
       const uint64_t policy = p.n_pair > 1 ? policy_evict_normal() : policy_evict_first();
-      const int ps = 1 << cv.ps_shift;
-      const int rows = ps < BN ? ps : BN;  // of a box
-      uint32_t st = 0, par = 0;            // ring place and its phase
+      const int row_shift = min(cv.ps_shift, 7), rows = 1 << row_shift;  // of a box
+      const uint32_t wide = E4M3 ? (uint32_t)min(cv.D, SH::UC) : 128u;   // bytes of a row in the unit
+      constexpr uint32_t RING = E4M3 ? RN : ST, UNIT = E4M3 ? SH::RAW : SH::STAGE;
+      const uint32_t ring = smem_u32(E4M3 ? sR : sT), ready = smem_u32(E4M3 ? raw_full : full);
+      uint64_t *freed = E4M3 ? raw_empty : empty;
+      uint32_t st = 0, par = 0;  // ring place and its phase
       uint32_t special_par = 0, issued = 0, issued_special = 0, issued_par = 0;
       while (next_segment_warp()) {
         const int nt = s.t1 - s.t0;
-        const bool shared = s.active == 2;
+        const bool turns = s.active != 2;
         const int len = s.ctx + s.nn;
         const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
-        for (int i = 0; i < 2 * nt; ++i) {
-          const int o = order(nt, shared, i);
-          const bool is_v = o < 0;
-          const int base = (s.t0 + (is_v ? -1 - o : o)) * BN;
-          // boxes with positions before the end
-          const int some = (min(len - base, BN) + rows - 1) / rows;
+        // a lane's box of tile j; its page is looked up a tile ahead
+        auto page_at = [&](int j) {
+          const int t = (s.t0 + j) * BN + (lane << row_shift);
           int page = 0;
-          if (lane < some) {
-            page = __ldg(table + ((base + lane * rows) >> cv.ps_shift));
-            if (page < 0 || page >= cv.n_pages) {
+          if (j < nt && (lane << row_shift) < BN && t < len) {
+            page = __ldg(table + (t >> cv.ps_shift));
+            if ((unsigned)page >= (unsigned)cv.n_pages) {
               report(p.status, MFD_ERR_INPUT);
               page = cv.n_pages;  // outside the map: reads as zeros
             }
           }
-          const int slot = (base + lane * rows) & (ps - 1);
-          const CUtensorMap *map = is_v ? &map_v : &map_k;
+          return page;
+        };
+        int page_next = page_at(0);
+        for (int i = 0; i < 2 * nt; ++i) {
+          const Turn tn = turn_at(turns, nt, i);
+          if (tn.is_v != is_v) {
+            // the other warp's, but waited for in its turn: a wait for a later
+            // phase of the same place would take this one's parity for its own
+            for (int u = 0; u < NU; ++u) {
+              wait(&freed[st], par ^ 1u);
+              if (++st == RING) {
+                st = 0;
+                par ^= 1u;
+              }
+            }
+            continue;
+          }
+          const int j = tn.j;
+          const int base = (s.t0 + j) * BN;
+          const int page = page_next;
+          page_next = page_at(j + 1);
+          const int some = (min(len - base, BN) + rows - 1) >> row_shift;  // boxes with positions before the end
+          const int slot = base & ((1 << cv.ps_shift) - 1);  // of the first box; boxes of smaller pages start at 0
+          const bool sp = !E4M3 && is_v && base + BN > s.ctx;
 #pragma unroll 1
           for (int u = 0; u < NU; ++u) {
-            const bool sp = !E4M3 && is_v && base + BN > s.ctx;
-            uint64_t *bar = E4M3 ? &raw_full[st] : sp ? &special[st] : &full[st];
-            const int wide = E4M3 ? min(cv.D, SH::UC) : 128 * NB;
-            wait(E4M3 ? &raw_empty[st] : &empty[st], par ^ 1u);
-            if (__all_sync(0xffffffffu, ok)) {
-              if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * rows * wide));
-              __syncwarp();
-              if (lane < some) {
-                if (E4M3) {
-                  tma_load_4d(sR + st * SH::RAW + lane * rows * wide, map, u * SH::UC, slot, s.h, page, bar, policy);
-                } else {
-#pragma unroll
-                  for (int b = 0; b < NB; ++b)
-                    tma_load_4d(sT + st * SH::STAGE + b * (BN * 128) + lane * rows * 128, map, u * SH::UC + b * 64, slot,
-                                s.h, page, bar, policy);
+            wait(&freed[st], par ^ 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              const uint32_t bar = sp ? smem_u32(&special[st]) : ready + st * 8;
+              uint32_t dst = ring + st * UNIT;
+              const bool one = elect_one();
+              if (one) expect_bytes(bar, (uint32_t)some * rows * wide * (E4M3 ? 1 : NB));
+              for (int b = 0; b < some; ++b, dst += rows * wide) {
+                const int pg = __shfl_sync(0xffffffffu, page, b);
+                if (one) {
+                  tma_load_4d(dst, map, u * SH::UC, slot, s.h, pg, bar, policy);
+                  if (!E4M3 && NB == 2) tma_load_4d(dst + BN * 128, map, u * SH::UC + 64, slot, s.h, pg, bar, policy);
                 }
               }
-              issued |= 1u << st;
-              const uint32_t bp = sp ? (special_par >> st) & 1u : par;
-              issued_par = (issued_par & ~(1u << st)) | (bp << st);
-              issued_special = (issued_special & ~(1u << st)) | ((sp ? 1u : 0u) << st);
-              if (sp) special_par ^= 1u << st;
+              const uint32_t bit = 1u << st;
+              issued |= bit;
+              issued_par = (sp ? (special_par & bit) != 0 : par != 0) ? issued_par | bit : issued_par & ~bit;
+              issued_special = sp ? issued_special | bit : issued_special & ~bit;
+              if (sp) special_par ^= bit;
             }
-            if (++st == (E4M3 ? RN : ST)) {
+            if (++st == RING) {
               st = 0;
               par ^= 1u;
             }
           }
         }
       }
-      // every load issued lands before the CTA may exit
-      if (lane == 0)
-        for (uint32_t i = 0; i < (E4M3 ? RN : ST); ++i)
+      // Every load issued lands before the CTA may exit.  All have been consumed
+      // unless a wait ran out; a place that the other warp has filled since holds
+      // this warp's load no more, and its wait then runs out too.
+      if (!ok && lane == 0)
+        for (uint32_t i = 0; i < RING; ++i)
           if ((issued >> i) & 1u)
             mbar_wait(E4M3 ? &raw_full[i] : ((issued_special >> i) & 1u) ? &special[i] : &full[i],
                       (issued_par >> i) & 1u, never);
@@ -933,17 +1011,14 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       }
       __syncwarp();
     } else if (warp == 2) {
-      if (lane == 0) sched.emit(p, seg_ring, seg_full, seg_empty, never);
-      __syncwarp();
-    } else if (E4M3) {
-      // ------------------------------------------------------- powers
-      // The exponent bytes of every tile's positions, four a lane, as powers
+      // ------------------------------------------------- list of work
+      // E4M3: also the exponent bytes of every tile's positions, four a lane, as powers
       // for the helpers; pages are looked up one tile ahead.
       uint32_t n = 0;
       int seg = 0;
-      while (next_segment_warp()) {
+      while (sched.next(p, s, lane, seg_ring, seg_full, seg_empty, never)) {
         const int nt = s.t1 - s.t0;
-        if (nt == 0) continue;
+        if (!E4M3 || nt == 0) continue;
         const int len = s.ctx + s.nn;
         const bool note = p.N > 1;  // else every key before the end is seen
         bool clean = false;
@@ -1110,27 +1185,32 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           // in a rolled loop: 128 in registers took unrolled code for all of
           // them, and the warps then waited for instructions (3.5 cycles an
           // issue) more than for anything else.
+          constexpr int SW = SH::SW;
           float top = -INFINITY;
 #pragma unroll 1
-          for (int part = 0; part < BN / 32; ++part) {
-            uint32_t x[32];
-            tmem_ld32(sa + 32 * part, x);
+          for (int part = 0; part < BN / SW; ++part) {
+            uint32_t x[SW];
+#pragma unroll
+            for (int k = 0; k < SW; k += 32) tmem_ld32(sa + SW * part + k, x + k);
             tmem_wait_ld();
-            tie32(x);
+#pragma unroll
+            for (int k = 0; k < SW; k += 32) tie32(x + k);
             if (edge) {
-              const uint32_t w = part == 0 ? vis[0] : part == 1 ? vis[1] : part == 2 ? vis[2] : vis[3];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = (w >> k) & 1u ? x[k] : 0xFF800000u;
-              tmem_st16(sa + 32 * part, x);
-              tmem_st16(sa + 32 * part + 16, x + 16);
-            }
-            float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
+              for (int c = 0; c < SW; c += 32) {
+                const int i = part * (SW / 32) + c / 32;
+                const uint32_t w = i == 0 ? vis[0] : i == 1 ? vis[1] : i == 2 ? vis[2] : vis[3];
 #pragma unroll
-            for (int k = 2; k < 32; k += 4) {
-              t0 = max3(t0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-              if (k + 2 < 32) t1 = max3(t1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                for (int k = 0; k < 32; ++k) x[c + k] = (w >> k) & 1u ? x[c + k] : 0xFF800000u;
+                tmem_st16(sa + SW * part + c, x + c);
+                tmem_st16(sa + SW * part + c + 16, x + c + 16);
+              }
             }
-            top = max3(top, t0, t1);
+            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < SW; k += 2)
+              t[(k >> 1) & 3] = max3(t[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            top = max3(max3(t[0], t[1], t[2]), t[3], top);
           }
           if (edge) tmem_wait_st();
           top *= p.c;
@@ -1160,22 +1240,29 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           const uint64_t cc = pair(p.c, p.c), mm = pair(-mz, -mz);
           uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-          for (int part = 0; part < BN / 32; ++part) {
-            uint32_t x[32], pk[16];
-            tmem_ld32(sa + 32 * part, x);
-            tmem_wait_ld();
-            tie32(x);
+          for (int part = 0; part < BN / SW; ++part) {
+            uint32_t x[SW];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 y = unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), cc, mm));
-              const float a = ex2(y.x), b = ex2(y.y);
-              if (k & 1)
-                sum1 = add2(sum1, pair(a, b));
-              else
-                sum0 = add2(sum0, pair(a, b));
-              pk[k] = pack2<T>(a, b);
+            for (int k = 0; k < SW; k += 32) tmem_ld32(sa + SW * part + k, x + k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < SW; k += 32) tie32(x + k);
+#pragma unroll
+            for (int c = 0; c < SW; c += 32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 y =
+                    unpair(fma2(pair(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), cc, mm));
+                const float a = ex2(y.x), b = ex2(y.y);
+                if (k & 1)
+                  sum1 = add2(sum1, pair(a, b));
+                else
+                  sum0 = add2(sum0, pair(a, b));
+                pk[k] = pack2<T>(a, b);
+              }
+              tmem_st16(sa + (SW * part + c) / 2, pk);
             }
-            tmem_st16(sa + 16 * part, pk);
           }
           const float2 sum = unpair(add2(sum0, sum1));
           l += sum.x + sum.y;
@@ -1225,38 +1312,50 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int part = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
         const bool fix = p.N > 1 && s.t1 * BN > s.ctx && *any_bad;
         float4 *po = p.part_o + (int64_t)part * (cv.D / 4) * p.part_rows + rt * BM + r;
-        uint16_t *out = p.out + at * cv.D;
+        // a row's place: 16 columns are 32 bytes of the output, or 4 of its
+        // part's float4, each the rows' length from the next
+        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out + at * cv.D) : reinterpret_cast<uint8_t *>(po);
+        const int64_t hop = (int64_t)p.part_rows * 16;
 #pragma unroll 1
         for (int d = 0; d < cv.D; d += 16) {
-          uint32_t o[16], o1[16];
+          uint32_t o[16];
           tmem_ld16(o_base + d, o);
-          if (two) tmem_ld16(o_base + DP + d, o1);
-          tmem_wait_ld();
-          tie16(o);
-          float f[16];
-          // E4M3: columns 4 i .. 4 i + 3 were widened in the order 1, 3, 0, 2
-          constexpr int FROM[4] = {E4M3 ? 2 : 0, E4M3 ? 0 : 1, E4M3 ? 3 : 2, E4M3 ? 1 : 3};
-#pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(o[(k & ~3) + FROM[k & 3]]) * a0;
           if (two) {
+            uint32_t o1[16];
+            tmem_ld16(o_base + DP + d, o1);
+            tmem_wait_ld();
+            tie16(o);
             tie16(o1);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(o1[(k & ~3) + FROM[k & 3]]), a1, f[k]);
+            for (int k = 0; k < 16; ++k)
+              o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), a1, __uint_as_float(o[k]) * a0));
+          } else {
+            tmem_wait_ld();
+            tie16(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a0);
           }
           if (fix && row_live)
             add_back<T, E4M3>(p, s.q, s.h, s.ctx, max(0, s.t0 * BN - s.ctx), min(s.nn, s.t1 * BN - s.ctx), node, mask_row,
-                              bad, d, f);
+                              bad, d, o);
+          // E4M3: columns 4 i .. 4 i + 3 were widened in the order 1, 3, 0, 2
+          auto f = [&](int k) {
+            constexpr int FROM[4] = {E4M3 ? 2 : 0, E4M3 ? 0 : 1, E4M3 ? 3 : 2, E4M3 ? 1 : 3};
+            return __uint_as_float(o[(k & ~3) + FROM[k & 3]]);
+          };
           if (row_live) {
             if (whole) {
-#pragma unroll
-              for (int k = 0; k < 16; k += 8)
-                *reinterpret_cast<uint4 *>(out + d + k) =
-                    make_uint4(pack2<T>(f[k], f[k + 1]), pack2<T>(f[k + 2], f[k + 3]), pack2<T>(f[k + 4], f[k + 5]),
-                               pack2<T>(f[k + 6], f[k + 7]));
+              st_global16(dst, make_uint4(pack2<T>(f(0), f(1)), pack2<T>(f(2), f(3)), pack2<T>(f(4), f(5)), pack2<T>(f(6), f(7))));
+              st_global16(dst + 16,
+                          make_uint4(pack2<T>(f(8), f(9)), pack2<T>(f(10), f(11)), pack2<T>(f(12), f(13)), pack2<T>(f(14), f(15))));
+              dst += 32;
             } else {
 #pragma unroll
-              for (int k = 0; k < 16; k += 4)
-                po[(int64_t)((d + k) >> 2) * p.part_rows] = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+              for (int k = 0; k < 16; k += 4) {
+                st_global16(dst, make_uint4(__float_as_uint(f(k)), __float_as_uint(f(k + 1)), __float_as_uint(f(k + 2)),
+                                            __float_as_uint(f(k + 3))));
+                dst += hop;
+              }
             }
           }
         }
@@ -1283,22 +1382,25 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
   } else {
     // --------------------------------------------------------- helpers
-    const int ht = tid - SH::HELP_WARP * 32;
+    // E4M3: the two warpgroups take the units in turn
+    const int ht = (tid - SH::HELP_WARP * 32) & 127, hg = (tid - SH::HELP_WARP * 32) >> 7;
+    uint32_t unit = 0;
     uint32_t st = 0, par = 0, rs = 0, rpar = 0;  // places in the rings and their phases
     uint32_t special_par = 0, pow_n = 0;
     int seg = 0;
     while (next_segment_warp()) {
       const int nt = s.t1 - s.t0;
       if (nt == 0) continue;
-      const bool shared = s.active == 2;
+      const bool turns = s.active != 2;
       const int len = s.ctx + s.nn;
       // one row per request: every key before the end is seen
       const bool note = p.N > 1;
       bool clean = false;  // the bad-node bits are this segment's
+      // bf16 and fp16: only value tiles that reach past the context
       for (int i = 0; i < 2 * nt; ++i) {
-        const int o = order(nt, shared, i);
-        const bool is_v = o < 0;
-        const int j = is_v ? -1 - o : o;
+        const Turn tn = turn_at(turns, nt, i);
+        const bool is_v = tn.is_v;
+        const int j = tn.j;
         const int base = (s.t0 + j) * BN;
         const bool sp = is_v && base + BN > s.ctx;
         if (!E4M3 && sp && note && !clean) {
@@ -1310,10 +1412,15 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           clean = true;
         }
         const uint32_t pn = pow_n + j;
-        if (E4M3 && !is_v) wait(&pow_full[pn & 3], (pn >> 2) & 1u);
 #pragma unroll 1
         for (int u = 0; u < NU; ++u) {
-          if (E4M3) {
+          if (E4M3 && (int)(unit++ & 1u) != hg) {
+            if (++rs == RN) {
+              rs = 0;
+              rpar ^= 1u;
+            }
+          } else if (E4M3) {
+            wait(&pow_full[pn & 3], (pn >> 2) & 1u);
             wait(&empty[st], par ^ 1u);
             wait(&raw_full[rs], rpar);
             ok = __all_sync(0xffffffffu, ok);
@@ -1328,7 +1435,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             if (lane == 0 && ok) {
               mbar_arrive(&raw_empty[rs]);
               mbar_arrive(&full[st]);
-              if (is_v && u == NU - 1) mbar_arrive(&pow_empty[pn & 3]);
+              mbar_arrive(&pow_empty[pn & 3]);
             }
             if (++rs == RN) {
               rs = 0;
@@ -1395,55 +1502,48 @@ constexpr int JOIN_ROWS = 16;
 // thread for each row and 8 columns adds the parts up in their order.
 template <typename T, int NS>
 __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p, int n_cta) {
-  __shared__ int64_t sums[3];  // the line's length, the request's start on it, the request
+  __shared__ int64_t at_s[3];  // the line's length, the item's start and end
+  __shared__ int where_s[4];   // request, head, item, whether this block joins it
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
   __shared__ int slot_s[ATTENTION_MAX_CTAS];
-  __shared__ int64_t cost_s[1024];
   const int tid = threadIdx.x, lane = tid & 31, threads = JOIN_ROWS * (p.cv.D / 8);
-  for (int i = tid; i < p.n_req; i += threads) {
-    int ctx, nn;
-    lengths(p, i, ctx, nn);
-    cost_s[i] = p.cv.Hk * head_cost<NS>(p, ctx, nn);
-  }
-  block_sync();
   const int c = (int)blockIdx.x + 1;
   if (tid < 32) {
-    int64_t total = 0;
-    for (int i = lane; i < p.n_req; i += 32) total += cost_s[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int q, ctx, nn;
+    int64_t begin;
+    const int64_t total = line_walk<NS>(p, lane, -1, false, q, begin);
     const int64_t x = border(total, c, n_cta);
+    line_walk<NS>(p, lane, x, false, q, begin);
+    lengths(p, q, ctx, nn);
+    const int64_t hc = head_cost_warp<NS>(p, ctx, nn, lane);
+    const int h = (int)divide(x - begin, hc);
+    int64_t rest = x - begin - h * hc;
+    const int pr = find_item<NS>(p, ctx, nn, lane, rest);
+    const Item it = item_of<NS>(p, ctx, nn, pr);
+    const int64_t u0 = x - rest;
     if (lane == 0) {
-      sums[0] = total;
-      int64_t before = 0;
-      int q = 0;
-      while (q < p.n_req - 1 && before + cost_s[q] <= x) before += cost_s[q++];
-      sums[1] = before;
-      sums[2] = q;
+      at_s[0] = total;
+      at_s[1] = u0;
+      at_s[2] = u0 + it.cost;
+      where_s[0] = q;
+      where_s[1] = h;
+      where_s[2] = pr;
+      // cut here, and not before
+      where_s[3] = rest > 0 && border(total, c - 1, n_cta) <= u0 && it.tiles > 0;
     }
   }
   block_sync();
-  const int64_t total = sums[0], x = border(total, c, n_cta);
-  const int q = (int)sums[2];
-  int ctx, nn;
-  lengths(p, q, ctx, nn);
-  const int64_t hc = head_cost<NS>(p, ctx, nn);
-  const int h = (int)divide(x - sums[1], hc);
-  int64_t u0 = sums[1] + h * hc;
-  int pr = 0;
-  Item it;
-  for (;; ++pr) {
-    it = item_of<NS>(p, ctx, nn, pr);
-    if (x < u0 + it.cost) break;
-    u0 += it.cost;
-  }
-  const int64_t u1 = u0 + it.cost;
+  const int64_t total = at_s[0], u0 = at_s[1], u1 = at_s[2];
   // Every block waits for the parts, also those with nothing to join: this grid
   // must not end before the one it follows.
-  if (x == u0 || border(total, c - 1, n_cta) > u0 || it.tiles == 0) {  // not cut here, or another block's
+  if (!where_s[3]) {
     pdl_wait();
     return;
   }
+  const int q = where_s[0], h = where_s[1], pr = where_s[2];
+  int ctx, nn;
+  lengths(p, q, ctx, nn);
+  const Item it = item_of<NS>(p, ctx, nn, pr);
   const int first = pr * NS * BM;
   const int rows = min(nn * p.G - first, NS * BM);
   const int row0 = (int)blockIdx.y * JOIN_ROWS;
