@@ -325,7 +325,7 @@ int mfd_verify(const float *target_logits, int n_req, int B, int V, int L,
  * (N = 1), or a stretch of a prompt.  Row n of request q sits at cache
  * position ctx_len[q] + n; its rotation position is pos[q][n], which for a
  * tree is the one mfd_build_tree emits.  n_nodes[q] <= N rows are live (NULL:
- * all N); the others are neither read nor cached.
+ * all N); what the others hold does not matter, and they are not cached.
  *
  * Element types.  Queries and outputs are bf16 or fp16.  A cache holds the
  * same type, or E4M3 with one power of two per (position, head) row of D

@@ -504,15 +504,63 @@ __device__ __forceinline__ bool try_wait_sleep(uint64_t *bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase with `parity`; false when the limit passes or *abort is set.
-__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
-                                           volatile int *abort) {
-  if (try_wait_sleep(bar, parity)) return true;
+// Waits for the phase with `parity`; false when the limit passes or *abort is
+// set.  Out of line, like all that is not taken for every tile: the roles' hot
+// code shares an instruction cache that is small for it.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, volatile int *abort) {
   const unsigned long long t0 = globaltimer();
   for (;;) {
     if (try_wait_sleep(bar, parity)) return true;
     if (*abort || globaltimer() - t0 > limit_ns) return false;
   }
+}
+__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
+                                           volatile int *abort) {
+  return try_wait_sleep(bar, parity) || wait_long(bar, parity, limit_ns, abort);
+}
+// A pipeline wait that ran out, or was told to stop.
+__device__ __noinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+  if (wait_long(bar, parity, kWaitLimitNs, abort_flag)) return true;
+  if (!*abort_flag) report(status, MFD_ERR_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+
+// Scores of a warp's rows that a tile past the context hides, to -infinity, in
+// tensor memory: 32 columns per word of `vis`.
+__device__ __noinline__ void hide_scores(uint32_t sa, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+#pragma unroll 1
+  for (int part = 0; part < 8; ++part) {
+    const uint32_t w = (part < 2 ? v0 : part < 4 ? v1 : part < 6 ? v2 : v3) >> (16 * (part & 1));
+    uint32_t x[16];
+    tmem_ld16(sa + 16 * part, x);
+    tmem_wait_ld();
+    tie16(x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = (w >> k) & 1u ? x[k] : 0xFF800000u;
+    tmem_st16(sa + 16 * part, x);
+  }
+  tmem_wait_st();
+}
+// A warp's rows of an accumulator times each row's factor.
+__device__ __noinline__ void scale_rows(uint32_t oa, int columns, float a) {
+#pragma unroll 1
+  for (int d = 0; d < columns; d += 16) {
+    uint32_t o[16];
+    tmem_ld16(oa + d, o);
+    tmem_wait_ld();
+    tie16(o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+    tmem_st16(oa + d, o);
+  }
+}
+// Zeros and -infinity for a row that is not live.
+__device__ __noinline__ void zero_row(const Params &p, int q, int h, int row) {
+  const int n = row / p.G, g = row - n * p.G;
+  const int64_t at = ((int64_t)q * p.N + n) * p.Hq + h * p.G + g;
+  for (int d = 0; d < p.cv.D; d += 8) *reinterpret_cast<uint4 *>(p.out + at * p.cv.D + d) = make_uint4(0, 0, 0, 0);
+  if (p.lse) p.lse[at] = -INFINITY;
 }
 
 // The order in which a segment's tiles pass the ring: keys and values as K0 V0
@@ -798,12 +846,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   // A wait that ran out, or was told to stop, ends the CTA's work: every role
   // goes on through its list without waiting or touching anything.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (!ok) return;
-    if (!wait_limit(bar, parity, kWaitLimitNs, abort_flag)) {
-      if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
-      *abort_flag = 1;
-      ok = false;
-    }
+    if (ok && !try_wait_sleep(bar, parity)) ok = wait_or_abort(bar, parity, abort_flag, p.status);
   };
   // The next entry; `arrive`: the thread that says it has been read.
   auto next_segment = [&](bool arrive) {
@@ -1147,12 +1190,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       // rows past n_nodes, once per item
       if (s.head) {
         const int zrow = (s.pair * NS + ws) * BM + r;
-        if (zrow < p.M && zrow >= (s.tiles ? live : 0)) {
-          const int zn = zrow / p.G, zg = zrow - zn * p.G;
-          const int64_t at = ((int64_t)s.q * p.N + zn) * p.Hq + s.h * p.G + zg;
-          for (int d = 0; d < cv.D; d += 8) *reinterpret_cast<uint4 *>(p.out + at * cv.D + d) = make_uint4(0, 0, 0, 0);
-          if (p.lse) p.lse[at] = -INFINITY;
-        }
+        if (zrow < p.M && zrow >= (s.tiles ? live : 0))
+          zero_row(p, s.q, s.h, zrow);
       }
       if (nt == 0) continue;
       cp_async_wait();
@@ -1169,11 +1208,12 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int slot = i & 1;
         const int t_base = (s.t0 + (shared ? i >> 1 : i)) * BN;
         uint32_t vis[BN / 32];
-        const bool edge = t_base + BN > s.ctx;
-        if (edge && warp_live) {
+        bool hide = false;
+        if (t_base + BN > s.ctx && warp_live) {
 #pragma unroll
           for (int k = 0; k < BN / 32; ++k)
-            vis[k] = row_live ? visible32(mask_row, p.W32, node, s.nn, t_base + 32 * k - s.ctx) : 0u;
+            vis[k] = row_live ? visible32(mask_row, p.W32, node, s.nn, t_base + 32 * k - s.ctx) : 0xFFFFFFFFu;
+          hide = __any_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) != 0xFFFFFFFFu);
         }
         wait(&s_full[slot], (s_par >> slot) & 1u);
         s_par ^= 1u << slot;
@@ -1185,6 +1225,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           // in a rolled loop: 128 in registers took unrolled code for all of
           // them, and the warps then waited for instructions (3.5 cycles an
           // issue) more than for anything else.
+          if (hide) hide_scores(sa, vis[0], vis[1], vis[2], vis[3]);
           constexpr int SW = SH::SW;
           float top = -INFINITY;
 #pragma unroll 1
@@ -1195,24 +1236,12 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < SW; k += 32) tie32(x + k);
-            if (edge) {
-#pragma unroll
-              for (int c = 0; c < SW; c += 32) {
-                const int i = part * (SW / 32) + c / 32;
-                const uint32_t w = i == 0 ? vis[0] : i == 1 ? vis[1] : i == 2 ? vis[2] : vis[3];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[c + k] = (w >> k) & 1u ? x[c + k] : 0xFF800000u;
-                tmem_st16(sa + SW * part + c, x + c);
-                tmem_st16(sa + SW * part + c + 16, x + c + 16);
-              }
-            }
             float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < SW; k += 2)
               t[(k >> 1) & 3] = max3(t[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
             top = max3(max3(t[0], t[1], t[2]), t[3], top);
           }
-          if (edge) tmem_wait_st();
           top *= p.c;
           // move the maximum when it has grown by enough (or is the first)
           const bool move = row_live && top > m + MAX_GROWTH;
@@ -1224,16 +1253,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             if (done) {
               wait(&pv_done[ws], (pv_n - 1u) & 1u);
               tc_fence_after();
-#pragma unroll 1
-              for (int d = 0; d < DP; d += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_base + d, o);
-                tmem_wait_ld();
-                tie16(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                tmem_st16(o_base + d, o);
-              }
+              scale_rows(o_base, DP, a);
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;

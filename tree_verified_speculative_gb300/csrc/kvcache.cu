@@ -19,7 +19,7 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_D = 256;
-constexpr int UNROLL = 4;  // rows a lane has in flight
+constexpr int UNROLL = 4;  // rows a lane of the read has in flight
 
 // Page of position p of request q, or -1 (the caller reports).
 __device__ __forceinline__ int page_of(const CacheView &c, int q, int64_t p) {
@@ -60,17 +60,18 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t prod, float &c, float &s) 
 // Where the keys (and values) go.
 enum { SINK_TENSOR = 0, SINK_CACHE = 1, SINK_E4M3 = 2 };
 
-// One block handles up to WARPS * (32 / LR) * UNROLL rows (heads) of one
-// token; a row of D elements is LR lanes of 8 elements (LR: the power of two
-// at or above D / 8), so a lane keeps its place in the row, and with it its
-// cosines and sines, for all of the block's rows.  Each lane's UNROLL rows are
-// loaded before the angles are computed.
+// One block handles up to WARPS * (32 / LR) * U rows (heads) of one token; a
+// row of D elements is LR lanes of 8 elements (LR: the power of two at or above
+// D / 8), so a lane keeps its place in the row, and with it its cosines and
+// sines, for all of the block's rows.  A block is short and waits for memory
+// most of its time: everything whose address is known at the start (U rows a
+// lane, weights, phases, lengths) is loaded before anything is used.
 //
 // ROT_SMEM: halves that are not a multiple of 8 elements; a lane's partners
 // then lie in two other lanes at an offset, and the row passes through shared
 // memory.  Otherwise the partner is one lane's chunk (a shuffle) or, in the
 // interleaved form, the lane's own.
-template <typename T, int SINK, int LR, bool ROT_SMEM>
+template <typename T, int SINK, int LR, int U, bool ROT_SMEM>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   constexpr int RW = 32 / LR;  // rows of a warp at once
   __shared__ float cos_s[MAX_D / 2], sin_s[MAX_D / 2];
@@ -81,26 +82,14 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   const int q = tok / p.N, n = tok - q * p.N;
   const int rows = p.Hq + (SINK == SINK_TENSOR ? 1 : 2) * p.Hk;
   const bool in_row = c * 8 < p.D;
-  const int row0 = (int)blockIdx.y * (WARPS * RW * UNROLL) + warp * RW + sub;
+  const int row0 = (int)blockIdx.y * (WARPS * RW * U) + warp * RW + sub;
 
-  bool live = true;
-  int ctx = 0, page = -1;
-  if (SINK != SINK_TENSOR) {
-    const int nn = p.n_nodes ? __ldg(p.n_nodes + q) : p.N;
-    ctx = __ldg(p.ctx_len + q);
-    const bool ok = nn >= 0 && nn <= p.N && ctx >= 0;
-    if (!ok && threadIdx.x == 0) report(p.status, MFD_ERR_INPUT);
-    live = ok && n < nn;
-    if (live) page = page_of(p.cache, q, (int64_t)ctx + n);
-    if (live && page < 0 && threadIdx.x == 0) report(p.status, MFD_ERR_INPUT);
-  }
-
-  uint4 raw[UNROLL];
+  uint4 raw[U];
 #pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int row = row0 + u * WARPS * RW;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (live && in_row && row < rows) {
+    if (in_row && row < rows) {  // before n_nodes is known: dead rows' values are not used
       const uint8_t *src;
       if (row < p.Hq)
         src = p.q + ((int64_t)tok * p.q_stride + (int64_t)row * p.D + c * 8) * 2;
@@ -112,10 +101,26 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
     }
   }
   const int h = p.rot_dim >> 1;
-  if (live) {
-    const int64_t pos = __ldg(p.pos + tok);
-    for (int i = threadIdx.x; i < h; i += THREADS) turn_cos_sin(__ldg(p.phase + i) * (uint64_t)pos, cos_s[i], sin_s[i]);
+  const bool turns = (int)threadIdx.x < h;  // h <= THREADS
+  const uint64_t phase = turns ? __ldg(p.phase + threadIdx.x) : 0;
+  const int64_t pos = turns ? __ldg(p.pos + tok) : 0;
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (in_row) {
+    if (p.q_w) wq = __ldg(reinterpret_cast<const uint4 *>(p.q_w + c * 16));
+    if (p.k_w) wk = __ldg(reinterpret_cast<const uint4 *>(p.k_w + c * 16));
   }
+  bool live = true;
+  int ctx = 0, page = -1;
+  if (SINK != SINK_TENSOR) {
+    const int nn = p.n_nodes ? __ldg(p.n_nodes + q) : p.N;
+    ctx = __ldg(p.ctx_len + q);
+    const bool ok = nn >= 0 && nn <= p.N && ctx >= 0;
+    if (!ok && threadIdx.x == 0) report(p.status, MFD_ERR_INPUT);
+    live = ok && n < nn;
+    if (live) page = page_of(p.cache, q, (int64_t)ctx + n);
+    if (live && page < 0 && threadIdx.x == 0) report(p.status, MFD_ERR_INPUT);
+  }
+  if (turns) turn_cos_sin(phase * (uint64_t)pos, cos_s[threadIdx.x], sin_s[threadIdx.x]);
   block_sync();
   // per element: y = x * cs + partner * sn (left as it is past rot_dim)
   float cs[8], sn[8];
@@ -134,20 +139,17 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   // the lane whose chunk holds this chunk's partners (halves of whole chunks)
   const int hc = h >> 3;
   const int partner = c < hc ? lane + hc : c < 2 * hc ? lane - hc : lane;
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (live && in_row) {
-    if (p.q_w) wq = *reinterpret_cast<const uint4 *>(p.q_w + c * 16);
-    if (p.k_w) wk = *reinterpret_cast<const uint4 *>(p.k_w + c * 16);
-  }
-
 #pragma unroll
-  for (int u = 0; u < UNROLL; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int row = row0 + u * WARPS * RW;
     if (row0 - sub + u * WARPS * RW >= rows) break;  // the same for the whole warp
     const bool have = row < rows;
     const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hk;
     float x[8];
     unpack8<T>(raw[u], x);
+    if (!live)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
     // norm: rows of q and k with a weight (values and dead rows pass)
     float ss = 0.f;
 #pragma unroll
@@ -233,16 +235,23 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   }
 }
 
+template <typename T, int SINK, int LR, int U>
+cudaError_t launch_append_u(const AppendParams &p, int rows, cudaStream_t stream) {
+  const int per = WARPS * (32 / LR) * U;
+  const dim3 grid(p.T, (rows + per - 1) / per);
+  if (!p.interleaved && (p.rot_dim / 2) % 8 != 0)
+    append_kernel<T, SINK, LR, U, true><<<grid, THREADS, 0, stream>>>(p);
+  else
+    append_kernel<T, SINK, LR, U, false><<<grid, THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Rows a lane: as many as one block needs for a token, up to 6.
 template <typename T, int SINK, int LR>
 cudaError_t launch_append_lr(const AppendParams &p, cudaStream_t stream) {
   const int rows = p.Hq + (SINK == SINK_TENSOR ? 1 : 2) * p.Hk;
-  const int per = WARPS * (32 / LR) * UNROLL;
-  const dim3 grid(p.T, (rows + per - 1) / per);
-  if (!p.interleaved && (p.rot_dim / 2) % 8 != 0)
-    append_kernel<T, SINK, LR, true><<<grid, THREADS, 0, stream>>>(p);
-  else
-    append_kernel<T, SINK, LR, false><<<grid, THREADS, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int need = (rows + WARPS * (32 / LR) - 1) / (WARPS * (32 / LR));
+  return need <= 3 ? launch_append_u<T, SINK, LR, 3>(p, rows, stream) : launch_append_u<T, SINK, LR, 6>(p, rows, stream);
 }
 
 template <typename T, int SINK>
@@ -263,19 +272,19 @@ cudaError_t launch_append_t(const AppendParams &p, int sink, cudaStream_t stream
 
 // -------------------------------------------------------------------- read
 
-// One lane moves 8 elements: a row of D is LR lanes, as in the append; a
-// block moves WARPS * (32 / LR) * UNROLL rows (position, head) of one request,
-// keys (blockIdx.z = 0) or values.
+// One lane moves 16 bytes of the cache (8 elements, or 16 E4M3 ones); a row of
+// D is LR lanes of that; a block moves WARPS * (32 / LR) * UNROLL rows
+// (position, head) of one request, keys (blockIdx.z = 0) or values.
 template <typename T, bool E4M3, int LR>
 __global__ void __launch_bounds__(THREADS)
     read_kernel(const CacheView cv, int L_max, const int32_t *__restrict__ start, const int32_t *__restrict__ length,
                 uint8_t *k_out, uint8_t *v_out, int32_t *status) {
-  constexpr int RW = 32 / LR;
+  constexpr int RW = 32 / LR, EL = E4M3 ? 16 : 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & (LR - 1), sub = lane / LR;
   const int q = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  if (c * 8 >= cv.D) return;
+  if (c * EL >= cv.D) return;
   const int st = __ldg(start + q), len = __ldg(length + q);
   const bool ok = st >= 0 && len >= 0 && len <= L_max;
   if (!ok && threadIdx.x == 0) report(status, MFD_ERR_INPUT);
@@ -291,7 +300,14 @@ __global__ void __launch_bounds__(THREADS)
     raw[u] = make_uint4(0, 0, 0, 0);
     code[u] = 0;
     if (row < rows && ok) {
-      const int i = (int)(row / cv.Hk), hd = (int)(row - (int64_t)i * cv.Hk);
+      int i, hd;  // position and head
+      if (rows < (1ll << 31)) {
+        i = (int)((uint32_t)row / (uint32_t)cv.Hk);
+        hd = (int)row - i * cv.Hk;
+      } else {
+        i = (int)(row / cv.Hk);
+        hd = (int)(row - (int64_t)i * cv.Hk);
+      }
       if (i < len) {
         const int64_t pos = (int64_t)st + i;
         const int page = page_of(cv, q, pos);
@@ -299,15 +315,9 @@ __global__ void __launch_bounds__(THREADS)
           report(status, MFD_ERR_INPUT);
         } else {
           const int slot = (int)(pos & ((1 << cv.ps_shift) - 1));
-          const int64_t e = page * cv.page_stride + hd * cv.head_stride + slot * cv.token_stride + c * 8;
-          if (E4M3) {
-            const uint2 b = *reinterpret_cast<const uint2 *>(base + e);
-            raw[u].x = b.x;
-            raw[u].y = b.y;
-            code[u] = exps[(((int64_t)page * cv.Hk + hd) << cv.ps_shift) + slot];
-          } else {
-            raw[u] = *reinterpret_cast<const uint4 *>(base + e * 2);
-          }
+          const int64_t e = page * cv.page_stride + hd * cv.head_stride + slot * cv.token_stride + c * EL;
+          raw[u] = *reinterpret_cast<const uint4 *>(base + e * (E4M3 ? 1 : 2));
+          if (E4M3) code[u] = exps[(((int64_t)page * cv.Hk + hd) << cv.ps_shift) + slot];
         }
       }
     }
@@ -316,34 +326,37 @@ __global__ void __launch_bounds__(THREADS)
   for (int u = 0; u < UNROLL; ++u) {
     const int64_t row = row0 + u * WARPS * RW;
     if (row >= rows) break;
-    uint4 o = raw[u];
+    uint4 *dst = reinterpret_cast<uint4 *>((is_v ? v_out : k_out) + (((int64_t)q * rows + row) * cv.D + c * EL) * 2);
     if (E4M3) {
       const float s = e4m3_scale(code[u]);
-      float x[8];
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = e4m3x2_float((i < 2 ? raw[u].x : raw[u].y) >> (16 * (i & 1)) & 0xFFFFu);
-        x[2 * i] = f.x * s;
-        x[2 * i + 1] = f.y * s;
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = e4m3x2_float(w[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
+        o[i] = pack2<T>(f.x * s, f.y * s);
       }
-      o = pack8<T>(x);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+      *dst = raw[u];
     }
-    *reinterpret_cast<uint4 *>((is_v ? v_out : k_out) + (((int64_t)q * rows + row) * cv.D + c * 8) * 2) = o;
   }
 }
 
 template <typename T, bool E4M3>
 cudaError_t launch_read_t(const KvReadLaunch &A, cudaStream_t stream) {
-  const int LR = A.cache.D <= 64 ? 8 : A.cache.D <= 128 ? 16 : 32;
+  const int lanes = A.cache.D / (E4M3 ? 16 : 8);
+  const int LR = lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int64_t per = WARPS * (32 / LR) * UNROLL;
   const dim3 grid((unsigned)(((int64_t)A.L_max * A.cache.Hk + per - 1) / per), A.n_req, 2);
   uint8_t *ko = static_cast<uint8_t *>(A.k_out), *vo = static_cast<uint8_t *>(A.v_out);
-  if (LR == 8)
-    read_kernel<T, E4M3, 8><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status);
-  else if (LR == 16)
-    read_kernel<T, E4M3, 16><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status);
-  else
-    read_kernel<T, E4M3, 32><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status);
+  switch (LR) {
+    case 4: read_kernel<T, E4M3, 4><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status); break;
+    case 8: read_kernel<T, E4M3, 8><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status); break;
+    case 16: read_kernel<T, E4M3, 16><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status); break;
+    default: read_kernel<T, E4M3, 32><<<grid, THREADS, 0, stream>>>(A.cache, A.L_max, A.start, A.length, ko, vo, A.status); break;
+  }
   return cudaGetLastError();
 }
 
@@ -361,12 +374,13 @@ __global__ void __launch_bounds__(COMMIT_THREADS)
                   int32_t *status) {
   const int q = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ctx = ctx_len[q], acc = __ldg(accept_len + q), nn = __ldg(n_nodes + q);
-  bool ok = ctx >= 0 && acc >= 0 && acc <= L;
   // lane j checks step j and finds its entries' places
-  int src_page = -1, dst_page = -1, node = 0;
+  int src_page = -1, dst_page = -1;
+  const int node = lane <= L ? __ldg(path + (size_t)q * (L + 1) + lane) : 0;
+  const int up = __shfl_up_sync(0xffffffffu, node, 1);
+  bool ok = ctx >= 0 && acc >= 0 && acc <= L;
   if (ok && lane <= acc) {
-    node = __ldg(path + (size_t)q * (L + 1) + lane);
-    const int before = lane ? __ldg(path + (size_t)q * (L + 1) + lane - 1) : -1;
+    const int before = lane ? up : -1;
     src_page = page_of(cv, q, (int64_t)ctx + node);
     dst_page = page_of(cv, q, (int64_t)ctx + lane);
     ok = node > before && node < nn && (lane > 0 || node == 0) && src_page >= 0 && dst_page >= 0;

@@ -176,7 +176,7 @@ def _p_dev_or_pinned(t) -> int:
 
 def _s(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -427,8 +427,9 @@ class KVCache:
             assert t.is_cuda, "device tensors"
         # a dimension of one element has no stride of its own
         st = [k.stride(i) if k.shape[i] > 1 else self.D for i in range(3)]
-        self._c = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _p(k_exp), _p(v_exp), _p(table), _DTYPE[k.dtype],
-                                 self.n_pages, self.page_size, self.max_pages, self.Hk, self.D, st[0], st[1], st[2])
+        self._lib_struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _p(k_exp), _p(v_exp), _p(table), _DTYPE[k.dtype],
+                                          self.n_pages, self.page_size, self.max_pages, self.Hk, self.D, *st)
+        self._c = ctypes.byref(self._lib_struct)
 
 
 def rope_phases(theta: float, rot_dim: int, inv_freq=None, device="cuda"):
@@ -447,15 +448,15 @@ def rope_phases(theta: float, rot_dim: int, inv_freq=None, device="cuda"):
 def _rows(t, heads, D):
     """(pointer, token stride) of a [..., tokens, heads, D] tensor whose heads
     are contiguous; all leading dimensions step by the token stride."""
-    assert isinstance(t, torch.Tensor) and t.is_cuda and t.dim() >= 3 and tuple(t.shape[-2:]) == (heads, D), \
-        "device tensor [..., tokens, heads, D]"
-    assert t.stride(-1) == 1 and (heads == 1 or t.stride(-2) == D), "contiguous heads"
-    n, st = t.shape[-3], t.stride(-3)
+    shape, strides = t.shape, t.stride()
+    assert t.is_cuda and len(shape) >= 3 and shape[-1] == D and shape[-2] == heads, "device tensor [..., tokens, heads, D]"
+    assert strides[-1] == 1 and (heads == 1 or strides[-2] == D), "contiguous heads"
+    n, st = shape[-3], strides[-3]
     if n == 1:  # one token each: the stride is that of the dimension before, if it has one
-        st = t.stride(-4) if t.dim() > 3 and t.shape[-4] > 1 else heads * D
-    for i in range(t.dim() - 4, -1, -1):
-        assert t.shape[i] == 1 or t.stride(i) == n * st, "tokens at one stride"
-        n *= t.shape[i]
+        st = strides[-4] if len(shape) > 3 and shape[-4] > 1 else heads * D
+    for i in range(len(shape) - 4, -1, -1):
+        assert shape[i] == 1 or strides[i] == n * st, "tokens at one stride"
+        n *= shape[i]
     return t.data_ptr(), st
 
 
@@ -501,7 +502,7 @@ def mfd_kv_append(q, k, v, q_w, k_w, eps, phase, rot_dim, interleaved, pos, ctx_
     (kp, ks), (vp, vs) = _rows(k, Hk, D), _rows(v, Hk, D)
     rc = load().mfd_kv_append(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hq, _p(q_w), _p(k_w), eps,
                               _p(phase) if rot_dim else None, rot_dim, int(interleaved), _p(pos), _p(ctx_len),
-                              _p(n_nodes), _p(q_out) if q is not None else None, ctypes.byref(cache._c), _p(status),
+                              _p(n_nodes), _p(q_out) if q is not None else None, cache._c, _p(status),
                               _s(stream))
     _check(rc, "mfd_kv_append")
 
@@ -514,7 +515,7 @@ def mfd_kv_read(cache, start, length, k_out, v_out, status, stream=None) -> None
     assert n_req == cache.n_req
     for t in (start, length):
         assert t.dtype == torch.int32 and t.numel() == n_req
-    rc = load().mfd_kv_read(ctypes.byref(cache._c), n_req, L_max, _p(start), _p(length), _DTYPE[k_out.dtype],
+    rc = load().mfd_kv_read(cache._c, n_req, L_max, _p(start), _p(length), _DTYPE[k_out.dtype],
                             _p(k_out), _p(v_out), _p(status), _s(stream))
     _check(rc, "mfd_kv_read")
 
@@ -527,7 +528,7 @@ def mfd_kv_commit(cache, ctx_len, accept_len, path_nodes, n_nodes, new_len, stat
     for t in (ctx_len, accept_len, n_nodes, new_len):
         assert t.dtype == torch.int32 and t.numel() == n_req
     assert path_nodes.dtype == torch.int32
-    rc = load().mfd_kv_commit(ctypes.byref(cache._c), n_req, L1 - 1, _p(ctx_len), _p(accept_len), _p(path_nodes),
+    rc = load().mfd_kv_commit(cache._c, n_req, L1 - 1, _p(ctx_len), _p(accept_len), _p(path_nodes),
                               _p(n_nodes), _p(new_len), _p(status), _s(stream))
     _check(rc, "mfd_kv_commit")
 
@@ -547,7 +548,7 @@ def mfd_tree_attention(q, cache, ctx_len, n_nodes, mask, scale, out, lse, status
     assert mask is None or (mask.dtype == torch.int32 and tuple(mask.shape) == (n_req, N, (N + 31) // 32))
     assert lse is None or (lse.dtype == torch.float32 and lse.numel() == n_req * N * Hq)
     qp, qs = _rows(q, Hq, D)
-    rc = load().mfd_tree_attention(qp, qs, _DTYPE[q.dtype], n_req, N, Hq, ctypes.byref(cache._c), _p(ctx_len),
+    rc = load().mfd_tree_attention(qp, qs, _DTYPE[q.dtype], n_req, N, Hq, cache._c, _p(ctx_len),
                                    _p(n_nodes), _p(mask), scale, _p(out), _p(lse), _p(status), _p(ws),
                                    ws.numel() * ws.element_size(), _s(stream))
     _check(rc, "mfd_tree_attention")
