@@ -62,19 +62,26 @@ enum { SINK_TENSOR = 0, SINK_CACHE = 1, SINK_E4M3 = 2 };
 
 // One block handles up to WARPS * (32 / LR) * U rows (heads) of one token; a
 // row of D elements is LR lanes of 8 elements (LR: the power of two at or above
-// D / 8), so a lane keeps its place in the row, and with it its cosines and
-// sines, for all of the block's rows.  A block is short and waits for memory
-// most of its time: everything whose address is known at the start (U rows a
-// lane, weights, phases, lengths) is loaded before anything is used.
+// D / 8).  A block is short and waits for memory at its start: everything whose
+// address is known (U rows a lane, weights, phases, lengths) is loaded before
+// anything is used.
 //
-// ROT_SMEM: halves that are not a multiple of 8 elements; a lane's partners
-// then lie in two other lanes at an offset, and the row passes through shared
-// memory.  Otherwise the partner is one lane's chunk (a shuffle) or, in the
-// interleaved form, the lane's own.
+// Norm and rotation are one product of three: with r = 1 / sqrt(mean x^2 + eps),
+//   y_e = r * (x_e (w_e cos a_e) + x_p (+- w_p sin a_e)),   p the partner of e,
+// and the two bracketed factors are the same for every head of the token: the
+// block makes them once, for queries and for keys, in shared memory.  A row is
+// then one sum of squares and two products an element.  (With weights, cosines
+// and sines applied one after the other the kernel waited for its own
+// instructions: 16,000 tokens of 24 heads of 256 took 120 us.)
+//
+// Partners: another lane's chunk (halves of whole chunks: one shuffle of packed
+// pairs), the lane's own pairs (interleaved), or, ROT_SMEM, two lanes' chunks at
+// an offset; the row then passes through shared memory.
 template <typename T, int SINK, int LR, int U, bool ROT_SMEM>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   constexpr int RW = 32 / LR;  // rows of a warp at once
   __shared__ float cos_s[MAX_D / 2], sin_s[MAX_D / 2];
+  __shared__ __align__(16) float own_s[2][MAX_D], other_s[2][MAX_D];  // w cos, +- w sin: queries, keys
   __shared__ float row_s[ROT_SMEM ? WARPS * RW : 1][ROT_SMEM ? MAX_D : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & (LR - 1), sub = lane / LR;
@@ -92,11 +99,11 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
     if (in_row && row < rows) {  // before n_nodes is known: dead rows' values are not used
       const uint8_t *src;
       if (row < p.Hq)
-        src = p.q + ((int64_t)tok * p.q_stride + (int64_t)row * p.D + c * 8) * 2;
+        src = p.q + ((int64_t)tok * p.q_stride + row * p.D + c * 8) * 2;
       else if (row < p.Hq + p.Hk)
-        src = p.k + ((int64_t)tok * p.k_stride + (int64_t)(row - p.Hq) * p.D + c * 8) * 2;
+        src = p.k + ((int64_t)tok * p.k_stride + (row - p.Hq) * p.D + c * 8) * 2;
       else
-        src = p.v + ((int64_t)tok * p.v_stride + (int64_t)(row - p.Hq - p.Hk) * p.D + c * 8) * 2;
+        src = p.v + ((int64_t)tok * p.v_stride + (row - p.Hq - p.Hk) * p.D + c * 8) * 2;
       raw[u] = *reinterpret_cast<const uint4 *>(src);
     }
   }
@@ -104,10 +111,18 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   const bool turns = (int)threadIdx.x < h;  // h <= THREADS
   const uint64_t phase = turns ? __ldg(p.phase + threadIdx.x) : 0;
   const int64_t pos = turns ? __ldg(p.pos + tok) : 0;
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (in_row) {
-    if (p.q_w) wq = __ldg(reinterpret_cast<const uint4 *>(p.q_w + c * 16));
-    if (p.k_w) wk = __ldg(reinterpret_cast<const uint4 *>(p.k_w + c * 16));
+  // this thread's two elements of the factors: weights of the element and its partner
+  float w_own[2][2], w_other[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = threadIdx.x + i * THREADS;
+    const int o = e >= 2 * h ? e : p.interleaved ? e ^ 1 : e < h ? e + h : e - h;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t *w = k ? p.k_w : p.q_w;
+      w_own[i][k] = w && e < p.D ? unpack2<T>(__ldg(reinterpret_cast<const uint16_t *>(w) + e)).x : 1.f;
+      w_other[i][k] = w && e < p.D ? unpack2<T>(__ldg(reinterpret_cast<const uint16_t *>(w) + o)).x : 1.f;
+    }
   }
   bool live = true;
   int ctx = 0, page = -1;
@@ -122,23 +137,34 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   }
   if (turns) turn_cos_sin(phase * (uint64_t)pos, cos_s[threadIdx.x], sin_s[threadIdx.x]);
   block_sync();
-  // per element: y = x * cs + partner * sn (left as it is past rot_dim)
-  float cs[8], sn[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = c * 8 + i;
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (live && e < 2 * h) {
-      const bool second = p.interleaved ? (e & 1) : e >= h;
-      const int a = p.interleaved ? e >> 1 : (second ? e - h : e);
-      cs[i] = cos_s[a];
-      sn[i] = second ? sin_s[a] : -sin_s[a];
+  for (int i = 0; i < 2; ++i) {
+    const int e = threadIdx.x + i * THREADS;
+    if (e < p.D) {
+      float cs = 1.f, sn = 0.f;
+      if (e < 2 * h) {
+        const bool second = p.interleaved ? (e & 1) : e >= h;
+        const int a = p.interleaved ? e >> 1 : (second ? e - h : e);
+        cs = cos_s[a];
+        sn = second ? sin_s[a] : -sin_s[a];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        own_s[k][e] = w_own[i][k] * cs;
+        other_s[k][e] = w_other[i][k] * sn;
+      }
     }
   }
+  block_sync();
   // the lane whose chunk holds this chunk's partners (halves of whole chunks)
   const int hc = h >> 3;
   const int partner = c < hc ? lane + hc : c < 2 * hc ? lane - hc : lane;
+  const bool paired = c < 2 * hc;
+  const float per_d = 1.f / (float)p.D;
+  // the token's place in the cache, in elements
+  const int slot = (ctx + n) & ((1 << p.cache.ps_shift) - 1);
+  const int64_t place = SINK == SINK_TENSOR ? 0 : page * p.cache.page_stride + slot * p.cache.token_stride + c * 8;
+
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int row = row0 + u * WARPS * RW;
@@ -147,28 +173,12 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
     const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hk;
     float x[8];
     unpack8<T>(raw[u], x);
-    if (!live)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    // norm: rows of q and k with a weight (values and dead rows pass)
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = 1; o < LR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (live && !is_v && (is_q ? p.q_w : p.k_w)) {
-      const float r = 1.f / sqrtf(ss / (float)p.D + p.eps);
-      float w[8];
-      unpack8<T>(is_q ? wq : wk, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    }
-    // rotation
-    if (h) {
+    if (!__all_sync(0xffffffffu, is_v)) {
+      // partners, from the values as they came
       float xp[8];
       if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xp[i] = x[i ^ 1];
+        for (int i = 0; i < 8; ++i) xp[i] = c * 8 + i < 2 * h ? x[i ^ 1] : 0.f;
       } else if (ROT_SMEM) {
         float *buf = row_s[warp * RW + sub];
         __syncwarp();
@@ -182,26 +192,45 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
           xp[i] = e < 2 * h ? buf[e < h ? e + h : e - h] : 0.f;
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xp[i] = __shfl_sync(0xffffffffu, x[i], partner);
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
+        o.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
+        o.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
+        o.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
+        if (!paired) o = make_uint4(0, 0, 0, 0);
+        unpack8<T>(o, xp);
       }
-      if (!is_v)
+      float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = c * 8 + i < 2 * h ? fmaf(xp[i], sn[i], x[i] * cs[i]) : x[i];
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = 1; o < LR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!is_v && in_row) {
+        const float r = (is_q ? p.q_w : p.k_w) ? rsqrtf(fmaf(ss, per_d, p.eps)) : 1.f;
+        const float4 *fo = reinterpret_cast<const float4 *>(own_s[is_q ? 0 : 1] + c * 8);
+        const float4 *ft = reinterpret_cast<const float4 *>(other_s[is_q ? 0 : 1] + c * 8);
+        const float4 a = fo[0], b = fo[1], d = ft[0], e = ft[1];
+        x[0] = r * fmaf(xp[0], d.x, x[0] * a.x);
+        x[1] = r * fmaf(xp[1], d.y, x[1] * a.y);
+        x[2] = r * fmaf(xp[2], d.z, x[2] * a.z);
+        x[3] = r * fmaf(xp[3], d.w, x[3] * a.w);
+        x[4] = r * fmaf(xp[4], e.x, x[4] * b.x);
+        x[5] = r * fmaf(xp[5], e.y, x[5] * b.y);
+        x[6] = r * fmaf(xp[6], e.z, x[6] * b.z);
+        x[7] = r * fmaf(xp[7], e.w, x[7] * b.w);
+      }
     }
     // out
     if (is_q || SINK == SINK_TENSOR) {
       if (have && in_row) {
         uint8_t *dst = is_q ? p.q_out + (((int64_t)tok * p.Hq + row) * p.D + c * 8) * 2
                             : p.k_out + (((int64_t)tok * p.Hk + row - p.Hq) * p.D + c * 8) * 2;
-        *reinterpret_cast<uint4 *>(dst) = pack8<T>(x);
+        *reinterpret_cast<uint4 *>(dst) = live ? pack8<T>(x) : make_uint4(0, 0, 0, 0);
       }
     } else if (SINK == SINK_CACHE) {
       if (have && in_row && page >= 0) {
-        const int slot = (ctx + n) & ((1 << p.cache.ps_shift) - 1);
         const int hd = row - p.Hq - (is_v ? p.Hk : 0);
-        uint8_t *dst = static_cast<uint8_t *>(is_v ? p.cache.v : p.cache.k) +
-                       (page * p.cache.page_stride + hd * p.cache.head_stride + slot * p.cache.token_stride + c * 8) * 2;
+        uint8_t *dst = static_cast<uint8_t *>(is_v ? p.cache.v : p.cache.k) + (place + hd * p.cache.head_stride) * 2;
         *reinterpret_cast<uint4 *>(dst) = is_v ? raw[u] : pack8<T>(x);
       }
     }
@@ -218,14 +247,15 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
         if (code != EXP_NAN) {
           const float inv = e4m3_inv(code), lim = e4m3_limit<T>(code);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i] * inv, -lim), lim);
+          for (int i = 0; i < 8; ++i) x[i] *= inv;
+          if (lim < 448.f)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -lim), lim);
           b.x = e4m3x4(x[0], x[1], x[2], x[3]);
           b.y = e4m3x4(x[4], x[5], x[6], x[7]);
         }
-        const int slot = (ctx + n) & ((1 << p.cache.ps_shift) - 1);
         const int hd = row - p.Hq - (is_v ? p.Hk : 0);
-        uint8_t *dst = static_cast<uint8_t *>(is_v ? p.cache.v : p.cache.k) + page * p.cache.page_stride +
-                       hd * p.cache.head_stride + slot * p.cache.token_stride + c * 8;
+        uint8_t *dst = static_cast<uint8_t *>(is_v ? p.cache.v : p.cache.k) + place + hd * p.cache.head_stride;
         *reinterpret_cast<uint2 *>(dst) = b;
         if (c == 0)
           (is_v ? p.cache.v_exp : p.cache.k_exp)[(((int64_t)page * p.Hk + hd) << p.cache.ps_shift) + slot] =
