@@ -85,14 +85,17 @@ struct Shape {
   static constexpr int ST = E4M3_ ? (DP == 64 ? 4 : 3) : (DP == 64 ? 8 : 5);
   static constexpr int RST = E4M3_ ? (DP == 64 ? 6 : 4) : 0;
   static constexpr int HELPERS = E4M3_ ? 2 : 1;        // warpgroups that help
-  static constexpr int THREADS = 128 * (1 + NS + HELPERS);
-  static constexpr int HELP_WARP = 4 + 4 * NS;
+  static constexpr bool SPLIT = NS == 1 && !E4M3_;     // one stream's columns shared by two softmax warpgroups
+  static constexpr int SG = NS == 2 || SPLIT ? 2 : 1;  // softmax warpgroups
+  static constexpr int THREADS = 128 * (1 + SG + HELPERS);
+  static constexpr int HELP_WARP = 4 + 4 * SG;
   static constexpr int SW = 32;                        // score columns a softmax thread holds
   static constexpr int TM_S = 0;                       // two S accumulators; P over them
   static constexpr int TM_O = 2 * BN;
   static constexpr int POWERS = E4M3_ ? 2 * 4 * BN * 2 : 0;  // [k, v][tile mod 4][position], 16 bits
-  static constexpr int BARS = (E4M3_ ? 2 : 3) * ST + 2 * RST + 8 + 8 + 2 * SEG_RING;
-  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + POWERS + MAX_N / 8 + BARS * 8 + SEG_RING * 40 + 48;
+  static constexpr int BARS = (E4M3_ ? 2 : 3) * ST + 2 * RST + 8 + (E4M3_ ? 8 : 0) + 2 * SEG_RING;
+  static constexpr int TOPS = SPLIT ? 2 * 2 * BM * 4 : 0;  // row maxima the two exchange, [step mod 2][half]
+  static constexpr int SMEM = NS * Q_TILE + ST * STAGE + RST * RAW + POWERS + MAX_N / 8 + BARS * 8 + SEG_RING * 40 + 48 + TOPS;
 };
 
 // ------------------------------------------------------------------ line of work
@@ -528,9 +531,9 @@ __device__ __noinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volat
 
 // Scores of a warp's rows that a tile past the context hides, to -infinity, in
 // tensor memory: 32 columns per word of `vis`.
-__device__ __noinline__ void hide_scores(uint32_t sa, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+__device__ __noinline__ void hide_scores(uint32_t sa, int columns, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
 #pragma unroll 1
-  for (int part = 0; part < 8; ++part) {
+  for (int part = 0; part < columns / 16; ++part) {
     const uint32_t w = (part < 2 ? v0 : part < 4 ? v1 : part < 6 ? v2 : v3) >> (16 * (part & 1));
     uint32_t x[16];
     tmem_ld16(sa + 16 * part, x);
@@ -555,14 +558,6 @@ __device__ __noinline__ void scale_rows(uint32_t oa, int columns, float a) {
     tmem_st16(oa + d, o);
   }
 }
-// Zeros and -infinity for a row that is not live.
-__device__ __noinline__ void zero_row(const Params &p, int q, int h, int row) {
-  const int n = row / p.G, g = row - n * p.G;
-  const int64_t at = ((int64_t)q * p.N + n) * p.Hq + h * p.G + g;
-  for (int d = 0; d < p.cv.D; d += 8) *reinterpret_cast<uint4 *>(p.out + at * p.cv.D + d) = make_uint4(0, 0, 0, 0);
-  if (p.lse) p.lse[at] = -INFINITY;
-}
-
 // The order in which a segment's tiles pass the ring: keys and values as K0 V0
 // K1 V1 .. when both streams read every tile, K0 K1 V0 K2 V1 .. when they take
 // turns (a stream's scores are then two tiles ahead).  Step i of 2 n.
@@ -758,7 +753,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const Params p) {
   using SH = Shape<DP, E4M3>;
-  constexpr int NS = SH::NS, NU = SH::NU, NB = SH::NB, ST = SH::ST, RST = SH::RST;
+  constexpr int NS = SH::NS, NU = SH::NU, NB = SH::NB, ST = SH::ST, RST = SH::RST, SG = SH::SG;
+  constexpr bool SPLIT = SH::SPLIT;
   constexpr uint32_t RN = RST ? RST : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem;
@@ -777,8 +773,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   uint64_t *q_full = pv_done + 2;
   uint64_t *drain = q_full + 1;
   uint64_t *pow_full = drain + 1;
-  uint64_t *pow_empty = pow_full + 4;
-  uint64_t *seg_full = pow_empty + 4;
+  uint64_t *pow_empty = pow_full + (E4M3 ? 4 : 0);
+  uint64_t *seg_full = pow_empty + (E4M3 ? 4 : 0);
   uint64_t *seg_empty = seg_full + SEG_RING;
   Segment *seg_ring = reinterpret_cast<Segment *>(seg_empty + SEG_RING);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(seg_ring + SEG_RING);
@@ -787,6 +783,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   volatile int *seg_done = never + 1;  // segments a softmax warpgroup has left [2]
   volatile int *any_bad = seg_done + 2;
   volatile int *wide_s = any_bad + 1;  // E4M3: a tile with a power that has no number (1 keys, 2 values) [4]
+
+  float *top_s = reinterpret_cast<float *>(const_cast<int *>(wide_s) + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CacheView &cv = p.cv;
@@ -809,18 +807,18 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], SPLIT ? 8 : 4);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < SEG_RING; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 3 + 4 * (NS + SH::HELPERS));
+      mbar_init(&seg_empty[i], 3 + 4 * (SG + SH::HELPERS));
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (E4M3 ? 4 : 0); ++i) {
       mbar_init(&pow_full[i], 1);
       mbar_init(&pow_empty[i], 8 * NU);  // four warps for each of a tile's units
     }
-    mbar_init(q_full, 4 * NS);
+    mbar_init(q_full, 4 * SG);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *never = 0;
@@ -875,7 +873,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     if (!ok) return;
     const unsigned long long t0 = globaltimer();
     for (uint32_t it = 1;; ++it) {
-      if (seg_done[0] >= seg && (NS == 1 || seg_done[1] >= seg)) return;
+      if (seg_done[0] >= seg && (SG == 1 || seg_done[1] >= seg)) return;
       if ((it & 15u) == 0 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
         if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -1038,7 +1036,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               const uint32_t va = desc_lo(smem_u32(sT) + vst * SH::STAGE, BN * 128);
               const uint32_t d = tmem + SH::TM_O + (uint32_t)(acc * DP + u * SH::UC);
 #pragma unroll
-              for (int k = 0; k < BN / 16; ++k) mma_ts(d, a + k * 8, va + k * (2048 >> 4), id_o, more || k != 0);
+              for (int k = 0; k < BN / 16; ++k) mma_ts(d, a + k * 8 + (SPLIT && k >= 4 ? 32 : 0), va + k * (2048 >> 4), id_o, more || k != 0);
               if (!shared || (i & 1)) tc_commit(&empty[vst]);
             }
             if (ok) tc_commit(&pv_done[acc]);
@@ -1122,11 +1120,14 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
   } else if (warp < SH::HELP_WARP) {
     // --------------------------------------------------------- softmax
-    const int ws = NS == 2 ? (warp - 4) >> 2 : 0;  // stream
+    const int ws = SG == 2 ? (warp - 4) >> 2 : 0;  // stream, or half of a stream's columns (SPLIT)
     const int wq = warp & 3;                       // the warp's lanes of tensor memory
     const int r = wq * 32 + lane;
+    const int acc = NS == 2 ? ws : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t o_base = lane_base + SH::TM_O + (uint32_t)ws * DP;
+    constexpr int S_COLS = SPLIT ? BN / 2 : BN, O_COLS = SPLIT ? DP / 2 : DP;  // this thread's
+    const int s_col = SPLIT ? ws * S_COLS : 0;
+    const uint32_t o_base = lane_base + SH::TM_O + (uint32_t)ws * O_COLS;
     uint32_t s_par = 0, pv_n = 0;
     // alternating streams exchange (m, l) in the space of the second Q tile
     float2 *ml_s = reinterpret_cast<float2 *>(sQ + (NS - 1) * SH::Q_TILE);
@@ -1145,8 +1146,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       // stay as they are (a row's scores reach no other row)
       if (nt > 0) {
         constexpr int C = DP / 8, STEP = 128 / C;
-        const int base_row = shared || NS == 1 ? 0 : ws * (BM / 2);  // alternating: half the rows each
-        const int have = min(shared || NS == 1 ? BM : BM / 2, live - row0 - base_row);  // rows to load
+        const bool all = shared || SG == 1;  // else half the rows each
+        const int base_row = all ? 0 : ws * (BM / 2);
+        const int have = min(all ? BM : BM / 2, live - row0 - base_row);  // rows to load
         const int ch = r % C;
         const uint32_t dst = smem_u32(sQ + rt * SH::Q_TILE) + (ch >> 3) * (BM * 128);
         const uint16_t *src = p.q + (int64_t)s.q * p.N * p.q_stride + (int64_t)s.h * p.G * cv.D + ch * 8;
@@ -1187,11 +1189,18 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           }
         }
       }
-      // rows past n_nodes, once per item
-      if (s.head) {
-        const int zrow = (s.pair * NS + ws) * BM + r;
-        if (zrow < p.M && zrow >= (s.tiles ? live : 0))
-          zero_row(p, s.q, s.h, zrow);
+      // rows past n_nodes, once per item: zeros and -infinity
+      if (s.head && (NS == 2 || ws == 0)) {
+        const int first = (s.pair * NS + acc) * BM + wq * 32, c8 = cv.D / 8;
+        const int lo = max(first, s.tiles ? live : 0), rows = min(first + 32, p.M) - lo;
+#pragma unroll 1
+        for (int i = lane; i < rows * c8; i += 32) {
+          const int rr = lo + i / c8, ch = i % c8;
+          const int zn = rr / p.G, zg = rr - zn * p.G;
+          const int64_t at = ((int64_t)s.q * p.N + zn) * p.Hq + s.h * p.G + zg;
+          st_global16(p.out + at * cv.D + ch * 8, make_uint4(0, 0, 0, 0));
+          if (ch == 0 && p.lse) p.lse[at] = -INFINITY;
+        }
       }
       if (nt == 0) continue;
       cp_async_wait();
@@ -1207,29 +1216,32 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       for (int i = NS == 2 ? ws : 0; i < steps; i += NS) {
         const int slot = i & 1;
         const int t_base = (s.t0 + (shared ? i >> 1 : i)) * BN;
-        uint32_t vis[BN / 32];
+        uint32_t vis[S_COLS / 32];
         bool hide = false;
         if (t_base + BN > s.ctx && warp_live) {
+          uint32_t every = 0xFFFFFFFFu;
 #pragma unroll
-          for (int k = 0; k < BN / 32; ++k)
-            vis[k] = row_live ? visible32(mask_row, p.W32, node, s.nn, t_base + 32 * k - s.ctx) : 0xFFFFFFFFu;
-          hide = __any_sync(0xffffffffu, (vis[0] & vis[1] & vis[2] & vis[3]) != 0xFFFFFFFFu);
+          for (int k = 0; k < S_COLS / 32; ++k) {
+            vis[k] = row_live ? visible32(mask_row, p.W32, node, s.nn, t_base + s_col + 32 * k - s.ctx) : 0xFFFFFFFFu;
+            every &= vis[k];
+          }
+          hide = __any_sync(0xffffffffu, every != 0xFFFFFFFFu);
         }
         wait(&s_full[slot], (s_par >> slot) & 1u);
         s_par ^= 1u << slot;
         ok = __all_sync(0xffffffffu, ok);
+        const uint32_t sa = lane_base + SH::TM_S + (uint32_t)(slot * BN + s_col);
+        constexpr int SW = SH::SW;
+        float top = -INFINITY;
         if (ok && warp_live) {
           tc_fence_after();
-          const uint32_t sa = lane_base + SH::TM_S + (uint32_t)slot * BN;
+          if (hide) hide_scores(sa, S_COLS, vis[0], vis[1], vis[S_COLS / 32 - 2], vis[S_COLS / 32 - 1]);
           // Both passes read the scores from tensor memory, 32 columns at a time
           // in a rolled loop: 128 in registers took unrolled code for all of
           // them, and the warps then waited for instructions (3.5 cycles an
           // issue) more than for anything else.
-          if (hide) hide_scores(sa, vis[0], vis[1], vis[2], vis[3]);
-          constexpr int SW = SH::SW;
-          float top = -INFINITY;
 #pragma unroll 1
-          for (int part = 0; part < BN / SW; ++part) {
+          for (int part = 0; part < S_COLS / SW; ++part) {
             uint32_t x[SW];
 #pragma unroll
             for (int k = 0; k < SW; k += 32) tmem_ld32(sa + SW * part + k, x + k);
@@ -1242,6 +1254,14 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               t[(k >> 1) & 3] = max3(t[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
             top = max3(max3(t[0], t[1], t[2]), t[3], top);
           }
+        }
+        if (SPLIT) {  // the row's maximum over both halves
+          float *mine = top_s + (i & 1) * (2 * BM) + r;
+          mine[ws * BM] = top;
+          named_sync(1, 256);
+          top = fmaxf(top, mine[(ws ^ 1) * BM]);
+        }
+        if (ok && warp_live) {
           top *= p.c;
           // move the maximum when it has grown by enough (or is the first)
           const bool move = row_live && top > m + MAX_GROWTH;
@@ -1251,16 +1271,16 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             m = m2;
             l *= a;
             if (done) {
-              wait(&pv_done[ws], (pv_n - 1u) & 1u);
+              wait(&pv_done[acc], (pv_n - 1u) & 1u);
               tc_fence_after();
-              scale_rows(o_base, DP, a);
+              scale_rows(o_base, O_COLS, a);
             }
           }
           const float mz = m == -INFINITY ? 0.f : m;
           const uint64_t cc = pair(p.c, p.c), mm = pair(-mz, -mz);
           uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-          for (int part = 0; part < BN / SW; ++part) {
+          for (int part = 0; part < S_COLS / SW; ++part) {
             uint32_t x[SW];
 #pragma unroll
             for (int k = 0; k < SW; k += 32) tmem_ld32(sa + SW * part + k, x + k);
@@ -1281,7 +1301,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
                   sum0 = add2(sum0, pair(a, b));
                 pk[k] = pack2<T>(a, b);
               }
-              tmem_st16(sa + (SW * part + c) / 2, pk);
+              tmem_st16(sa + (SW * part + c) / 2, pk);  // over scores that have been read
             }
           }
           const float2 sum = unpair(add2(sum0, sum1));
@@ -1298,51 +1318,60 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       // ------------------------------------------------------- epilogue
       // With one stream the last but one product may still run (scores are two
       // tiles ahead of it); a wait on a parity needs the phase before it complete.
-      if (NS == 1 && done > 1) wait(&pv_done[ws], pv_n & 1u);
-      if (done) wait(&pv_done[ws], (pv_n - 1u) & 1u);
+      if (NS == 1 && done > 1) wait(&pv_done[acc], pv_n & 1u);
+      if (done) wait(&pv_done[acc], (pv_n - 1u) & 1u);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const bool alternating = NS == 2 && !shared;
       float a0 = 1.f, a1 = 0.f;
       if (alternating) {
-        if (ws == 1) ml_s[r] = make_float2(m, l);
+        ml_s[ws * BM + r] = make_float2(m, l);
         named_sync(1, 256);
-        if (ws == 0) {
-          const float2 o = ml_s[r];
-          const float top = fmaxf(m, o.x);
-          if (top > -INFINITY) {
-            a0 = m == -INFINITY ? 0.f : ex2(m - top);
-            a1 = o.x == -INFINITY ? 0.f : ex2(o.x - top);
-            l = l * a0 + o.y * a1;
-            m = top;
-          } else {
-            l += o.y;  // nothing seen (0), or NaN
-          }
+        const float2 f = ml_s[r], o = ml_s[BM + r];
+        m = fmaxf(f.x, o.x);
+        if (m > -INFINITY) {
+          a0 = f.x == -INFINITY ? 0.f : ex2(f.x - m);
+          a1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+          l = f.y * a0 + o.y * a1;
+        } else {
+          l = f.y + o.y;  // nothing seen (0), or NaN
         }
       }
+      if (SPLIT) {
+        float *mine = top_s + (steps & 1) * (2 * BM) + r;
+        mine[ws * BM] = l;
+        named_sync(1, 256);
+        l = mine[0] + mine[BM];
+      }
       const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-      if (ok && (!alternating || ws == 0) && warp_live) {
+      if (ok && warp_live) {
         const bool two = alternating && steps > 1;
         if (whole) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           a0 *= inv;
           a1 *= inv;
         }
+        // columns: all of this stream's, or half of the two streams' sum, or
+        // this warpgroup's half of the one stream's
+        const bool half = alternating || SPLIT;
+        const int middle = SPLIT ? O_COLS : (cv.D + 31) / 32 * 16;
+        const int d0 = half && ws == 1 ? middle : 0, d1 = half && ws == 0 ? min(middle, cv.D) : cv.D;
+        const uint32_t from = alternating ? lane_base + SH::TM_O : o_base - (SPLIT ? ws * O_COLS : 0);
         const int64_t at = row_live ? ((int64_t)s.q * p.N + node) * p.Hq + s.h * p.G + g : 0;
         const int part = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
         const bool fix = p.N > 1 && s.t1 * BN > s.ctx && *any_bad;
         float4 *po = p.part_o + (int64_t)part * (cv.D / 4) * p.part_rows + rt * BM + r;
         // a row's place: 16 columns are 32 bytes of the output, or 4 of its
         // part's float4, each the rows' length from the next
-        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out + at * cv.D) : reinterpret_cast<uint8_t *>(po);
         const int64_t hop = (int64_t)p.part_rows * 16;
+        uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(p.out + at * cv.D + d0) : reinterpret_cast<uint8_t *>(po) + hop * (d0 / 4);
 #pragma unroll 1
-        for (int d = 0; d < cv.D; d += 16) {
+        for (int d = d0; d < d1; d += 16) {
           uint32_t o[16];
-          tmem_ld16(o_base + d, o);
+          tmem_ld16(from + d, o);
           if (two) {
             uint32_t o1[16];
-            tmem_ld16(o_base + DP + d, o1);
+            tmem_ld16(from + DP + d, o1);
             tmem_wait_ld();
             tie16(o);
             tie16(o1);
@@ -1379,7 +1408,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             }
           }
         }
-        if (row_live) {
+        if (row_live && !(half && ws == 1)) {
           if (!whole)
             p.part_ml[(int64_t)part * p.part_rows + rt * BM + r] = make_float2(m, l);
           else if (p.lse)
@@ -1387,7 +1416,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         }
       }
       tc_fence_before();
-      if (alternating) named_sync(1, 256);  // the first stream has read the second's O and (m, l)
+      if (alternating) named_sync(1, 256);  // each has read the other's O and (m, l)
       tc_fence_after();
       if (p.N > 1) {  // the noted nodes are read: the helpers may clear them
         if (ws == 0)
