@@ -55,6 +55,15 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
 
+// What a CTA leaves for the join: whether it holds parts (of the item its
+// stretch starts in, of the one it ends in), and of the latter, if this CTA has
+// its first part, where it is and how many CTAs it reaches over.
+struct Cut {
+  int has[2];
+  int reach;  // 0: no first part
+  int q, h, pair, nn;
+};
+
 struct Params {
   CacheView cv;
   const uint16_t *q;
@@ -70,6 +79,7 @@ struct Params {
   float4 *part_o;   // [slot][D / 4][part_rows]
   float2 *part_ml;  // [slot][part_rows]
   int part_rows;
+  struct Cut *cuts;  // [CTA]
 };
 
 template <int DP_, bool E4M3_>
@@ -576,19 +586,21 @@ __device__ __forceinline__ Turn turn_at(bool turns, int n, int i) {
 // costs are summed by its lanes.
 template <int NS>
 struct Scheduler {
-  int64_t x, x1;
+  int64_t x, x1, total;
   int q, h, pair, z, ctx, nn;
   uint32_t n;  // entries written
   bool ended;
+  Cut cut;
 
   __device__ __forceinline__ void start(const Params &p, int lane) {
     int64_t begin;
-    const int64_t total = line_walk<NS>(p, lane, -1, blockIdx.x == 0, q, begin);
+    total = line_walk<NS>(p, lane, -1, blockIdx.x == 0, q, begin);
     x = border(total, blockIdx.x, gridDim.x);
     x1 = border(total, blockIdx.x + 1, gridDim.x);
     h = pair = z = ctx = nn = 0;
     n = 0;
     ended = false;
+    cut = Cut{};
     if (x >= x1) return;
     line_walk<NS>(p, lane, x, false, q, begin);
     lengths(p, q, ctx, nn);
@@ -626,6 +638,16 @@ struct Scheduler {
       s.t0 = tile_at(it, z);
       s.t1 = tile_at(it, end);
       s.head = z == 0;
+      if (s.t0 < s.t1 && !(s.t0 == 0 && s.t1 == it.tiles)) {
+        cut.has[s.t0 == 0 ? 1 : 0] = 1;
+        if (s.t0 == 0) {
+          cut.reach = cta_of(total, x - z + it.cost - 1, gridDim.x) - (int)blockIdx.x + 1;
+          cut.q = q;
+          cut.h = h;
+          cut.pair = pair;
+          cut.nn = nn;
+        }
+      }
       x += end - z;
       z = 0;
       if (end == it.cost && ++pair == p.n_pair) {
@@ -637,6 +659,7 @@ struct Scheduler {
       }
     }
     if (lane == 0) {
+      if (ended) p.cuts[blockIdx.x] = cut;
       ring[st] = s;
       mbar_arrive(&seg_full[st]);
     }
@@ -1546,67 +1569,26 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
 constexpr int JOIN_ROWS = 16;
 
 // Combines the parts of the items that borders cut.  Block (c, y): the item
-// whose first inner border is CTA c + 1's start, if there is one, and 16 of its
-// rows; first every part's weight 2^(m - max m) / sum for these rows, then a
-// thread for each row and 8 columns adds the parts up in their order.
+// whose first part CTA c holds, if any, and 16 of its rows; first every part's
+// weight 2^(m - max m) / sum for these rows, then a thread for each row and 8
+// columns adds the parts up in their order.
 template <typename T, int NS>
-__global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p, int n_cta) {
-  __shared__ int64_t at_s[3];  // the line's length, the item's start and end
-  __shared__ int where_s[4];   // request, head, item, whether this block joins it
+__global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
   __shared__ int slot_s[ATTENTION_MAX_CTAS];
   const int tid = threadIdx.x, lane = tid & 31, threads = JOIN_ROWS * (p.cv.D / 8);
-  const int c = (int)blockIdx.x + 1;
-  if (tid < 32) {
-    int q, ctx, nn;
-    int64_t begin;
-    const int64_t total = line_walk<NS>(p, lane, -1, false, q, begin);
-    const int64_t x = border(total, c, n_cta);
-    line_walk<NS>(p, lane, x, false, q, begin);
-    lengths(p, q, ctx, nn);
-    const int64_t hc = head_cost_warp<NS>(p, ctx, nn, lane);
-    const int h = (int)divide(x - begin, hc);
-    int64_t rest = x - begin - h * hc;
-    const int pr = find_item<NS>(p, ctx, nn, lane, rest);
-    const Item it = item_of<NS>(p, ctx, nn, pr);
-    const int64_t u0 = x - rest;
-    if (lane == 0) {
-      at_s[0] = total;
-      at_s[1] = u0;
-      at_s[2] = u0 + it.cost;
-      where_s[0] = q;
-      where_s[1] = h;
-      where_s[2] = pr;
-      // cut here, and not before
-      where_s[3] = rest > 0 && border(total, c - 1, n_cta) <= u0 && it.tiles > 0;
-    }
-  }
-  block_sync();
-  const int64_t total = at_s[0], u0 = at_s[1], u1 = at_s[2];
-  // Every block waits for the parts, also those with nothing to join: this grid
-  // must not end before the one it follows.
-  if (!where_s[3]) {
-    pdl_wait();
-    return;
-  }
-  const int q = where_s[0], h = where_s[1], pr = where_s[2];
-  int ctx, nn;
-  lengths(p, q, ctx, nn);
-  const Item it = item_of<NS>(p, ctx, nn, pr);
-  const int first = pr * NS * BM;
-  const int rows = min(nn * p.G - first, NS * BM);
+  pdl_wait();  // the parts are written
+  const int c0 = blockIdx.x;
+  const Cut cut = p.cuts[c0];
+  const int n_part = cut.reach, q = cut.q, h = cut.h;
+  const int first = cut.pair * NS * BM;
+  const int rows = min(cut.nn * p.G - first, NS * BM);
   const int row0 = (int)blockIdx.y * JOIN_ROWS;
-  const int c0 = c - 1, n_part = cta_of(total, u1 - 1, n_cta) - c0 + 1;
-  // each part's slot, or -1 if it holds no key tile; all tiles in one part: it wrote the result
-  bool direct = false;
-  for (int i = tid; i < n_part; i += threads) {
-    const int64_t lo = border(total, c0 + i, n_cta), hi = border(total, c0 + i + 1, n_cta);
-    const int t0 = tile_at(it, (int)((lo > u0 ? lo : u0) - u0)), t1 = tile_at(it, (int)((hi < u1 ? hi : u1) - u0));
-    slot_s[i] = t0 >= t1 ? -1 : 2 * (c0 + i) + (t0 == 0 ? 1 : 0);
-    direct |= t0 == 0 && t1 == it.tiles;
-  }
-  pdl_wait();
-  if (__syncthreads_or(direct) || row0 >= rows) return;
+  if (n_part == 0 || row0 >= rows) return;
+  // each part's slot, or -1 where a CTA's stretch of the item holds no key tile
+  for (int i = tid; i < n_part; i += threads)
+    slot_s[i] = i == 0 ? 2 * c0 + 1 : p.cuts[c0 + i].has[0] ? 2 * (c0 + i) : -1;
+  __syncthreads();
   // weights: D / 8 threads (a power of two of them, at most 16) for each row
   const int G = p.cv.D >= 128 ? 16 : p.cv.D >= 64 ? 8 : p.cv.D >= 32 ? 4 : 2;
   if (tid < JOIN_ROWS * G) {
@@ -1679,7 +1661,7 @@ cudaError_t launch_shape(const AttentionLaunch &A, const Params &p, int n_cta, c
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the join launches while the last CTAs run and waits for them before it reads their parts
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_cta - 1, (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
+  cfg.gridDim = dim3(n_cta, (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
   cfg.blockDim = dim3(JOIN_ROWS * (p.cv.D / 8));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1687,7 +1669,7 @@ cudaError_t launch_shape(const AttentionLaunch &A, const Params &p, int n_cta, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, join_kernel<T, SH::NS>, p, n_cta);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, SH::NS>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1705,7 +1687,7 @@ int part_rows(int M, int D) { return M < row_group(D) ? (M + 7) / 8 * 8 : row_gr
 
 size_t attention_part_bytes(int M, int D) {
   // two parts at most for every CTA: of the item its stretch starts in, and of the one it ends in
-  return (size_t)2 * ATTENTION_MAX_CTAS * part_rows(M, D) * ((size_t)D * 4 + 8);
+  return (size_t)2 * ATTENTION_MAX_CTAS * part_rows(M, D) * ((size_t)D * 4 + 8) + ATTENTION_MAX_CTAS * sizeof(Cut);
 }
 int attention_box_rows(int page_size) {
   return page_size < BN ? page_size : BN;
@@ -1734,6 +1716,7 @@ cudaError_t launch_tree_attention(const AttentionLaunch &A, cudaStream_t stream)
   p.part_o = static_cast<float4 *>(A.ws);
   p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(A.ws) +
                                          (size_t)2 * ATTENTION_MAX_CTAS * p.part_rows * A.cache.D * 4);
+  p.cuts = reinterpret_cast<Cut *>(p.part_ml + (size_t)2 * ATTENTION_MAX_CTAS * p.part_rows);
   const int n_cta = A.n_sm < ATTENTION_MAX_CTAS ? A.n_sm : ATTENTION_MAX_CTAS;
   const bool e4m3 = A.cache.dtype == MFD_E4M3;
   if (A.dtype == MFD_BF16)
