@@ -1077,7 +1077,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     } else if (warp == 2) {
       // ------------------------------------------------- list of work
       // E4M3: also the exponent bytes of every tile's positions, four a lane, as powers
-      // for the helpers; pages are looked up one tile ahead.
+      // for the helpers.
       uint32_t n = 0;
       int seg = 0;
       while (sched.next(p, s, lane, seg_ring, seg_full, seg_empty, never)) {
@@ -1088,15 +1088,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         bool clean = false;
         const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
         auto page_at = [&](int t) { return t < min(len, s.t1 * BN) ? __ldg(table + (t >> cv.ps_shift)) : -1; };
-        int page[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) page[i] = page_at(s.t0 * BN + 32 * i + lane);
-        for (int j = 0; j < nt; ++j, ++n) {
-          const int base = (s.t0 + j) * BN, slot = n & 3;
-          int ck[4], cw[4];
+        int page[4], ck[4], cw[4];  // pages two tiles ahead, bytes one tile ahead
+        auto load = [&](int t0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = base + 32 * i + lane;
+            const int t = t0 + 32 * i + lane;
             ck[i] = cw[i] = -1;
             if (page[i] >= 0 && page[i] < cv.n_pages) {
               const int64_t e = (((int64_t)page[i] * cv.Hk + s.h) << cv.ps_shift) + (t & ((1 << cv.ps_shift) - 1));
@@ -1105,6 +1101,19 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             }
             page[i] = page_at(t + BN);
           }
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) page[i] = page_at(s.t0 * BN + 32 * i + lane);
+        load(s.t0 * BN);
+        for (int j = 0; j < nt; ++j, ++n) {
+          const int base = (s.t0 + j) * BN, slot = n & 3;
+          int now_k[4], now_v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            now_k[i] = ck[i];
+            now_v[i] = cw[i];
+          }
+          load(base + BN);
           if (note && base + BN > s.ctx && !clean) {
             wait_rows_out(seg);
             for (int k = lane; k < MAX_N / 32; k += 32) bad[k] = 0;
@@ -1118,9 +1127,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = base + 32 * i + lane;
-            const uint16_t pk = ck[i] < 0 ? 0 : Widen<T>::power(ck[i], wk);
-            uint16_t pv = cw[i] < 0 ? 0 : Widen<T>::power(cw[i], wv);
-            if (cw[i] == EXP_NAN && note && t >= s.ctx) {
+            const uint16_t pk = now_k[i] < 0 ? 0 : Widen<T>::power(now_k[i], wk);
+            uint16_t pv = now_v[i] < 0 ? 0 : Widen<T>::power(now_v[i], wv);
+            if (now_v[i] == EXP_NAN && note && t >= s.ctx) {
               // a NaN that some rows do not see: out of the product, added back later
               pv = 0;
               atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
