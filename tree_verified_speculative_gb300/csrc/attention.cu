@@ -882,6 +882,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the setup above may overlap the previous grid; all that follows reads global memory
 
   Segment s;
   uint32_t seg_n = 0;
@@ -1609,6 +1610,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
   __shared__ int slot_s[ATTENTION_MAX_CTAS];
   const int tid = threadIdx.x, lane = tid & 31, threads = JOIN_ROWS * (p.cv.D / 8);
+  pdl_launch_dependents();
   pdl_wait();  // the parts are written
   const int c0 = blockIdx.x;
   const Cut cut = p.cuts[c0];
@@ -1689,18 +1691,22 @@ cudaError_t launch_shape(const AttentionLaunch &A, const Params &p, int n_cta, c
       return e;
     if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   }
-  attention_kernel<T, DP, E4M3><<<n_cta, SH::THREADS, SH::SMEM, stream>>>(*A.map_k, *A.map_v, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the join launches while the last CTAs run and waits for them before it reads their parts
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_cta, (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
-  cfg.blockDim = dim3(JOIN_ROWS * (p.cv.D / 8));
+  cfg.gridDim = dim3(n_cta);
+  cfg.blockDim = dim3(SH::THREADS);
+  cfg.dynamicSmemBytes = SH::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attention_kernel<T, DP, E4M3>, *A.map_k, *A.map_v, p);
+  if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+  // the join launches while the last CTAs run and waits for them before it reads their parts
+  cfg.gridDim = dim3(n_cta, (p.part_rows + JOIN_ROWS - 1) / JOIN_ROWS);
+  cfg.blockDim = dim3(JOIN_ROWS * (p.cv.D / 8));
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, join_kernel<T, SH::NS>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -80,6 +80,7 @@ enum { SINK_TENSOR = 0, SINK_CACHE = 1, SINK_E4M3 = 2 };
 template <typename T, int SINK, int LR, int U, bool ROT_SMEM>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   constexpr int RW = 32 / LR;  // rows of a warp at once
+  pdl_launch_dependents();     // the attention that follows sets itself up meanwhile
   __shared__ float cos_s[MAX_D / 2], sin_s[MAX_D / 2];
   __shared__ __align__(16) float own_s[2][MAX_D], other_s[2][MAX_D];  // w cos, +- w sin: queries, keys
   __shared__ float row_s[ROT_SMEM ? WARPS * RW : 1][ROT_SMEM ? MAX_D : 1];
