@@ -588,6 +588,12 @@ __device__ __forceinline__ Turn turn_at(bool turns, int n, int i) {
   return {(i & 1) == 0, (i & 1) ? (i + 1) >> 1 : (i - 2) >> 1};
 }
 
+// The same the other way round: where tile j's keys or values come, in tiles.
+__device__ __forceinline__ int ring_place(bool is_v, bool turns, int n, int j) {
+  if (!turns || n == 1) return 2 * j + (is_v ? 1 : 0);
+  return is_v ? min(2 * j + 2, 2 * n - 1) : max(2 * j - 1, 0);
+}
+
 // The CTA's stretch of the line, entry by entry, by one warp: the requests'
 // costs are summed by its lanes.
 template <int NS>
@@ -947,6 +953,22 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       uint64_t *freed = E4M3 ? raw_empty : empty;
       uint32_t st = 0, par = 0;  // ring place and its phase
       uint32_t special_par = 0, issued = 0, issued_special = 0, issued_par = 0;
+      auto next_place = [&]() {
+        if (++st == RING) {
+          st = 0;
+          par ^= 1u;
+        }
+      };
+      // Past the other warp's units.  A wait for a place must not come a phase
+      // early, when the parity of the phase before last would pass for it.  The
+      // MMAs free places in order, so this warp's last wait vouches for that; the
+      // two groups of helpers do not, and their frees are waited for one by one.
+      auto skip = [&](int units) {
+        for (; units > 0; --units) {
+          if (E4M3) wait(&freed[st], par ^ 1u);
+          next_place();
+        }
+      };
       while (next_segment_warp()) {
         const int nt = s.t1 - s.t0;
         const bool turns = s.active != 2;
@@ -966,21 +988,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           return page;
         };
         int page_next = page_at(0);
-        for (int i = 0; i < 2 * nt; ++i) {
-          const Turn tn = turn_at(turns, nt, i);
-          if (tn.is_v != is_v) {
-            // the other warp's, but waited for in its turn: a wait for a later
-            // phase of the same place would take this one's parity for its own
-            for (int u = 0; u < NU; ++u) {
-              wait(&freed[st], par ^ 1u);
-              if (++st == RING) {
-                st = 0;
-                par ^= 1u;
-              }
-            }
-            continue;
-          }
-          const int j = tn.j;
+        int at = 0;  // tiles of the segment that have passed
+        for (int j = 0; j < nt; ++j) {
+          const int place = ring_place(is_v, turns, nt, j);
+          skip((place - at) * NU);
+          at = place + 1;
           const int base = (s.t0 + j) * BN;
           const int page = page_next;
           page_next = page_at(j + 1);
@@ -1009,12 +1021,10 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               issued_special = sp ? issued_special | bit : issued_special & ~bit;
               if (sp) special_par ^= bit;
             }
-            if (++st == RING) {
-              st = 0;
-              par ^= 1u;
-            }
+            next_place();
           }
         }
+        skip((2 * nt - at) * NU);
       }
       // Every load issued lands before the CTA may exit.  All have been consumed
       // unless a wait ran out; a place that the other warp has filled since holds
