@@ -57,6 +57,7 @@ constexpr float LN2 = 0.6931471805599453f;
 // filling and draining, the output.  Measured, three prompts of 1,777 rows: 153
 // us with 1, 133 with 4, 137 with 6; 32 trees of 129 nodes: 413, 404, 399.
 constexpr int START_COST = 5;
+constexpr float LARGE_SCORE = 65536.f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
 
 // What a CTA leaves for the join: whether it holds parts (of the item its
@@ -558,6 +559,23 @@ __device__ __noinline__ void hide_scores(uint32_t sa, int columns, uint32_t v0, 
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] = (w >> k) & 1u ? x[k] : 0xFF800000u;
     tmem_st16(sa + 16 * part, x);
+  }
+  tmem_wait_st();
+}
+// Scores so large that a product and a difference in one rounding would leave
+// the maximum itself well off 2^0: each minus the maximum, rounded as the
+// maximum was, in tensor memory.
+__device__ __noinline__ void center_scores(uint32_t sa, int columns, float c, float m) {
+  const float back = 1.f / c;
+#pragma unroll 1
+  for (int d = 0; d < columns; d += 16) {
+    uint32_t x[16];
+    tmem_ld16(sa + d, x);
+    tmem_wait_ld();
+    tie16(x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[k]), c), m) * back);
+    tmem_st16(sa + d, x);
   }
   tmem_wait_st();
 }
@@ -1342,7 +1360,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               scale_rows(o_base, O_COLS, a);
             }
           }
-          const float mz = m == -INFINITY ? 0.f : m;
+          float mz = m == -INFINITY ? 0.f : m;
+          if (__any_sync(0xffffffffu, fabsf(mz) > LARGE_SCORE)) {
+            center_scores(sa, S_COLS, p.c, mz);
+            mz = 0.f;
+          }
           const uint64_t cc = pair(p.c, p.c), mm = pair(-mz, -mz);
           uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
