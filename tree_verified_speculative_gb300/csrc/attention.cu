@@ -624,8 +624,20 @@ struct Scheduler {
 
   __device__ __forceinline__ void start(const Params &p, int lane) {
     int64_t begin, own = 0;
-    const bool one_pass = p.n_req <= 32 && one_form(p);  // a request a lane
-    if (one_pass) {
+    const bool one_pass = p.n_req <= 32;  // a request a lane
+    if (one_pass && !one_form(p)) {
+      for (int b = 0; b < p.n_req; ++b) {
+        int c, m;
+        if (!lengths(p, b, c, m) && blockIdx.x == 0 && lane == 0) report(p.status, MFD_ERR_INPUT);
+        const int64_t cost = p.cv.Hk * head_cost_warp<NS>(p, c, m, lane);
+        if (lane == b) {
+          own = cost;
+          ctx = c;
+          nn = m;
+        }
+        total = b ? total + cost : cost;
+      }
+    } else if (one_pass) {
       if (lane < p.n_req) {
         if (!lengths(p, lane, ctx, nn) && blockIdx.x == 0) report(p.status, MFD_ERR_INPUT);
         own = p.cv.Hk * head_cost<NS>(p, ctx, nn);
