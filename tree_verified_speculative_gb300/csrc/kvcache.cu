@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
   constexpr int RW = 32 / LR;  // rows of a warp at once
   pdl_launch_dependents();     // the attention that follows sets itself up meanwhile
   __shared__ float cos_s[MAX_D / 2], sin_s[MAX_D / 2];
-  __shared__ __align__(16) float own_s[2][MAX_D], other_s[2][MAX_D];  // w cos, +- w sin: queries, keys
+  // w cos and +- w sin of queries and of keys, [half of a chunk][chunk]:
+  // neighbouring lanes read neighbouring 16 bytes
+  __shared__ float4 own_s[2][2][MAX_D / 8], other_s[2][2][MAX_D / 8];
   __shared__ float row_s[ROT_SMEM ? WARPS * RW : 1][ROT_SMEM ? MAX_D : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & (LR - 1), sub = lane / LR;
@@ -151,8 +153,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        own_s[k][e] = w_own[i][k] * cs;
-        other_s[k][e] = w_other[i][k] * sn;
+        reinterpret_cast<float *>(&own_s[k][(e >> 2) & 1][e >> 3])[e & 3] = w_own[i][k] * cs;
+        reinterpret_cast<float *>(&other_s[k][(e >> 2) & 1][e >> 3])[e & 3] = w_other[i][k] * sn;
       }
     }
   }
@@ -208,9 +210,8 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
       for (int o = 1; o < LR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (!is_v && in_row) {
         const float r = (is_q ? p.q_w : p.k_w) ? rsqrtf(fmaf(ss, per_d, p.eps)) : 1.f;
-        const float4 *fo = reinterpret_cast<const float4 *>(own_s[is_q ? 0 : 1] + c * 8);
-        const float4 *ft = reinterpret_cast<const float4 *>(other_s[is_q ? 0 : 1] + c * 8);
-        const float4 a = fo[0], b = fo[1], d = ft[0], e = ft[1];
+        const int k = is_q ? 0 : 1;
+        const float4 a = own_s[k][0][c], b = own_s[k][1][c], d = other_s[k][0][c], e = other_s[k][1][c];
         x[0] = r * fmaf(xp[0], d.x, x[0] * a.x);
         x[1] = r * fmaf(xp[1], d.y, x[1] * a.y);
         x[2] = r * fmaf(xp[2], d.z, x[2] * a.z);
