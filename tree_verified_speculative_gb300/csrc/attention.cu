@@ -266,6 +266,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_global16(void *dst, uint4 v) {
   asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -1254,17 +1259,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           const int dn = STEP / p.G, dg = STEP - dn * p.G;
 #pragma unroll 1
           for (; i < have; i += 4 * STEP) {
-            uint4 x[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const int rr = base_row + i + b * STEP;
               const uint16_t *at = src + n1 * p.q_stride + g1 * cv.D;
-              if (i + b * STEP < have) {
-                if (E4M3)
-                  x[b] = __ldg(reinterpret_cast<const uint4 *>(at));
-                else
-                  cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), at);
-              }
+              if (i + b * STEP < have) cp_async16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), at);
               n1 += dn;
               g1 += dg;
               if (g1 >= p.G) {
@@ -1272,15 +1271,15 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
                 ++n1;
               }
             }
-            if (E4M3) {  // in the widened keys' order
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const int rr = base_row + i + b * STEP;
-                if (i + b * STEP < have)
-                  st_shared16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-                              make_uint4(__byte_perm(x[b].x, x[b].y, 0x7632), __byte_perm(x[b].x, x[b].y, 0x5410),
-                                         __byte_perm(x[b].z, x[b].w, 0x7632), __byte_perm(x[b].z, x[b].w, 0x5410)));
-              }
+          }
+          if (E4M3) {  // into the widened keys' order: a thread's own chunks, once they are here
+            cp_async_wait();
+#pragma unroll 4
+            for (int rr = base_row + r / C; rr < base_row + have; rr += STEP) {
+              const uint32_t at = dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+              const uint4 x = ld_shared16(at);
+              st_shared16(at, make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.x, x.y, 0x5410),
+                                         __byte_perm(x.z, x.w, 0x7632), __byte_perm(x.z, x.w, 0x5410)));
             }
           }
         }
