@@ -1407,6 +1407,10 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
           l += sum.x + sum.y;
           tmem_wait_st();
         }
+        // With one stream scores are two tiles ahead of the products, and the last
+        // but one may still run.  It is waited for before the last can start: a
+        // wait on a parity is for the one phase that is open.
+        if (NS == 1 && done && i + 1 == steps) wait(&pv_done[acc], (pv_n - 1u) & 1u);
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&p_full[slot]);
@@ -1415,9 +1419,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       }
 
       // ------------------------------------------------------- epilogue
-      // With one stream the last but one product may still run (scores are two
-      // tiles ahead of it); a wait on a parity needs the phase before it complete.
-      if (NS == 1 && done > 1) wait(&pv_done[acc], pv_n & 1u);
       if (done) wait(&pv_done[acc], (pv_n - 1u) & 1u);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
