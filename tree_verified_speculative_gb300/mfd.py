@@ -81,6 +81,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     """Load libmfd.so (or the library at `path`); raises if it is missing (no
     fallback)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -176,7 +178,7 @@ def _p_dev_or_pinned(t) -> int:
 
 def _s(stream) -> int | None:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -449,6 +451,15 @@ def _rows(t, heads, D):
     """(pointer, token stride) of a [..., tokens, heads, D] tensor whose heads
     are contiguous; all leading dimensions step by the token stride."""
     shape, strides = t.shape, t.stride()
+    if len(shape) == 4:  # the usual case, in few steps: a small call's time is this binding's
+        r, n, h, d = shape
+        sr, st, sh, sd = strides
+        if n == 1:
+            st = sr if r > 1 else heads * D
+        assert t.is_cuda and h == heads and d == D, "device tensor [..., tokens, heads, D]"
+        assert sd == 1 and (h == 1 or sh == D), "contiguous heads"
+        assert r == 1 or sr == n * st, "tokens at one stride"
+        return t.data_ptr(), st
     assert t.is_cuda and len(shape) >= 3 and shape[-1] == D and shape[-2] == heads, "device tensor [..., tokens, heads, D]"
     assert strides[-1] == 1 and (heads == 1 or strides[-2] == D), "contiguous heads"
     n, st = shape[-3], strides[-3]
@@ -485,25 +496,27 @@ def mfd_kv_append(q, k, v, q_w, k_w, eps, phase, rot_dim, interleaved, pos, ctx_
     """Norm and rotation of q, k [n_req, N, heads, D], with k and v written
     into `cache` (KVCache) at positions ctx_len[q] + n.  q and q_out may be
     None (the cache write alone), and n_nodes (all N rows live)."""
-    n_req, N, Hk, D = k.shape
-    assert v.shape == k.shape and v.dtype == k.dtype and (Hk, D) == (cache.Hk, cache.D)
-    assert n_req == cache.n_req and tuple(pos.shape) == (n_req, N) and pos.dtype == torch.int32
-    assert ctx_len.dtype == torch.int32 and ctx_len.numel() == n_req
-    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == n_req)
-    for w in (q_w, k_w):
-        assert w is None or (w.dtype == k.dtype and w.numel() == D), "norm weights [D] of k's type"
+    shape, dt, i32 = k.shape, k.dtype, torch.int32
+    n_req, N, Hk, D = shape
+    assert v.shape == shape and v.dtype is dt and Hk == cache.Hk and D == cache.D
+    assert n_req == cache.n_req and pos.shape == shape[:2] and pos.dtype is i32
+    assert ctx_len.dtype is i32 and ctx_len.numel() == n_req
+    assert n_nodes is None or (n_nodes.dtype is i32 and n_nodes.numel() == n_req)
+    assert q_w is None or (q_w.dtype is dt and q_w.numel() == D), "norm weights [D] of k's type"
+    assert k_w is None or (k_w.dtype is dt and k_w.numel() == D), "norm weights [D] of k's type"
     assert phase is None or phase.numel() >= rot_dim // 2
-    Hq, qp, qs = 0, None, 0
+    Hq, qp, qs, op = 0, None, 0, None
     if q is not None:
-        Hq = q.shape[2]
-        assert tuple(q.shape) == (n_req, N, Hq, D) and q.dtype == k.dtype
-        assert q_out.shape == q.shape and q_out.dtype == q.dtype
+        rows = q.shape
+        Hq = rows[2]
+        assert rows[:2] == shape[:2] and q.dtype is dt
+        assert q_out.shape == rows and q_out.dtype is dt
         qp, qs = _rows(q, Hq, D)
+        op = _p(q_out)
     (kp, ks), (vp, vs) = _rows(k, Hk, D), _rows(v, Hk, D)
-    rc = load().mfd_kv_append(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hq, _p(q_w), _p(k_w), eps,
-                              _p(phase) if rot_dim else None, rot_dim, int(interleaved), _p(pos), _p(ctx_len),
-                              _p(n_nodes), _p(q_out) if q is not None else None, cache._c, _p(status),
-                              _s(stream))
+    rc = load().mfd_kv_append(qp, qs, kp, ks, vp, vs, _DTYPE[dt], n_req, N, Hq, _p(q_w), _p(k_w), eps,
+                              _p(phase) if rot_dim else None, rot_dim, 1 if interleaved else 0, _p(pos), _p(ctx_len),
+                              _p(n_nodes), op, cache._c, _p(status), _s(stream))
     _check(rc, "mfd_kv_append")
 
 
