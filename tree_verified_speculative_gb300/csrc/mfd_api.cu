@@ -716,42 +716,26 @@ int cache_view(const mfd_kv_cache *c, mfd::CacheView *out) {
   return MFD_OK;
 }
 
-using KvMapKey = std::tuple<int, const void *, int, int, int, int, int, int64_t, int64_t, int64_t, int>;
-std::map<KvMapKey, CUtensorMap> g_kv_maps;
-
 // Keys or values as a 4-D tensor (D, slot, head, page).  A 16-bit cache's box
 // is 64 columns x `rows` slots of one head and page with the 128-byte swizzle
 // (columns past D read as zero); an E4M3 one's is D or 128 columns x `rows`
 // slots as they are.
 int kv_map(const void *ptr, const mfd::CacheView &c, int rows, CUtensorMap *out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MFD_ERR_CUDA;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return MFD_ERR_CUDA;
   const bool e4m3 = c.dtype == MFD_E4M3;
   const int esz = e4m3 ? 1 : 2;
-  std::lock_guard<std::mutex> lk(g_mu);
-  const KvMapKey key{dev, ptr, c.dtype, c.D, 1 << c.ps_shift, c.Hk, c.n_pages, c.token_stride, c.head_stride, c.page_stride, rows};
-  auto it = g_kv_maps.find(key);
-  if (it == g_kv_maps.end()) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return MFD_ERR_CUDA;
-    CUtensorMap m;
-    std::memset(&m, 0, sizeof m);
-    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)1 << c.ps_shift, (cuuint64_t)c.Hk, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)(c.token_stride * esz), (cuuint64_t)(c.head_stride * esz),
-                                   (cuuint64_t)(c.page_stride * esz)};
-    const cuuint32_t box[4] = {(cuuint32_t)(!e4m3 ? 64 : c.D < 128 ? c.D : 128), (cuuint32_t)rows, 1u, 1u};
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    const CUresult r = fn(&m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : c.dtype == MFD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return MFD_ERR_CUDA;
-    if (g_kv_maps.size() > 4096) g_kv_maps.clear();
-    it = g_kv_maps.emplace(key, m).first;
-  }
-  *out = it->second;
-  return MFD_OK;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)1 << c.ps_shift, (cuuint64_t)c.Hk, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)(c.token_stride * esz), (cuuint64_t)(c.head_stride * esz),
+                                 (cuuint64_t)(c.page_stride * esz)};
+  const cuuint32_t box[4] = {(cuuint32_t)(!e4m3 ? 64 : c.D < 128 ? c.D : 128), (cuuint32_t)rows, 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = fn(out, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : c.dtype == MFD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MFD_OK : MFD_ERR_CUDA;
 }
 
 int need_sm103() {
