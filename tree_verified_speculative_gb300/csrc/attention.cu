@@ -23,7 +23,9 @@
 // both read every key and value tile.  Rows for one tile ("alternating"): the
 // streams take the key and value tiles in turn with a maximum, sum and O each,
 // joined at the end.  Heads wider than 128 leave tensor memory for one O:
-// one stream, with two S accumulators used in turn.
+// one stream, with two S accumulators used in turn; a 16-bit cache's has two
+// softmax warpgroups, each with half of a row's columns (an 8-bit cache's
+// helpers leave no room for the second).
 //
 // Work split.  All (request, key head, row tile pair) items and their key
 // tiles form one line, ordered so that the row tiles of a head, which read
@@ -33,12 +35,29 @@
 // the device: a short and a long request keep all SMs busy alike, and a graph
 // replays with other lengths.
 //
-// Warps: 0 loads (TMA, one box per page and 64 columns), 1 issues the MMAs,
-// 4-7 and 8-11 softmax, the last four help: they turn E4M3 tiles into the
-// operand type, and, in tiles that reach past the context, clear value rows
-// past the end and values that are not finite, which a product would spread
-// to rows that do not see them (0 * NaN); a cleared value's node is noted and
-// added back for the rows that do see it.
+// Warps: 0 loads keys and 3 values (TMA, one box per page and 64 columns), 1
+// issues the MMAs, 2 makes the list of work and turns E4M3 rows' exponent bytes
+// into powers, then the softmax warpgroups, then the helpers: two warpgroups
+// that widen E4M3 tiles to the operand type, or one that goes over value tiles
+// of 16-bit caches that reach past the context.  There it clears rows past the
+// end and values that are not finite, which a product would spread to rows that
+// do not see them (0 * NaN); a cleared value's node is noted and added back for
+// the rows that do see it.
+//
+// What bounds it, on the GPU alone (a captured call replayed):
+//   one token over 200,002 positions, 32/8 heads of 128, bf16: HBM; 132 us, 6.2
+//     TB/s, 0.91 of what a copy reaches
+//   32 requests of one token over ragged contexts up to 16,000, the same heads,
+//     E4M3: the widening; 239 us, 3.1 TB/s, each byte read being one
+//     element to turn into two bytes (two helper warpgroups; one: 297 us)
+//   32 trees of 129 nodes over up to 6,000, the same heads, E4M3: a stream's
+//     chain of scores, softmax and product; 402 us, 0.69 PFLOP/s.  A step of 128
+//     rows and 128 keys takes 2,900 cycles of which the tensor pipe needs 1,024;
+//     neither issue slots (51 %) nor exponentials (16 %) are used up
+//   one tree of 257 nodes over 8,191, 16/4 heads of 256, bf16: 60 us; of that
+//     the pipelines' filling, the cut items' parts (20 MB) and their join take
+//     half, the products 0.58 PFLOP/s over the whole
+//   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 132 us
 #include <atomic>
 
 #include "kvcache.h"
@@ -55,7 +74,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 // What an item's start and end cost, in steps: the queries' load, the pipeline's
 // filling and draining, the output.  Measured, three prompts of 1,777 rows: 153
-// us with 1, 133 with 4, 137 with 6; 32 trees of 129 nodes: 413, 404, 399.
+// us with 1, 133 with 4, 137 with 6; 32 trees of 129 nodes (before later steps):
+// 413, 404, 399.
 constexpr int START_COST = 5;
 constexpr float LARGE_SCORE = 65536.f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
@@ -973,9 +993,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   if (warp < 4) {
     if (warp == 0 || warp == 3) {
       // ------------------------------------------------------- loads
-      // Warp 0 the keys, warp 3 the values: one warp for both took longer over
-      // a tile (its pages, waits and copies, about 1.6 us a unit of small pages)
-      // than the rest of the SM.
+      // Warp 0 the keys, warp 3 the values: one warp for both took about 1.6 us
+      // over a unit of small pages (looking them up, waits, copies), longer than
+      // the rest of the SM over the tile.
       const bool is_v = warp == 3;
       const CUtensorMap *map = is_v ? &map_v : &map_k;
       // Keys and values of one token serve M rows of this CTA only, or of
@@ -1648,7 +1668,9 @@ constexpr int JOIN_ROWS = 16;
 // Combines the parts of the items that borders cut.  Block (c, y): the item
 // whose first part CTA c holds, if any, and 16 of its rows; first every part's
 // weight 2^(m - max m) / sum for these rows, then a thread for each row and 8
-// columns adds the parts up in their order.
+// columns adds the parts up in their order, whatever CTA was done first.  It
+// waits for its loads: 3.4 us of the 15 us of one token over 700 positions, with
+// the launch, which overlaps the attention's end.
 template <typename T, int NS>
 __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
