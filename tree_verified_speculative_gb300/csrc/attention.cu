@@ -45,11 +45,11 @@
 // the rows that do see it.
 //
 // What bounds it, on the GPU alone (a captured call replayed):
-//   one token over 200,002 positions, 32/8 heads of 128, bf16: HBM; 132 us, 6.2
-//     TB/s, 0.91 of what a copy reaches
+//   one token over 200,002 positions, 32/8 heads of 128, bf16: HBM; 129 us, 6.4
+//     TB/s, 0.94 of what a copy reaches
 //   32 requests of one token over ragged contexts up to 16,000, the same heads,
-//     E4M3: the widening; 239 us, 3.1 TB/s, each byte read being one
-//     element to turn into two bytes (two helper warpgroups; one: 297 us)
+//     E4M3: the widening; 234 us, 3.2 TB/s, each byte read being one
+//     element to turn into two bytes (one helper warpgroup instead of two: 297)
 //   32 trees of 129 nodes over up to 6,000, the same heads, E4M3: a stream's
 //     chain of scores, softmax and product; 402 us, 0.69 PFLOP/s.  A step of 128
 //     rows and 128 keys takes 2,900 cycles of which the tensor pipe needs 1,024;
@@ -57,7 +57,8 @@
 //   one tree of 257 nodes over 8,191, 16/4 heads of 256, bf16: 60 us; of that
 //     the pipelines' filling, the cut items' parts (20 MB) and their join take
 //     half, the products 0.58 PFLOP/s over the whole
-//   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 132 us
+//   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 133 us, the same
+//     chain, and starts and ends of items of ten tiles
 #include <atomic>
 
 #include "kvcache.h"
@@ -1666,42 +1667,52 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
 constexpr int JOIN_ROWS = 16;
 
 // Combines the parts of the items that borders cut.  Block (c, y): the item
-// whose first part CTA c holds, if any, and 16 of its rows; first every part's
-// weight 2^(m - max m) / sum for these rows, then a thread for each row and 8
-// columns adds the parts up in their order, whatever CTA was done first.  It
-// waits for its loads: 3.4 us of the 15 us of one token over 700 positions, with
-// the launch, which overlaps the attention's end.
+// whose first part CTA c holds, if any, and 16 of its rows: first the notes of
+// the CTAs that may hold parts, then every part's (m, l), from which its weight
+// 2^(m - max m) / sum comes, then the parts' O.  A thread adds up one row's 8
+// columns, and where the block has few rows (one token) several threads share
+// the parts; the order is the parts', whatever CTA was done first.  It waits for
+// its loads, one round after the other: it is 5 us of the 14 of one token over
+// 700 positions (nine parts for each of 8 heads), 7 of the 129 over 200,002
+// (19 each), 10 of one tree's 59, whose parts are 20 MB.
 template <typename T, int NS>
 __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
   __shared__ int slot_s[ATTENTION_MAX_CTAS];
-  const int tid = threadIdx.x, lane = tid & 31, threads = JOIN_ROWS * (p.cv.D / 8);
+  __shared__ float4 sum_s[2][JOIN_ROWS * 32];
+  const int tid = threadIdx.x, lane = tid & 31, chunks = p.cv.D / 8, threads = JOIN_ROWS * chunks;
   pdl_launch_dependents();
   pdl_wait();  // the parts are written
   const int c0 = blockIdx.x;
   const Cut cut = p.cuts[c0];
   const int n_part = cut.reach, q = cut.q, h = cut.h;
-  const int first = cut.pair * NS * BM;
-  const int rows = min(cut.nn * p.G - first, NS * BM);
-  const int row0 = (int)blockIdx.y * JOIN_ROWS;
-  if (n_part == 0 || row0 >= rows) return;
   // each part's slot, or -1 where a CTA's stretch of the item holds no key tile
-  for (int i = tid; i < n_part; i += threads)
-    slot_s[i] = i == 0 ? 2 * c0 + 1 : p.cuts[c0 + i].has[0] ? 2 * (c0 + i) : -1;
+  auto note = [&](int i) { slot_s[i] = i == 0 ? 2 * c0 + 1 : p.cuts[c0 + i].has[0] ? 2 * (c0 + i) : -1; };
+  if (tid < 8 && c0 + tid < (int)gridDim.x) note(tid);  // before it is known how many there are
+  const int first = cut.pair * NS * BM;
+  const int row0 = (int)blockIdx.y * JOIN_ROWS;
+  const int rows = min(min(cut.nn * p.G - first, NS * BM) - row0, JOIN_ROWS);  // of this block
+  if (n_part == 0 || rows <= 0) return;
+  for (int i = 8 + tid; i < n_part; i += threads) note(i);
   __syncthreads();
-  // weights: D / 8 threads (a power of two of them, at most 16) for each row
+  // a thread's row, columns, and every `groups`th part from its own
+  const int per = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;  // 1, 2, 4, 8 or 16
+  const int groups = JOIN_ROWS / per;
+  const int r = tid % per, ch = tid / per % chunks, group = tid / per / chunks;
+  const bool have = r < rows;
+  // weights: G threads for each row
   const int G = p.cv.D >= 128 ? 16 : p.cv.D >= 64 ? 8 : p.cv.D >= 32 ? 4 : 2;
   if (tid < JOIN_ROWS * G) {
     const int r = tid / G, j = tid % G, row = row0 + r;
-    const unsigned group = (G == 32 ? 0xffffffffu : ((1u << G) - 1u)) << (lane / G * G);
+    const unsigned peers = ((1u << G) - 1u) << (lane / G * G);
     float m = -INFINITY;
     for (int i = j; i < n_part; i += G)
-      if (slot_s[i] >= 0 && row < rows) m = fmaxf(m, p.part_ml[(int64_t)slot_s[i] * p.part_rows + row].x);
-    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, o));
+      if (slot_s[i] >= 0 && r < rows) m = fmaxf(m, p.part_ml[(int64_t)slot_s[i] * p.part_rows + row].x);
+    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(peers, m, o));
     float l = 0.f;
     for (int i = j; i < n_part; i += G) {
       float w = 0.f;
-      if (slot_s[i] >= 0 && row < rows) {
+      if (slot_s[i] >= 0 && r < rows) {
         const float2 ml = p.part_ml[(int64_t)slot_s[i] * p.part_rows + row];
         // a part whose keys are not seen has sum 0; one whose scores are NaN a NaN
         w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : ex2(ml.x - m);
@@ -1709,27 +1720,24 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
       }
       w_s[i][r] = w;
     }
-    for (int o = G / 2; o > 0; o >>= 1) l += __shfl_xor_sync(group, l, o);
+    for (int o = G / 2; o > 0; o >>= 1) l += __shfl_xor_sync(peers, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     for (int i = j; i < n_part; i += G) w_s[i][r] *= inv;
-    if (row < rows && p.lse && j == 0) {
+    if (r < rows && p.lse && j == 0) {
       const int node = (first + row) / p.G, g = first + row - node * p.G;
       p.lse[((int64_t)q * p.N + node) * p.Hq + h * p.G + g] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
     }
   }
   __syncthreads();
-  const int r = tid % JOIN_ROWS, ch = tid / JOIN_ROWS, row = row0 + r;
-  if (row >= rows) return;
   float acc[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < n_part; ++i) {
-    const int s = slot_s[i];
-    const float w = w_s[i][r];
-    if (s < 0 || w == 0.f) continue;
-    const float4 a = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch) * p.part_rows + row];
-    const float4 b = p.part_o[((int64_t)s * (p.cv.D / 4) + 2 * ch + 1) * p.part_rows + row];
+  for (int i = group; i < n_part; i += groups) {
+    const float w = have ? w_s[i][r] : 0.f;  // 0 where there is no part
+    if (w == 0.f) continue;
+    const float4 *o = p.part_o + ((int64_t)slot_s[i] * (p.cv.D / 4) + 2 * ch) * p.part_rows + row0 + r;
+    const float4 a = o[0], b = o[p.part_rows];
     acc[0] = fmaf(w, a.x, acc[0]);
     acc[1] = fmaf(w, a.y, acc[1]);
     acc[2] = fmaf(w, a.z, acc[2]);
@@ -1739,7 +1747,25 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
     acc[6] = fmaf(w, b.z, acc[6]);
     acc[7] = fmaf(w, b.w, acc[7]);
   }
-  const int node = (first + row) / p.G, g = first + row - node * p.G;
+  if (groups > 1) {
+    sum_s[0][tid] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    sum_s[1][tid] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    __syncthreads();
+    if (group > 0) return;
+    for (int k = 1; k < groups; ++k) {
+      const float4 x = sum_s[0][tid + k * per * chunks], y = sum_s[1][tid + k * per * chunks];
+      acc[0] += x.x;
+      acc[1] += x.y;
+      acc[2] += x.z;
+      acc[3] += x.w;
+      acc[4] += y.x;
+      acc[5] += y.y;
+      acc[6] += y.z;
+      acc[7] += y.w;
+    }
+  }
+  if (!have) return;
+  const int node = (first + row0 + r) / p.G, g = first + row0 + r - node * p.G;
   *reinterpret_cast<uint4 *>(p.out + (((int64_t)q * p.N + node) * p.Hq + h * p.G + g) * p.cv.D + ch * 8) = pack8<T>(acc);
 }
 
