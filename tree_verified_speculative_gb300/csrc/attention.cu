@@ -1005,25 +1005,27 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       const int row_shift = min(cv.ps_shift, 7), rows = 1 << row_shift;  // of a box
       const uint32_t wide = E4M3 ? (uint32_t)min(cv.D, SH::UC) : 128u;   // bytes of a row in the unit
       constexpr uint32_t RING = E4M3 ? RN : ST, UNIT = E4M3 ? SH::RAW : SH::STAGE;
+      // The ring's places are both warps' in the units' order (16-bit caches: the
+      // ring that the MMAs read), or half of them each warp's own (8-bit ones).
+      const uint32_t st0 = E4M3 && is_v ? RN / 2 : 0, st1 = E4M3 ? st0 + RN / 2 : ST;
       const uint32_t ring = smem_u32(E4M3 ? sR : sT), ready = smem_u32(E4M3 ? raw_full : full);
       uint64_t *freed = E4M3 ? raw_empty : empty;
-      uint32_t st = 0, par = 0;  // ring place and its phase
+      uint32_t st = st0, par = 0;  // ring place and its phase
       uint32_t special_par = 0, issued = 0, issued_special = 0, issued_par = 0;
       auto next_place = [&]() {
-        if (++st == RING) {
-          st = 0;
+        if (++st == st1) {
+          st = st0;
           par ^= 1u;
         }
       };
-      // Past the other warp's units.  A wait for a place must not come a phase
-      // early, when the parity of the phase before last would pass for it.  The
-      // MMAs free places in order, so this warp's last wait vouches for that; the
-      // two groups of helpers do not, and their frees are waited for one by one.
+      // Past the other warp's units in the shared ring.  A wait for a place must
+      // not come a phase early or late, when a parity passes for another phase's:
+      // the MMAs free places in order, and no two units of a warp are further apart
+      // than the ring is long, so its last wait vouches for the phase before last.
+      // The two groups of helpers free places in no common order, so in the 8-bit
+      // rings every place's every phase is waited for by the warp that fills it.
       auto skip = [&](int units) {
-        for (; units > 0; --units) {
-          if (E4M3) wait(&freed[st], par ^ 1u);
-          next_place();
-        }
+        for (; !E4M3 && units > 0; --units) next_place();
       };
       while (next_segment_warp()) {
         const int nt = s.t1 - s.t0;
@@ -1555,7 +1557,12 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     // E4M3: the two warpgroups take the units in turn
     const int ht = (tid - SH::HELP_WARP * 32) & 127, hg = (tid - SH::HELP_WARP * 32) >> 7;
     uint32_t unit = 0;
-    uint32_t st = 0, par = 0, rs = 0, rpar = 0;  // places in the rings and their phases
+    uint32_t st = 0, par = 0;  // place in the MMAs' ring and its phase
+    // The same in the loaders' rings of keys and of values.  A group waits only for
+    // its own units there; by then the MMAs have read the unit a ring of theirs
+    // before, so the place's previous unit was loaded (with two units a tile, it
+    // was the group's own).
+    uint32_t rk = 0, rk_par = 0, rv = RN / 2, rv_par = 0;
     uint32_t special_par = 0, pow_n = 0;
     int seg = 0;
     while (next_segment_warp()) {
@@ -1584,11 +1591,17 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const uint32_t pn = pow_n + j;
 #pragma unroll 1
         for (int u = 0; u < NU; ++u) {
+          const uint32_t rs = is_v ? rv : rk, rpar = is_v ? rv_par : rk_par;
+          if (E4M3 && is_v && ++rv == RN) {
+            rv = RN / 2;
+            rv_par ^= 1u;
+          }
+          if (E4M3 && !is_v && ++rk == RN / 2) {
+            rk = 0;
+            rk_par ^= 1u;
+          }
           if (E4M3 && (int)(unit++ & 1u) != hg) {
-            if (++rs == RN) {
-              rs = 0;
-              rpar ^= 1u;
-            }
+            // the other group's
           } else if (E4M3) {
             wait(&pow_full[pn & 3], (pn >> 2) & 1u);
             wait(&empty[st], par ^ 1u);
@@ -1606,10 +1619,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               mbar_arrive(&raw_empty[rs]);
               mbar_arrive(&full[st]);
               mbar_arrive(&pow_empty[pn & 3]);
-            }
-            if (++rs == RN) {
-              rs = 0;
-              rpar ^= 1u;
             }
           } else if (sp) {
             wait(&special[st], (special_par >> st) & 1u);
