@@ -164,8 +164,12 @@ def status_string(code: int) -> str:
 def _p(t) -> int | None:
     if t is None:
         return None
-    assert isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous(), "device tensors, contiguous"
-    return t.data_ptr()
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    raise AssertionError("device tensors, contiguous")
 
 
 def _p_dev_or_pinned(t) -> int:
@@ -513,7 +517,12 @@ def mfd_kv_append(q, k, v, q_w, k_w, eps, phase, rot_dim, interleaved, pos, ctx_
         assert q_out.shape == rows and q_out.dtype is dt
         qp, qs = _rows(q, Hq, D)
         op = _p(q_out)
-    (kp, ks), (vp, vs) = _rows(k, Hk, D), _rows(v, Hk, D)
+    kp, ks = _rows(k, Hk, D)
+    if v.stride() == k.stride():
+        assert v.is_cuda, "device tensor [..., tokens, heads, D]"
+        vp, vs = v.data_ptr(), ks
+    else:
+        vp, vs = _rows(v, Hk, D)
     rc = load().mfd_kv_append(qp, qs, kp, ks, vp, vs, _DTYPE[dt], n_req, N, Hq, _p(q_w), _p(k_w), eps,
                               _p(phase) if rot_dim else None, rot_dim, 1 if interleaved else 0, _p(pos), _p(ctx_len),
                               _p(n_nodes), op, cache._c, _p(status), _s(stream))
@@ -537,10 +546,10 @@ def mfd_kv_commit(cache, ctx_len, accept_len, path_nodes, n_nodes, new_len, stat
     """Moves the accepted path's entries (mfd_verify's accept_len and
     path_nodes) behind the context; new_len may be ctx_len."""
     n_req, L1 = path_nodes.shape
-    assert n_req == cache.n_req
+    i32 = torch.int32
+    assert n_req == cache.n_req and path_nodes.dtype is i32
     for t in (ctx_len, accept_len, n_nodes, new_len):
-        assert t.dtype == torch.int32 and t.numel() == n_req
-    assert path_nodes.dtype == torch.int32
+        assert t.dtype is i32 and t.numel() == n_req
     rc = load().mfd_kv_commit(cache._c, n_req, L1 - 1, _p(ctx_len), _p(accept_len), _p(path_nodes),
                               _p(n_nodes), _p(new_len), _p(status), _s(stream))
     _check(rc, "mfd_kv_commit")
@@ -554,14 +563,15 @@ def mfd_tree_attention(q, cache, ctx_len, n_nodes, mask, scale, out, lse, status
     """Attention of q [n_req, N, Hq, D] over `cache` under the tree mask
     (int32 words [n_req, N, ceil(N / 32)]; None: causal) into out (q's shape)
     and lse (fp32 [n_req, N, Hq], or None)."""
-    n_req, N, Hq, D = q.shape
-    assert n_req == cache.n_req and D == cache.D and out.shape == q.shape and out.dtype == q.dtype
-    assert ctx_len.dtype == torch.int32 and ctx_len.numel() == n_req
-    assert n_nodes is None or (n_nodes.dtype == torch.int32 and n_nodes.numel() == n_req)
-    assert mask is None or (mask.dtype == torch.int32 and tuple(mask.shape) == (n_req, N, (N + 31) // 32))
-    assert lse is None or (lse.dtype == torch.float32 and lse.numel() == n_req * N * Hq)
+    shape, dt, i32 = q.shape, q.dtype, torch.int32
+    n_req, N, Hq, D = shape
+    assert n_req == cache.n_req and D == cache.D and out.shape == shape and out.dtype is dt
+    assert ctx_len.dtype is i32 and ctx_len.numel() == n_req
+    assert n_nodes is None or (n_nodes.dtype is i32 and n_nodes.numel() == n_req)
+    assert mask is None or (mask.dtype is i32 and tuple(mask.shape) == (n_req, N, (N + 31) // 32))
+    assert lse is None or (lse.dtype is torch.float32 and lse.numel() == n_req * N * Hq)
     qp, qs = _rows(q, Hq, D)
-    rc = load().mfd_tree_attention(qp, qs, _DTYPE[q.dtype], n_req, N, Hq, cache._c, _p(ctx_len),
+    rc = load().mfd_tree_attention(qp, qs, _DTYPE[dt], n_req, N, Hq, cache._c, _p(ctx_len),
                                    _p(n_nodes), _p(mask), scale, _p(out), _p(lse), _p(status), _p(ws),
                                    ws.numel() * ws.element_size(), _s(stream))
     _check(rc, "mfd_tree_attention")
