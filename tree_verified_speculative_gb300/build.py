@@ -20,7 +20,7 @@ LIB_CHECKED = os.path.join(BUILD, "libmfd_checked.so")
 SOURCES = ["lmhead.cu", "topk.cu", "tree.cu", "verify.cu", "analytics.cu", "kvcache.cu", "attention.cu",
            "mfd_api.cu"]
 CHECKED_SOURCES = ["tree.cu"]  # the sources with bounds checks under -DMFD_CHECKED
-HEADERS = ["lmhead.h", "kvcache.h", "mfd_device.cuh"]
+HEADERS = ["lmhead.h", "kvcache.h", "join_note.h", "mfd_device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -61,6 +61,7 @@
 //     chain, and starts and ends of items of ten tiles
 #include <atomic>
 
+#include "join_note.h"
 #include "kvcache.h"
 #include "mfd_device.cuh"
 
@@ -81,15 +82,6 @@ constexpr int START_COST = 5;
 constexpr float LARGE_SCORE = 65536.f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
 
-// What a CTA leaves for the join: whether it holds parts (of the item its
-// stretch starts in, of the one it ends in), and of the latter, if this CTA has
-// its first part, where it is and how many CTAs it reaches over.
-struct Cut {
-  int has[2];
-  int reach;  // 0: no first part
-  int q, h, pair, nn;
-};
-
 struct Params {
   CacheView cv;
   const uint16_t *q;
@@ -105,7 +97,7 @@ struct Params {
   float4 *part_o;   // [slot][D / 4][part_rows]
   float2 *part_ml;  // [slot][part_rows]
   int part_rows;
-  struct Cut *cuts;  // [CTA]
+  Cut *cuts;  // [CTA]
 };
 
 template <int DP_, bool E4M3_>
@@ -898,7 +890,11 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   const CacheView &cv = p.cv;
 
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles start on 1024-byte borders
-    if (tid == 0) report(p.status, MFD_ERR_CUDA);
+    pdl_wait();  // the grid before may still read its notes
+    if (tid == 0) {
+      p.cuts[blockIdx.x] = Cut{};
+      report(p.status, MFD_ERR_CUDA);
+    }
     return;
   }
   pdl_launch_dependents();
@@ -1169,6 +1165,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       // ------------------------------------------------- list of work
       // E4M3: also the exponent bytes of every tile's positions, four a lane, as powers
       // for the helpers.
+      if (lane == 0) p.cuts[blockIdx.x] = Cut{};  // stands if a wait runs out before the list's end
       sched.start(p, lane);
       uint32_t n = 0;
       int seg = 0;
@@ -1694,6 +1691,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   pdl_wait();  // the parts are written
   const int c0 = blockIdx.x;
   const Cut cut = p.cuts[c0];
+  const bool usable = cut_usable(cut, c0, (int)gridDim.x, p.n_req, p.cv.Hk, p.n_pair, p.N);
   const int n_part = cut.reach, q = cut.q, h = cut.h;
   // each part's slot, or -1 where a CTA's stretch of the item holds no key tile
   auto note = [&](int i) { slot_s[i] = i == 0 ? 2 * c0 + 1 : p.cuts[c0 + i].has[0] ? 2 * (c0 + i) : -1; };
@@ -1701,7 +1699,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   const int first = cut.pair * NS * BM;
   const int row0 = (int)blockIdx.y * JOIN_ROWS;
   const int rows = min(min(cut.nn * p.G - first, NS * BM) - row0, JOIN_ROWS);  // of this block
-  if (n_part == 0 || rows <= 0) return;
+  if (!usable || rows <= 0) return;
   for (int i = 8 + tid; i < n_part; i += threads) note(i);
   __syncthreads();
   // a thread's row, columns, and every `groups`th part from its own

@@ -1,0 +1,30 @@
+// join_note.h -- what a CTA of the attention leaves for the join, and when the
+// join may use it.  No CUDA header is needed, so host code can check it too.
+#pragma once
+
+#ifdef __CUDACC__
+#define MFD_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define MFD_HOST_DEVICE inline
+#endif
+
+namespace mfd {
+
+// Whether a CTA holds parts (of the item its stretch starts in, of the one it
+// ends in), and of the latter, if this CTA has its first part, where it is and
+// how many CTAs it reaches over.  All zeros: nothing to join.
+struct Cut {
+  int has[2];
+  int reach;  // 0: no first part
+  int q, h, pair, nn;
+};
+
+// Whether CTA `cta` of n_cta left the first part of an item of this call.  The
+// note lies in scratch that nobody zeroes, and its numbers become bounds and
+// addresses: a note that is not of this call must never be followed.
+MFD_HOST_DEVICE bool cut_usable(const Cut &c, int cta, int n_cta, int n_req, int Hk, int n_pair, int N) {
+  return c.reach > 0 && c.reach <= n_cta - cta && c.q >= 0 && c.q < n_req && c.h >= 0 && c.h < Hk && c.pair >= 0 &&
+         c.pair < n_pair && c.nn > 0 && c.nn <= N;
+}
+
+}  // namespace mfd
