@@ -88,7 +88,6 @@ struct Params {
   int64_t q_stride;
   int n_req, N, Hq, G, M, W32;
   int n_pair;  // row tile groups of an item line
-  int hides;   // a live row may not see an entry before the end: not so for one row without a mask
   const int32_t *ctx_len, *n_nodes;
   const uint32_t *mask;
   float c;  // scale * log2 e
@@ -1174,7 +1173,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const int nt = s.t1 - s.t0;
         if (!E4M3 || nt == 0) continue;
         const int len = s.ctx + s.nn;
-        const bool note = p.hides;
+        const bool note = p.N > 1 || p.mask;
         bool clean = false;
         const int32_t *table = cv.table + (size_t)s.q * cv.max_pages;
         auto page_at = [&](int t) { return t < min(len, s.t1 * BN) ? __ldg(table + (t >> cv.ps_shift)) : -1; };
@@ -1480,7 +1479,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
         const uint32_t from = alternating ? lane_base + SH::TM_O : o_base - (SPLIT ? ws * O_COLS : 0);
         const int64_t at = row_live ? ((int64_t)s.q * p.N + node) * p.Hq + s.h * p.G + g : 0;
         const int part = 2 * (int)blockIdx.x + (s.t0 == 0 ? 1 : 0);
-        const bool fix = p.hides && s.t1 * BN > s.ctx && *any_bad;
+        const bool fix = (p.N > 1 || p.mask) && s.t1 * BN > s.ctx && *any_bad;
         float4 *po = p.part_o + (int64_t)part * (cv.D / 4) * p.part_rows + rt * BM + r;
         // a row's place: 16 columns are 32 bytes of the output, or 4 of its
         // part's float4, each the rows' length from the next
@@ -1539,7 +1538,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       tc_fence_before();
       if (alternating) named_sync(1, 256);  // each has read the other's O and (m, l)
       tc_fence_after();
-      if (p.hides) {  // the noted nodes are read: the helpers may clear them
+      if (p.N > 1 || p.mask) {  // the noted nodes are read: the helpers may clear them
         if (ws == 0)
           named_sync(2, 128);
         else
@@ -1568,7 +1567,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
       if (nt == 0) continue;
       const bool turns = s.active != 2;
       const int len = s.ctx + s.nn;
-      const bool note = p.hides;
+      // one row without a mask sees every key before the end
+      const bool note = p.N > 1 || p.mask;
       bool clean = false;  // the bad-node bits are this segment's
       // bf16 and fp16: only value tiles that reach past the context
       for (int i = 0; i < 2 * nt; ++i) {
@@ -1845,7 +1845,6 @@ cudaError_t launch_tree_attention(const AttentionLaunch &A, cudaStream_t stream)
   p.ctx_len = A.ctx_len;
   p.n_nodes = A.n_nodes;
   p.mask = A.mask;
-  p.hides = A.N > 1 || A.mask;
   p.c = A.scale * LOG2E;
   p.out = static_cast<uint16_t *>(A.out);
   p.lse = A.lse;
