@@ -430,6 +430,8 @@ int mfd_kv_commit(const mfd_kv_cache *cache, int n_req, int L, const int32_t *ct
  *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t)
  * A row that sees nothing, or past n_nodes, gets zeros and lse -inf.  What a
  * row does not see does not reach it, infinities and NaN included.
+ * Keys and values of an E4M3 cache are those that mfd_kv_read gives in `dtype`:
+ * one past its range is an infinity.
  *   q     [n_req * N] tokens of [Hq][D], q_stride elements apart (as above),
  *         `dtype` MFD_BF16 or MFD_FP16; the cache's type, or any over MFD_E4M3
  *   mask  uint32 [n_req][N][ceil(N / 32)] from mfd_build_tree, or NULL (causal)

@@ -60,6 +60,7 @@
 //   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 133 us, the same
 //     chain, and starts and ends of items of ten tiles
 #include <atomic>
+#include <climits>
 
 #include "join_note.h"
 #include "kvcache.h"
@@ -444,6 +445,28 @@ __device__ __forceinline__ uint32_t nonfinite2<__half>(uint32_t w) {
   return ((w & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
 }
 
+// Whether some of eight elements are not finite, and the eight without those.
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(const uint4 &x) {
+  return (nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w)) != 0;
+}
+template <typename T>
+__device__ __forceinline__ uint4 without_nonfinite(const uint4 &x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t z = nonfinite2<T>(w[e]);
+    if (z & 0x8000u) w[e] &= 0xFFFF0000u;
+    if (z & 0x80000000u) w[e] &= 0x0000FFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Notes that node j has values taken out.
+__device__ __forceinline__ void note_node(int j, uint32_t *bad, volatile int *any_bad) {
+  atomicOr(&bad[j >> 5], 1u << (j & 31));
+  *any_bad = 1;
+}
+
 // E4M3 to the operand type.  A row's power is a 16-bit number that scales its
 // values as widen4 takes them (NaN where the row reads back as NaN); `wide`
 // says that the power has no such number and widen4_wide is to be used.  Four
@@ -747,7 +770,8 @@ struct Scheduler {
 
 // Adds back what the helpers took out of the values' product: for every noted
 // node from lo to hi - 1 that this row sees, the values that are not finite
-// (all NaN where an E4M3 row reads back as NaN), columns d .. d + 15.
+// (all NaN where an E4M3 row reads back as NaN, else those that leave the
+// type's range), columns d .. d + 15 in the accumulator's order.
 template <typename T, bool E4M3>
 __device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, int lo, int hi, int node,
                                       const uint32_t *mask_row, const uint32_t *bad, int d, uint32_t (&f)[16]) {
@@ -759,14 +783,26 @@ __device__ __noinline__ void add_back(const Params &p, int q, int h, int ctx, in
     const int pos = ctx + j;
     const int page = __ldg(cv.table + (size_t)q * cv.max_pages + (pos >> cv.ps_shift));
     if (page < 0 || page >= cv.n_pages) continue;
-    const int64_t e = page * cv.page_stride + h * cv.head_stride +
-                      (int64_t)(pos & ((1 << cv.ps_shift) - 1)) * cv.token_stride;
+    const int slot = pos & ((1 << cv.ps_shift) - 1);
+    const int64_t e = page * cv.page_stride + h * cv.head_stride + slot * cv.token_stride + d;
+    if (E4M3) {
+      const int code = cv.v_exp[(((int64_t)page * cv.Hk + h) << cv.ps_shift) + slot];
+      const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(cv.v) + e);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (E4M3) {
-        f[k] = 0x7FFFFFFFu;
-      } else {
-        const uint32_t w = static_cast<const uint16_t *>(cv.v)[e + d + k];
+      for (int k = 0; k < 4; ++k) {
+        const uint2 v = Widen<T>::widen4_wide(w[k], code);
+        const float2 a = unpack2<T>(v.x), b = unpack2<T>(v.y);
+        const float y[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (code == EXP_NAN || !(fabsf(y[i]) < INFINITY))
+            f[4 * k + i] = __float_as_uint(code == EXP_NAN ? __int_as_float(0x7FFFFFFF) : __uint_as_float(f[4 * k + i]) + y[i]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t w = static_cast<const uint16_t *>(cv.v)[e + k];
         if (nonfinite2<T>(w)) f[k] = __float_as_uint(__uint_as_float(f[k]) + unpack2<T>(w).x);
       }
     }
@@ -819,9 +855,13 @@ __device__ __forceinline__ void widen_unit(const Params &p, const uint8_t *src, 
 
 // The same thread's chunks again, for a unit in which some row's power of two
 // has no number of the operand type: those rows, with the power applied exactly.
+// Elements that leave the type's range become infinities, as they do when the row is
+// read back; those of value rows from position `hide_from` on are taken out and
+// their node noted (see above), since not every row of the queries sees them.
 template <typename T, int DP>
 __device__ __noinline__ void widen_unit_wide(const Params &p, int q, int h, int len, const uint8_t *src, uint8_t *dst,
-                                             int base, bool is_v, int ht, int c0) {
+                                             int base, bool is_v, int ht, int c0, int hide_from, uint32_t *bad,
+                                             volatile int *any_bad) {
   constexpr int UC = DP == 64 ? 64 : 128;
   constexpr int C = UC / 16, PER = 128 / C, K = BN / PER;
   const CacheView &cv = p.cv;
@@ -839,12 +879,22 @@ __device__ __noinline__ void widen_unit_wide(const Params &p, int q, int h, int 
     Widen<T>::power(code, odd);
     if (!odd) continue;
     const uint4 x = *reinterpret_cast<const uint4 *>(src + tok * wide + ch * 16);
-    const uint2 a = Widen<T>::widen4_wide(x.x, code), b = Widen<T>::widen4_wide(x.y, code),
-                c = Widen<T>::widen4_wide(x.z, code), d = Widen<T>::widen4_wide(x.w, code);
+    uint4 lo, hi;
+    {
+      const uint2 a = Widen<T>::widen4_wide(x.x, code), b = Widen<T>::widen4_wide(x.y, code),
+                  c = Widen<T>::widen4_wide(x.z, code), d = Widen<T>::widen4_wide(x.w, code);
+      lo = make_uint4(a.x, a.y, b.x, b.y);
+      hi = make_uint4(c.x, c.y, d.x, d.y);
+    }
+    if (t >= hide_from && (any_nonfinite<T>(lo) || any_nonfinite<T>(hi))) {
+      lo = without_nonfinite<T>(lo);
+      hi = without_nonfinite<T>(hi);
+      note_node(t - hide_from, bad, any_bad);
+    }
     uint8_t *row = dst + (ch >> 2) * (BN * 128) + tok * 128;
     const int c2 = (ch & 3) * 2, x7 = tok & 7;
-    *reinterpret_cast<uint4 *>(row + ((c2 ^ x7) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4 *>(row + (((c2 + 1) ^ x7) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+    *reinterpret_cast<uint4 *>(row + ((c2 ^ x7) << 4)) = lo;
+    *reinterpret_cast<uint4 *>(row + (((c2 + 1) ^ x7) << 4)) = hi;
   }
 }
 
@@ -1221,8 +1271,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
             if (now_v[i] == EXP_NAN && note && t >= s.ctx) {
               // a NaN that some rows do not see: out of the product, added back later
               pv = 0;
-              atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
-              *any_bad = 1;
+              note_node(t - s.ctx, bad, any_bad);
             }
             if (ok) {
               sC[slot * BN + 32 * i + lane] = pk;
@@ -1608,7 +1657,8 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
               widen_unit<T, DP>(p, sR + rs * SH::RAW, sT + st * SH::STAGE, sC + (is_v ? 4 * BN : 0) + (pn & 3) * BN, ht,
                                 u * SH::UC);
               if ((wide_s[pn & 3] >> (is_v ? 1 : 0)) & 1)
-                widen_unit_wide<T, DP>(p, s.q, s.h, len, sR + rs * SH::RAW, sT + st * SH::STAGE, base, is_v, ht, u * SH::UC);
+                widen_unit_wide<T, DP>(p, s.q, s.h, len, sR + rs * SH::RAW, sT + st * SH::STAGE, base, is_v, ht, u * SH::UC,
+                                       is_v && note ? s.ctx : INT_MAX, bad, any_bad);
             }
             fence_async_smem();
             __syncwarp();
@@ -1633,17 +1683,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
                   *at = make_uint4(0, 0, 0, 0);
                 } else if (note && t >= s.ctx) {
                   const uint4 x = *at;
-                  if (nonfinite2<T>(x.x) | nonfinite2<T>(x.y) | nonfinite2<T>(x.z) | nonfinite2<T>(x.w)) {
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      const uint32_t z = nonfinite2<T>(w[e]);
-                      if (z & 0x8000u) w[e] &= 0xFFFF0000u;
-                      if (z & 0x80000000u) w[e] &= 0x0000FFFFu;
-                    }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                    atomicOr(&bad[(t - s.ctx) >> 5], 1u << ((t - s.ctx) & 31));
-                    *any_bad = 1;
+                  if (any_nonfinite<T>(x)) {
+                    *at = without_nonfinite<T>(x);
+                    note_node(t - s.ctx, bad, any_bad);
                   }
                 }
               }
