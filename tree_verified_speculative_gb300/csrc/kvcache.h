@@ -135,15 +135,19 @@ __device__ __forceinline__ float e4m3_inv(int code) { return __uint_as_float((ui
 __device__ __forceinline__ float e4m3_scale(int code) {
   return code == EXP_NAN ? __int_as_float(0x7FFFFFFF) : __uint_as_float(code ? (uint32_t)code << 23 : 0x400000u);
 }
-// Largest magnitude to round: the last grid step below 448 * 2^e leaves the
-// type's range only in its top binade (bf16: code 247, fp16: code 135),
-// where values in (248, 255.9] * 2^e would round to 256 * 2^e.
+// Largest magnitude to round.  Values come in fp32 (keys after their norm and
+// rotation), and what is held must not pass the type's largest.  bf16: only in
+// its top binade, code 247, where values in (248, 255.9] * 2^e would round to
+// 256 * 2^e.  fp16: the grid's largest number inside is 1.875 * 2^15 = 61440
+// from code 135 on; in units of 2^e that is 240, 120, .. -- numbers of the
+// grid, a normal one as far as keys go (a norm's row is at most 16 times a
+// weight of 65504, a rotation adds sqrt 2: code 139; below 149 it is normal).
 template <typename T>
 __device__ __forceinline__ float e4m3_limit(int code);
 template <>
 __device__ __forceinline__ float e4m3_limit<__nv_bfloat16>(int code) { return code >= 247 ? 240.f : 448.f; }
 template <>
-__device__ __forceinline__ float e4m3_limit<__half>(int code) { return code >= 135 ? 240.f : 448.f; }
+__device__ __forceinline__ float e4m3_limit<__half>(int code) { return code >= 135 ? 61440.f * e4m3_inv(code) : 448.f; }
 
 // Four floats to four E4M3 bytes, round to nearest even.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
