@@ -435,7 +435,7 @@ int mfd_kv_commit(const mfd_kv_cache *cache, int n_req, int L, const int32_t *ct
  *   q     [n_req * N] tokens of [Hq][D], q_stride elements apart (as above),
  *         `dtype` MFD_BF16 or MFD_FP16; the cache's type, or any over MFD_E4M3
  *   mask  uint32 [n_req][N][ceil(N / 32)] from mfd_build_tree, or NULL (causal)
- *   scale finite, > 0
+ *   scale > 0, and scale * log2 e finite in fp32
  *   out   [n_req][N][Hq][D] of `dtype`, 16-byte aligned; lse fp32
  *         [n_req][N][Hq] (natural log) or NULL
  *   ws    mfd_tree_attention_workspace_bytes(n_req, N, Hq, Hk, D), 256-byte

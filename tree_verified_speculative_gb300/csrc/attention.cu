@@ -73,7 +73,6 @@ constexpr int BM = 128;  // rows of a tile
 constexpr int BN = 128;  // key positions of a tile
 constexpr int MAX_N = 4096;
 constexpr int SEG_RING = 4;  // entries of a CTA's list of work in flight
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 // What an item's start and end cost, in steps: the queries' load, the pipeline's
 // filling and draining, the output.  Measured, three prompts of 1,777 rows: 153
@@ -1896,7 +1895,7 @@ cudaError_t launch_tree_attention(const AttentionLaunch &A, cudaStream_t stream)
   p.ctx_len = A.ctx_len;
   p.n_nodes = A.n_nodes;
   p.mask = A.mask;
-  p.c = A.scale * LOG2E;
+  p.c = A.scale * ATTENTION_LOG2E;
   p.out = static_cast<uint16_t *>(A.out);
   p.lse = A.lse;
   p.status = A.status;

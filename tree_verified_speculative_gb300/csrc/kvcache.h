@@ -57,6 +57,7 @@ struct KvCommitLaunch {
 cudaError_t launch_kv_commit(const KvCommitLaunch &A, cudaStream_t stream);
 
 // attention.cu
+constexpr float ATTENTION_LOG2E = 1.4426950408889634f;
 constexpr int ATTENTION_MAX_CTAS = 152;  // GB300's SMs: scratch is sized without asking the device
 size_t attention_part_bytes(int M, int D);
 int attention_box_rows(int page_size);  // positions of a tensor map's box

@@ -921,7 +921,8 @@ int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, in
   if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
   if (cv.dtype != dtype && cv.dtype != MFD_E4M3) return MFD_ERR_INVALID_ARG;
   if (!rows_ok(q, q_stride, Hq, cv.D) || !aligned(out, 16)) return MFD_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MFD_ERR_INVALID_ARG;
+  // the kernel works with powers of two: scale * log2 e has to be a number too
+  if (!(scale > 0.f) || !std::isfinite(scale * mfd::ATTENTION_LOG2E)) return MFD_ERR_INVALID_ARG;
   const size_t need = mfd_tree_attention_workspace_bytes(n_req, N, Hq, cv.Hk, cv.D);
   if (need == 0) return MFD_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MFD_ERR_WORKSPACE;
