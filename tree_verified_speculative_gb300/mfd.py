@@ -390,7 +390,12 @@ class KVCache:
     [n_pages, Hk, page_size, D] views of bf16, fp16 or float8_e4m3fn storage
     (E4M3 with k_exp, v_exp uint8 [n_pages, Hk, page_size]), and block_table
     int32 [n_req, max_pages].  All are plain tensors the caller may fill; the
-    pages start uninitialised and the block table at zero."""
+    pages start uninitialised and the block table at zero.
+
+    The library gets the tensors' addresses, so they stay what they are: of a
+    cache's attributes only block_table may be assigned (a table of any n_req
+    and max_pages; calls made from then on use it, a captured graph keeps the
+    one it was captured with)."""
 
     def __init__(self, n_pages: int, page_size: int, Hk: int, D: int, n_req: int, max_pages: int,
                  dtype=torch.bfloat16, layout: str = "head", device="cuda"):
@@ -420,22 +425,31 @@ class KVCache:
     def _set(self, k, v, table, k_exp, v_exp):
         assert k.shape == v.shape and k.dim() == 4 and k.dtype == v.dtype and k.dtype in _DTYPE
         assert k.stride() == v.stride() and k.stride(3) == 1, "k and v: equal strides, contiguous rows"
-        assert table.dtype == torch.int32 and table.dim() == 2
+        assert table.dtype == torch.int32 and table.dim() == 2, "block_table: int32 [n_req, max_pages]"
         if k.dtype == torch.float8_e4m3fn:
             for e in (k_exp, v_exp):
                 assert e is not None and e.dtype == torch.uint8 and e.shape == k.shape[:3], "E4M3: row exponents"
         else:
             assert k_exp is None and v_exp is None, "row exponents belong to an E4M3 cache"
-        self.k, self.v, self.block_table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
-        self.n_pages, self.Hk, self.page_size, self.D = k.shape
-        self.n_req, self.max_pages = table.shape
         for t in (k, v):
             assert t.is_cuda, "device tensors"
+        n_pages, Hk, page_size, D = k.shape
+        n_req, max_pages = table.shape
         # a dimension of one element has no stride of its own
-        st = [k.stride(i) if k.shape[i] > 1 else self.D for i in range(3)]
-        self._lib_struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _p(k_exp), _p(v_exp), _p(table), _DTYPE[k.dtype],
-                                          self.n_pages, self.page_size, self.max_pages, self.Hk, self.D, *st)
-        self._c = ctypes.byref(self._lib_struct)
+        st = [k.stride(i) if k.shape[i] > 1 else D for i in range(3)]
+        struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _p(k_exp), _p(v_exp), _p(table), _DTYPE[k.dtype], n_pages,
+                                page_size, max_pages, Hk, D, *st)
+        self.__dict__.update(k=k, v=v, block_table=table, k_exp=k_exp, v_exp=v_exp, n_pages=n_pages, Hk=Hk,
+                             page_size=page_size, D=D, n_req=n_req, max_pages=max_pages, _lib_struct=struct,
+                             _c=ctypes.byref(struct))
+
+    def __setattr__(self, name, value):
+        if name == "block_table":
+            self._set(self.k, self.v, value, self.k_exp, self.v_exp)
+        elif name in self.__dict__:
+            raise AttributeError(f"KVCache.{name} stays as it is: make another cache (from_tensors)")
+        else:
+            object.__setattr__(self, name, value)
 
 
 def rope_phases(theta: float, rot_dim: int, inv_freq=None, device="cuda"):
