@@ -45,6 +45,7 @@ EXPORTS = ("mfd_status_string", "mfd_workspace_size", "mfd_lmhead_topk", "mfd_lm
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 MFD_BF16, MFD_FP16, MFD_E4M3 = 0, 1, 2
+_PHASE = (torch.int64, torch.uint64)  # what holds the 64-bit words of mfd_rope_phases
 _DTYPE = {torch.bfloat16: MFD_BF16, torch.float16: MFD_FP16, torch.float8_e4m3fn: MFD_E4M3}
 
 
@@ -501,7 +502,8 @@ def mfd_qk_norm_rope(q, k, q_w, k_w, eps, phase, rot_dim, interleaved, pos, q_ou
     assert q.numel() == T * Hq * D, "one position per token"
     for w in (q_w, k_w):
         assert w is None or (w.dtype == q.dtype and w.numel() == D), "norm weights [D] of q's type"
-    assert phase is None or phase.numel() >= rot_dim // 2
+    assert phase is None or (phase.dtype in _PHASE and phase.numel() >= rot_dim // 2), "phases of rope_phases"
+    assert status.dtype is torch.int32, "status: int32"
     (qp, qs), (kp, ks) = _rows(q, Hq, D), _rows(k, Hk, D)
     rc = load().mfd_qk_norm_rope(qp, qs, kp, ks, _DTYPE[q.dtype], T, Hq, Hk, D, _p(q_w), _p(k_w), eps,
                                  _p(phase) if rot_dim else None, rot_dim, int(interleaved), _p(pos), _p(q_out),
@@ -522,7 +524,8 @@ def mfd_kv_append(q, k, v, q_w, k_w, eps, phase, rot_dim, interleaved, pos, ctx_
     assert n_nodes is None or (n_nodes.dtype is i32 and n_nodes.numel() == n_req)
     assert q_w is None or (q_w.dtype is dt and q_w.numel() == D), "norm weights [D] of k's type"
     assert k_w is None or (k_w.dtype is dt and k_w.numel() == D), "norm weights [D] of k's type"
-    assert phase is None or phase.numel() >= rot_dim // 2
+    assert phase is None or (phase.dtype in _PHASE and phase.numel() >= rot_dim // 2), "phases of rope_phases"
+    assert status.dtype is i32, "status: int32"
     Hq, qp, qs, op = 0, None, 0, None
     if q is not None:
         rows = q.shape
@@ -551,6 +554,7 @@ def mfd_kv_read(cache, start, length, k_out, v_out, status, stream=None) -> None
     assert n_req == cache.n_req
     for t in (start, length):
         assert t.dtype == torch.int32 and t.numel() == n_req
+    assert status.dtype is torch.int32, "status: int32"
     rc = load().mfd_kv_read(cache._c, n_req, L_max, _p(start), _p(length), _DTYPE[k_out.dtype],
                             _p(k_out), _p(v_out), _p(status), _s(stream))
     _check(rc, "mfd_kv_read")
@@ -564,6 +568,7 @@ def mfd_kv_commit(cache, ctx_len, accept_len, path_nodes, n_nodes, new_len, stat
     assert n_req == cache.n_req and path_nodes.dtype is i32
     for t in (ctx_len, accept_len, n_nodes, new_len):
         assert t.dtype is i32 and t.numel() == n_req
+    assert status.dtype is i32, "status: int32"
     rc = load().mfd_kv_commit(cache._c, n_req, L1 - 1, _p(ctx_len), _p(accept_len), _p(path_nodes),
                               _p(n_nodes), _p(new_len), _p(status), _s(stream))
     _check(rc, "mfd_kv_commit")
@@ -584,6 +589,7 @@ def mfd_tree_attention(q, cache, ctx_len, n_nodes, mask, scale, out, lse, status
     assert n_nodes is None or (n_nodes.dtype is i32 and n_nodes.numel() == n_req)
     assert mask is None or (mask.dtype is i32 and tuple(mask.shape) == (n_req, N, (N + 31) // 32))
     assert lse is None or (lse.dtype is torch.float32 and lse.numel() == n_req * N * Hq)
+    assert status.dtype is i32, "status: int32"
     qp, qs = _rows(q, Hq, D)
     rc = load().mfd_tree_attention(qp, qs, _DTYPE[dt], n_req, N, Hq, cache._c, _p(ctx_len),
                                    _p(n_nodes), _p(mask), scale, _p(out), _p(lse), _p(status), _p(ws),
