@@ -181,9 +181,18 @@ def _p_dev_or_pinned(t) -> int:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object (a call's host time is this
+# binding's, and the object is 1 us of it).  Both are names inside torch: where one
+# is missing, the public call serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _s(stream) -> int | None:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream is None or _raw_device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
