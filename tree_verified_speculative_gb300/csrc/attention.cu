@@ -946,7 +946,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
     }
     return;
   }
-  pdl_launch_dependents();
   Scheduler<NS> sched;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -989,6 +988,9 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
   block_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Not before the CTA has its tensor memory: a grid launched from here on may ask
+  // for some on the same SM and keep it until this grid has ended.
+  pdl_launch_dependents();
   pdl_wait();  // the setup above may overlap the previous grid; all that follows reads global memory
 
   Segment s;
