@@ -1746,7 +1746,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   const int rows = min(min(cut.nn * p.G - first, NS * BM) - row0, JOIN_ROWS);  // of this block
   if (!usable || rows <= 0) return;
   for (int i = 8 + tid; i < n_part; i += threads) note(i);
-  __syncthreads();
+  block_sync();
   // a thread's row, columns, and every `groups`th part from its own
   const int per = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;  // 1, 2, 4, 8 or 16
   const int groups = JOIN_ROWS / per;
@@ -1782,7 +1782,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
       p.lse[((int64_t)q * p.N + node) * p.Hq + h * p.G + g] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
     }
   }
-  __syncthreads();
+  block_sync();
   float acc[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
@@ -1809,7 +1809,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   if (groups > 1) {
     sum_s[0][tid] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     sum_s[1][tid] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    __syncthreads();
+    block_sync();
     if (group > 0) return;
     for (int k = 1; k < groups; ++k) {
       const float4 x = sum_s[0][tid + k * per * chunks], y = sum_s[1][tid + k * per * chunks];
