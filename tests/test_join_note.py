@@ -1,8 +1,9 @@
 """CPU checks of the note that a CTA of the attention leaves for the join:
 every note of a call is followed, and none whose numbers would lead outside
-the call's tensors or the join's tables.  The check is compiled from the
-kernel's own header."""
+the call's tensors or the join's tables; and of a part's weight there.  The
+checks are compiled from the kernel's own header."""
 import ctypes
+import math
 import os
 import random
 import subprocess
@@ -17,6 +18,8 @@ extern "C" int usable(const int *n, int cta, int n_cta, int n_req, int Hk, int n
   c.has[0] = n[0]; c.has[1] = n[1]; c.reach = n[2]; c.q = n[3]; c.h = n[4]; c.pair = n[5]; c.nn = n[6];
   return mfd::cut_usable(c, cta, n_cta, n_req, Hk, n_pair, N);
 }
+extern "C" float weight(int slot, float w, float inv) { return mfd::join_weight(slot, w, inv); }
+extern "C" float tiny_weight() { return mfd::TINY_WEIGHT; }
 extern "C" int note_bytes() { return (int)sizeof(mfd::Cut); }
 extern "C" int empty() { const mfd::Cut c{}; return c.has[0] | c.has[1] | c.reach | c.q | c.h | c.pair | c.nn; }
 """
@@ -29,7 +32,10 @@ def lib(tmp_path_factory):
     with open(src, "w") as f:
         f.write(SRC)
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, src, "-o", out], check=True)
-    return ctypes.CDLL(out)
+    so = ctypes.CDLL(out)
+    so.weight.argtypes, so.weight.restype = [ctypes.c_int, ctypes.c_float, ctypes.c_float], ctypes.c_float
+    so.tiny_weight.restype = ctypes.c_float
+    return so
 
 
 def usable(lib, note, *call):
@@ -77,3 +83,16 @@ def test_stale_scratch_is_not_followed(lib):
     assert usable(lib, good, 10, 152, 2, 2, 2, 5)
     for at, bad in ((2, 143), (2, 0), (2, -1), (3, 2), (3, -1), (4, 2), (4, -1), (5, 2), (5, -1), (6, 6), (6, 0), (6, -1)):
         assert not usable(lib, good[:at] + [bad] + good[at + 1:], 10, 152, 2, 2, 2, 5), (at, bad)
+
+
+def test_an_absent_part_has_no_weight(lib):
+    """Whatever a row's sum is, a part that is not there (slot -1) has weight
+    zero and is not read; a part that is there keeps a NaN."""
+    inf, nan = float("inf"), float("nan")
+    for w in (0.0, 1.0, nan, inf, lib.tiny_weight()):
+        for inv in (0.0, 0.5, nan, inf, -inf):
+            assert lib.weight(-1, w, inv) == 0.0, (w, inv)
+    assert lib.weight(0, 0.5, 0.5) == 0.25 and lib.weight(7, 1.0, 0.0) == 0.0
+    assert math.isnan(lib.weight(3, 0.0, nan)) and math.isnan(lib.weight(3, nan, 1.0)) and math.isnan(lib.weight(3, 1.0, nan))
+    tiny = lib.tiny_weight()
+    assert tiny < 0 and lib.weight(3, tiny, 0.5) == tiny

@@ -1714,8 +1714,6 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
 // ------------------------------------------------------------------ join
 
 constexpr int JOIN_ROWS = 16;
-// Stands for a weight that is more than zero but nothing in 32 bits.
-constexpr float TINY = -1.f;
 
 // Combines the parts of the items that borders cut.  Block (c, y): the item
 // whose first part CTA c holds, if any, and 16 of its rows: first the notes of
@@ -1769,14 +1767,13 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
         // a part whose keys are not seen has sum 0; one whose scores are NaN a NaN
         w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : ml.y) : ex2(ml.x - m);
         l += w * ml.y;
-        if (w == 0.f && ml.x > -INFINITY) w = TINY;
+        if (w == 0.f && ml.x > -INFINITY) w = TINY_WEIGHT;
       }
       w_s[i][r] = w;
     }
     for (int o = G / 2; o > 0; o >>= 1) l += __shfl_xor_sync(peers, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = j; i < n_part; i += G)
-      if (w_s[i][r] != TINY) w_s[i][r] *= inv;
+    for (int i = j; i < n_part; i += G) w_s[i][r] = join_weight(slot_s[i], w_s[i][r], inv);
     if (r < rows && p.lse && j == 0) {
       const int node = (first + row) / p.G, g = first + row - node * p.G;
       p.lse[((int64_t)q * p.N + node) * p.Hq + h * p.G + g] = l == 0.f ? -INFINITY : m * LN2 + logf(l);
@@ -1792,7 +1789,7 @@ __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
     if (w == 0.f) continue;
     const float4 *o = p.part_o + ((int64_t)slot_s[i] * (p.cv.D / 4) + 2 * ch) * p.part_rows + row0 + r;
     float4 a = o[0], b = o[p.part_rows];
-    if (w == TINY) {  // only what is not finite counts; an infinity's sign is the weight's, times -1 below
+    if (w == TINY_WEIGHT) {  // only what is not finite counts; an infinity's sign is the weight's, times -1 below
       auto only = [](float x) { return fabsf(x) < INFINITY ? 0.f : -x; };
       a = make_float4(only(a.x), only(a.y), only(a.z), only(a.w));
       b = make_float4(only(b.x), only(b.y), only(b.z), only(b.w));

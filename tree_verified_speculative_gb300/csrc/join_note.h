@@ -29,4 +29,14 @@ MFD_HOST_DEVICE bool cut_usable(const Cut &c, int cta, int n_cta, int n_req, int
          ((unsigned)c.h < (unsigned)Hk) & ((unsigned)c.pair < (unsigned)n_pair) & ((unsigned)c.nn - 1u < (unsigned)N);
 }
 
+// A part's weight in the join's sum: `w` over the row's sum (inv: one over it).
+// A CTA's stretch of the item may hold no key tile; there is no part then (slot
+// -1), and it must have weight zero, which is what keeps it from being read,
+// whatever the sum is: a row with a NaN has a NaN for inv.  TINY_WEIGHT stands
+// for a weight that is more than zero but nothing in 32 bits.
+constexpr float TINY_WEIGHT = -1.f;
+MFD_HOST_DEVICE float join_weight(int slot, float w, float inv) {
+  return slot < 0 ? 0.f : w == TINY_WEIGHT ? w : w * inv;
+}
+
 }  // namespace mfd
