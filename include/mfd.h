@@ -334,7 +334,8 @@ int mfd_verify(const float *target_logits, int n_req, int B, int V, int L,
  * of two makes the held value q * 2^e exact in bf16 (and in fp16 inside its
  * range), so reading back rounds nothing.  A row with a NaN or an infinity
  * gets the byte 255 and reads back as NaN in whole; a value that would round
- * past the type's largest is held as the grid's next lower one. */
+ * past the type's largest is held as the grid's next lower one.  E4M3's own
+ * NaN (0x7F, 0xFF) is not part of the format and never written. */
 enum { MFD_BF16 = 0, MFD_FP16 = 1, MFD_E4M3 = 2 };
 
 /* A paged cache.  This struct lives on the host and is read during the call;
@@ -437,7 +438,7 @@ int mfd_kv_commit(const mfd_kv_cache *cache, int n_req, int L, const int32_t *ct
  *   mask  uint32 [n_req][N][ceil(N / 32)] from mfd_build_tree, or NULL (causal)
  *   scale > 0, and scale * log2 e finite in fp32
  *   out   [n_req][N][Hq][D] of `dtype`, 16-byte aligned; lse fp32
- *         [n_req][N][Hq] (natural log) or NULL
+ *         [n_req][N][Hq] (natural log) or NULL; neither overlaps q
  *   ws    mfd_tree_attention_workspace_bytes(n_req, N, Hq, Hk, D), 256-byte
  *         aligned; needs no zeroing and keeps nothing between calls
  * Scores, softmax statistics and sums are fp32; a row's weights are rounded to

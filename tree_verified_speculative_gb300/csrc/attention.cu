@@ -42,22 +42,23 @@
 // of 16-bit caches that reach past the context.  There it clears rows past the
 // end and values that are not finite, which a product would spread to rows that
 // do not see them (0 * NaN); a cleared value's node is noted and added back for
-// the rows that do see it.
+// the rows that do see it.  E4M3 rows that read back as NaN, or past the type's
+// range, are taken out and added back the same way.
 //
 // What bounds it, on the GPU alone (a captured call replayed):
 //   one token over 200,002 positions, 32/8 heads of 128, bf16: HBM; 129 us, 6.4
 //     TB/s, 0.94 of what a copy reaches
 //   32 requests of one token over ragged contexts up to 16,000, the same heads,
-//     E4M3: the widening; 234 us, 3.2 TB/s, each byte read being one
+//     E4M3: the widening; 236 us, 3.2 TB/s, each byte read being one
 //     element to turn into two bytes (one helper warpgroup instead of two: 297)
 //   32 trees of 129 nodes over up to 6,000, the same heads, E4M3: a stream's
-//     chain of scores, softmax and product; 402 us, 0.69 PFLOP/s.  A step of 128
+//     chain of scores, softmax and product; 403 us, 0.69 PFLOP/s (16-bit: 346).  A step of 128
 //     rows and 128 keys takes 2,900 cycles of which the tensor pipe needs 1,024;
 //     neither issue slots (51 %) nor exponentials (16 %) are used up
-//   one tree of 257 nodes over 8,191, 16/4 heads of 256, bf16: 60 us; of that
+//   one tree of 257 nodes over 8,191, 16/4 heads of 256, bf16: 61 us; of that
 //     the pipelines' filling, the cut items' parts (20 MB) and their join take
-//     half, the products 0.58 PFLOP/s over the whole
-//   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 133 us, the same
+//     half, the products 0.57 PFLOP/s over the whole
+//   three prompts of 1,777 tokens, 28/4 heads of 80, fp16: 131 us, the same
 //     chain, and starts and ends of items of ten tiles
 #include <atomic>
 #include <climits>
@@ -75,9 +76,9 @@ constexpr int MAX_N = 4096;
 constexpr int SEG_RING = 4;  // entries of a CTA's list of work in flight
 constexpr float LN2 = 0.6931471805599453f;
 // What an item's start and end cost, in steps: the queries' load, the pipeline's
-// filling and draining, the output.  Measured, three prompts of 1,777 rows: 153
-// us with 1, 133 with 4, 137 with 6; 32 trees of 129 nodes (before later steps):
-// 413, 404, 399.
+// filling and draining, the output.  Measured with 1, 4, 5 and 6: three prompts of
+// 1,777 rows 152, 131, 131, 135 us; 32 trees of 129 nodes 410, 400, 402, 397; one
+// tree of 257 nodes 59.5, 60.8, 60.9, 60.9.
 constexpr int START_COST = 5;
 constexpr float LARGE_SCORE = 65536.f;
 constexpr float MAX_GROWTH = 8.f;  // log2 of how far a weight may pass 1
@@ -141,7 +142,7 @@ __device__ __forceinline__ bool lengths(const Params &p, int q, int &ctx, int &n
 struct Item {
   int active;  // row tiles with live rows
   int tiles;   // key tiles
-  int cost;    // places on the line: a step per row tile and key tile, and one for its start and end
+  int cost;    // places on the line: a step per row tile and key tile, and START_COST (1 without live rows)
 };
 
 template <int NS>
@@ -1468,7 +1469,7 @@ __global__ void __launch_bounds__((Shape<DP, E4M3>::THREADS), 1)
                   sum1 = add2(sum1, pair(a, b));
                 else
                   sum0 = add2(sum0, pair(a, b));
-                pk[k] = pack2<T>(a, b);
+                pk[k] = pack2<T>(a, b);  // the type that the product takes; the sum has them unrounded
               }
               tmem_st16(sa + (SW * part + c) / 2, pk);  // over scores that have been read
             }
@@ -1721,9 +1722,9 @@ constexpr int JOIN_ROWS = 16;
 // 2^(m - max m) / sum comes, then the parts' O.  A thread adds up one row's 8
 // columns, and where the block has few rows (one token) several threads share
 // the parts; the order is the parts', whatever CTA was done first.  It waits for
-// its loads, one round after the other: it is 5 us of the 14 of one token over
+// its loads, one round after the other: it is 5 us of the 15 of one token over
 // 700 positions (nine parts for each of 8 heads), 7 of the 129 over 200,002
-// (19 each), 10 of one tree's 59, whose parts are 20 MB.
+// (19 each), 10 of one tree's 61, whose parts are 20 MB.
 template <typename T, int NS>
 __global__ void __launch_bounds__(JOIN_ROWS * 32) join_kernel(const Params p) {
   __shared__ float w_s[ATTENTION_MAX_CTAS][JOIN_ROWS];
