@@ -455,6 +455,120 @@ int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, in
                        const uint32_t *mask, float scale, void *out, float *lse, int32_t *status, void *ws,
                        size_t ws_bytes, mfd_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The target's recurrent layers (the method's pages name hybrid targets, whose
+ * gated-delta layers need tree kernels of their own: model card "MFD drafter
+ * for Qwen3.5-4B", Usage; project page, Results).  Where an attention layer has
+ * keys and values in a cache, such a layer has one matrix for each of its Hv
+ * value heads, S [Dk][Dv], and a row changes it by the gated delta rule:
+ *
+ *   S' = e^g S,  u = beta (v - S'^T k),  S = S' + k u^T,  o = scale S^T q
+ *
+ * with the query and key of head h / (Hv / Hk); with `normalize` both are first
+ * divided by sqrt(sum x^2 + eps).
+ *
+ *   mfd_delta_rule    rows one after the other, from a state to the next: one
+ *                     new token, or a stretch of a prompt
+ *   mfd_delta_tree    the nodes of a drafted tree, each behind its own path, in
+ *                     one pass; the state stays
+ *   mfd_delta_commit  after mfd_verify: the state behind the accepted path
+ *
+ * States are fp32 and belong to slots: request q is read from slot src[q] (NULL:
+ * q) and its new state goes to slot dst[q] (NULL: the one it came from).  src -1
+ * is the zero state of a fresh request, dst -1 drops the new state.  One slot may
+ * be read by several requests; a slot that is written belongs to one request of
+ * the call. */
+
+/* States on the device.  This struct lives on the host and is read during the
+ * call.  s: [n_slots][Hv][Dk][Dv], contiguous, 16-byte aligned.
+ * Limits: Dk % 16 == 0, 16 <= Dk <= 128; Dv % 16 == 0, 16 <= Dv <= 256; Hv <=
+ * 1024. */
+typedef struct {
+  float *s;
+  int32_t n_slots, Hv, Dk, Dv;
+} mfd_delta_state;
+
+/* N rows a request, one after the other.
+ *   q, k     [n_req * N] tokens of [Hk][Dk], q_stride and k_stride elements apart
+ *            (a multiple of 8, at least Hk * Dk), heads contiguous, `dtype`
+ *            MFD_BF16 or MFD_FP16, 16-byte aligned; Hv % Hk == 0
+ *   v        [n_req * N] tokens of [Hv][Dv], likewise
+ *   g, beta  fp32 [n_req][N][Hv]: log of the decay (0 keeps all, -inf nothing)
+ *            and the step's size
+ *   n_nodes  int32 [n_req], or NULL (N): rows from there on are not read, and
+ *            their outputs are zero
+ *   out      [n_req][N][Hv][Dv] of `dtype`, 16-byte aligned; no overlap with q,
+ *            k and v
+ *   src, dst int32 [n_req] or NULL, see above
+ * Sums and the state are fp32, products too or of operands that keep 22 bits of
+ * each factor.  Results do not change from run to run.  What a row holds reaches
+ * no row before it, infinities and NaN included.
+ * normalize: 0 or 1; eps >= 0; scale finite.
+ * Limits: as for the state; n_req * N < 2^31, n_req * Hv * 8 < 2^31.  Device
+ * errors (MFD_ERR_INPUT): n_nodes outside [0, N], a slot outside [-1, n_slots);
+ * that request's outputs are zero and its state is not written.  MFD_ERR_TIMEOUT
+ * as for every bounded wait. */
+int mfd_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   int dtype, int n_req, int N, int Hk, const float *g, const float *beta, int normalize, float eps,
+                   float scale, const int32_t *n_nodes, void *out, const mfd_delta_state *state, const int32_t *src,
+                   const int32_t *dst, int32_t *status, mfd_stream_t stream);
+
+/* N nodes of a tree a request: a node's S comes from its parent's, the root's
+ * from the request's state, which stays as it is.  Arguments as above, and
+ *   parent  int32 [n_req][N] from mfd_build_tree: -1 for node 0, else a node
+ *           before it; no node more than 16 below the root
+ * What a node holds reaches only nodes below it.  N <= 513.  Device errors
+ * (MFD_ERR_INPUT): as above, and parents that are none; that request's outputs
+ * are zero. */
+int mfd_delta_tree(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   int dtype, int n_req, int N, int Hk, const float *g, const float *beta, int normalize, float eps,
+                   float scale, const int32_t *parent, const int32_t *n_nodes, void *out, const mfd_delta_state *state,
+                   const int32_t *src, int32_t *status, mfd_stream_t stream);
+
+/* The state behind the accepted path: rows path_nodes[q][0 .. accept_len[q]] of
+ * the tree's k, v, g and beta, one after the other (node 0, the root, is the
+ * first).  accept_len [n_req] and path_nodes [n_req][L + 1] as mfd_verify writes
+ * them, 1 <= L <= 16; the rest as above.  Device errors (MFD_ERR_INPUT):
+ * accept_len outside [0, L], a path that does not start at node 0, does not
+ * increase or leaves [0, n_nodes), and as above; that request's state is not
+ * written. */
+int mfd_delta_commit(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype, int n_req, int N,
+                     int Hk, const float *g, const float *beta, int normalize, float eps, int L,
+                     const int32_t *accept_len, const int32_t *path_nodes, const int32_t *n_nodes,
+                     const mfd_delta_state *state, const int32_t *src, const int32_t *dst, int32_t *status,
+                     mfd_stream_t stream);
+
+/* What goes through a gate: nothing, 1 / (1 + e^-x), or x / (1 + e^-x). */
+enum { MFD_ACT_NONE = 0, MFD_ACT_SIGMOID = 1, MFD_ACT_SILU = 2 };
+
+/* Norm of each head's row times its gate, the end of a recurrent layer:
+ *   out = x / sqrt(mean(x^2) + eps) * w * act(gate)   (fp32, one rounding)
+ *   x, gate  [T] tokens of [heads][D], x_stride and gate_stride elements apart (a
+ *            multiple of 8, at least heads * D), heads contiguous, `dtype`
+ *            MFD_BF16 or MFD_FP16, 16-byte aligned
+ *   w        [D] of `dtype`, 16-byte aligned
+ *   out      [T][heads][D] contiguous, 16-byte aligned; may be x or gate
+ *            themselves where those are contiguous
+ * eps >= 0.  Limits: D % 8 == 0, 8 <= D <= 256; heads <= 1024; T * heads < 2^31. */
+int mfd_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, int dtype, int T, int heads,
+                   int D, const void *w, float eps, int act, void *out, mfd_stream_t stream);
+
+/* A block's end and the next one's start:
+ *   y' = y / sqrt(mean(y^2) + eps) * w_post   (w_post NULL: y)
+ *   r  = residual + scale * act(gate) * y'    (gate NULL: 1)
+ *   x  = r / sqrt(mean(r^2) + eps) * w_pre    (w_pre NULL: no x), from the r that
+ *                                              is not rounded yet
+ *   y, residual   [T][H] of `dtype`, contiguous, 16-byte aligned
+ *   gate          rows of H, gate_stride elements apart (0: one row for all
+ *                 tokens; else a multiple of 8, at least H), 16-byte aligned
+ *   w_post, w_pre [H] of `dtype`, 16-byte aligned, or NULL
+ *   residual_out  [T][H]; x_out [T][H], or NULL with w_pre NULL.  Each may be y or
+ *                 residual itself; not gate where that is one row
+ * eps >= 0, scale finite.  Limits: H % 8 == 0, 8 <= H <= 16384. */
+int mfd_residual_norm(const void *y, const void *residual, int dtype, int T, int H, const void *w_post,
+                      const void *gate, int64_t gate_stride, int act, float scale, const void *w_pre, float eps,
+                      void *residual_out, void *x_out, mfd_stream_t stream);
+
 /* Tree analytics: what a tree spends its budget on (project page "Multi-Future
  * Drafting", TL;DR and Abstract: chimeras -- prefixes spliced from different
  * futures that the target never produces; How it works, step 1, and "What the

@@ -11,6 +11,7 @@
 #include <tuple>
 
 #include "../../include/mfd.h"
+#include "delta.h"
 #include "kvcache.h"
 #include "lmhead.h"
 
@@ -952,6 +953,176 @@ int mfd_tree_attention(const void *q, int64_t q_stride, int dtype, int n_req, in
   A.lse = lse;
   A.status = status;
   return cuda_status(mfd::launch_tree_attention(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the three forms of the delta rule share; fills A from it.
+int delta_args(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype, int n_req, int N, int Hk,
+               const float *g, const float *beta, int normalize, float eps, const int32_t *n_nodes,
+               const mfd_delta_state *state, const int32_t *src, const int32_t *dst, int32_t *status,
+               mfd::DeltaArgs *A) {
+  if (!state || !state->s || !aligned(state->s, 16) || state->n_slots < 1 || state->Hv < 1 || state->Dk < 1 || state->Dv < 1)
+    return MFD_ERR_INVALID_ARG;
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (n_req < 1 || N < 1 || Hk < 1 || !g || !beta || !status) return MFD_ERR_INVALID_ARG;
+  for (const void *a : {(const void *)g, (const void *)beta, (const void *)n_nodes, (const void *)src, (const void *)dst,
+                        (const void *)status})
+    if (!aligned(a, 4)) return MFD_ERR_INVALID_ARG;
+  if (normalize != 0 && (normalize != 1 || !(eps >= 0.f) || !std::isfinite(eps))) return MFD_ERR_INVALID_ARG;
+  if (state->Dk % 16 != 0 || state->Dk > 128 || state->Dv % 16 != 0 || state->Dv > 256 || state->Hv > 1024 ||
+      state->Hv % Hk != 0)
+    return MFD_ERR_UNSUPPORTED;
+  if (!rows_ok(k, k_stride, Hk, state->Dk) || !rows_ok(v, v_stride, state->Hv, state->Dv)) return MFD_ERR_INVALID_ARG;
+  if ((int64_t)n_req * N >= ((int64_t)1 << 31) - 1 || (int64_t)n_req * state->Hv * 8 >= ((int64_t)1 << 31) - 1)
+    return MFD_ERR_UNSUPPORTED;
+  *A = mfd::DeltaArgs{};
+  A->k = static_cast<const uint16_t *>(k);
+  A->v = static_cast<const uint16_t *>(v);
+  A->k_stride = k_stride;
+  A->v_stride = v_stride;
+  A->dtype = dtype;
+  A->n_req = n_req;
+  A->N = N;
+  A->Hk = Hk;
+  A->Hv = state->Hv;
+  A->Dk = state->Dk;
+  A->Dv = state->Dv;
+  A->g = g;
+  A->beta = beta;
+  A->normalize = normalize;
+  A->eps = eps;
+  A->n_nodes = n_nodes;
+  A->s = state->s;
+  A->n_slots = state->n_slots;
+  A->src = src;
+  A->dst = dst;
+  A->status = status;
+  return MFD_OK;
+}
+
+// The queries and outputs of the two forms that have them.
+int delta_out(const void *q, int64_t q_stride, float scale, void *out, mfd::DeltaArgs *A) {
+  if (!rows_ok(q, q_stride, A->Hk, A->Dk) || !out || !aligned(out, 16) || !std::isfinite(scale)) return MFD_ERR_INVALID_ARG;
+  A->q = static_cast<const uint16_t *>(q);
+  A->q_stride = q_stride;
+  A->scale = scale;
+  A->out = static_cast<uint16_t *>(out);
+  return MFD_OK;
+}
+
+bool act_ok(int act) { return act == MFD_ACT_NONE || act == MFD_ACT_SIGMOID || act == MFD_ACT_SILU; }
+
+}  // namespace
+
+extern "C" {
+
+int mfd_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   int dtype, int n_req, int N, int Hk, const float *g, const float *beta, int normalize, float eps,
+                   float scale, const int32_t *n_nodes, void *out, const mfd_delta_state *state, const int32_t *src,
+                   const int32_t *dst, int32_t *status, mfd_stream_t stream) {
+  mfd::DeltaArgs A;
+  int rc = delta_args(k, k_stride, v, v_stride, dtype, n_req, N, Hk, g, beta, normalize, eps, n_nodes, state, src, dst, status, &A);
+  if (rc != MFD_OK || (rc = delta_out(q, q_stride, scale, out, &A)) != MFD_OK) return rc;
+  DeviceInfo d;
+  if ((rc = current_device_info(&d)) != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
+  return cuda_status(mfd::launch_delta_rows(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_delta_tree(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   int dtype, int n_req, int N, int Hk, const float *g, const float *beta, int normalize, float eps,
+                   float scale, const int32_t *parent, const int32_t *n_nodes, void *out, const mfd_delta_state *state,
+                   const int32_t *src, int32_t *status, mfd_stream_t stream) {
+  mfd::DeltaArgs A;
+  int rc = delta_args(k, k_stride, v, v_stride, dtype, n_req, N, Hk, g, beta, normalize, eps, n_nodes, state, src, nullptr, status, &A);
+  if (rc != MFD_OK || (rc = delta_out(q, q_stride, scale, out, &A)) != MFD_OK) return rc;
+  if (!parent || !aligned(parent, 4)) return MFD_ERR_INVALID_ARG;
+  if (N > mfd::DELTA_MAX_NODES) return MFD_ERR_UNSUPPORTED;
+  A.parent = parent;
+  DeviceInfo d;
+  if ((rc = current_device_info(&d)) != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
+  return cuda_status(mfd::launch_delta_tree(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_delta_commit(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype, int n_req, int N,
+                     int Hk, const float *g, const float *beta, int normalize, float eps, int L,
+                     const int32_t *accept_len, const int32_t *path_nodes, const int32_t *n_nodes,
+                     const mfd_delta_state *state, const int32_t *src, const int32_t *dst, int32_t *status,
+                     mfd_stream_t stream) {
+  mfd::DeltaArgs A;
+  int rc = delta_args(k, k_stride, v, v_stride, dtype, n_req, N, Hk, g, beta, normalize, eps, n_nodes, state, src, dst, status, &A);
+  if (rc != MFD_OK) return rc;
+  if (!accept_len || !path_nodes || !aligned(accept_len, 4) || !aligned(path_nodes, 4) || L < 1) return MFD_ERR_INVALID_ARG;
+  if (L > 16) return MFD_ERR_UNSUPPORTED;
+  A.accept_len = accept_len;
+  A.path = path_nodes;
+  A.L = L;
+  DeviceInfo d;
+  if ((rc = current_device_info(&d)) != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
+  return cuda_status(mfd::launch_delta_commit(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, int dtype, int T, int heads,
+                   int D, const void *w, float eps, int act, void *out, mfd_stream_t stream) {
+  if (T < 1 || heads < 1 || D < 1 || !w || !aligned(w, 16) || !out || !aligned(out, 16)) return MFD_ERR_INVALID_ARG;
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !act_ok(act)) return MFD_ERR_INVALID_ARG;
+  if (D % 8 != 0 || D > 256 || heads > 1024 || (int64_t)T * heads >= ((int64_t)1 << 31) - 1) return MFD_ERR_UNSUPPORTED;
+  if (!rows_ok(x, x_stride, heads, D) || !rows_ok(gate, gate_stride, heads, D)) return MFD_ERR_INVALID_ARG;
+  const int rc = need_sm103();
+  if (rc != MFD_OK) return rc;
+  mfd::GatedNormArgs A;
+  A.x = static_cast<const uint16_t *>(x);
+  A.gate = static_cast<const uint16_t *>(gate);
+  A.w = static_cast<const uint16_t *>(w);
+  A.x_stride = x_stride;
+  A.gate_stride = gate_stride;
+  A.dtype = dtype;
+  A.T = T;
+  A.heads = heads;
+  A.D = D;
+  A.act = act;
+  A.eps = eps;
+  A.out = static_cast<uint16_t *>(out);
+  return cuda_status(mfd::launch_gated_norm(A, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mfd_residual_norm(const void *y, const void *residual, int dtype, int T, int H, const void *w_post,
+                      const void *gate, int64_t gate_stride, int act, float scale, const void *w_pre, float eps,
+                      void *residual_out, void *x_out, mfd_stream_t stream) {
+  if (T < 1 || H < 1 || !y || !residual || !residual_out) return MFD_ERR_INVALID_ARG;
+  if ((w_pre != nullptr) != (x_out != nullptr)) return MFD_ERR_INVALID_ARG;
+  for (const void *a : {y, residual, w_post, gate, w_pre, (const void *)residual_out, (const void *)x_out})
+    if (a && !aligned(a, 16)) return MFD_ERR_INVALID_ARG;
+  if (dtype != MFD_BF16 && dtype != MFD_FP16) return MFD_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale) || !act_ok(act)) return MFD_ERR_INVALID_ARG;
+  if (H % 8 != 0 || H > 16384) return MFD_ERR_UNSUPPORTED;
+  if (gate && gate_stride != 0 && (gate_stride < H || gate_stride % 8 != 0 || gate_stride >= ((int64_t)1 << 40)))
+    return MFD_ERR_INVALID_ARG;
+  if (residual_out == x_out) return MFD_ERR_INVALID_ARG;
+  const int rc = need_sm103();
+  if (rc != MFD_OK) return rc;
+  mfd::ResidualNormArgs A;
+  A.y = static_cast<const uint16_t *>(y);
+  A.residual = static_cast<const uint16_t *>(residual);
+  A.w_post = static_cast<const uint16_t *>(w_post);
+  A.gate = static_cast<const uint16_t *>(gate);
+  A.w_pre = static_cast<const uint16_t *>(w_pre);
+  A.gate_stride = gate_stride;
+  A.dtype = dtype;
+  A.T = T;
+  A.H = H;
+  A.act = act;
+  A.scale = scale;
+  A.eps = eps;
+  A.residual_out = static_cast<uint16_t *>(residual_out);
+  A.x_out = static_cast<uint16_t *>(x_out);
+  return cuda_status(mfd::launch_residual_norm(A, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

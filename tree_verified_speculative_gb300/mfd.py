@@ -41,10 +41,13 @@ EXPORTS = ("mfd_status_string", "mfd_workspace_size", "mfd_lmhead_topk", "mfd_lm
            "mfd_lmhead_packed_fp8_bytes", "mfd_lmhead_pack_fp8", "mfd_fp8_quantize_rows",
            "mfd_lmhead_fp8_workspace_bytes", "mfd_lmhead_topk_fp8", "mfd_tree_analytics",
            "mfd_rope_phases", "mfd_qk_norm_rope", "mfd_kv_append", "mfd_kv_read", "mfd_kv_commit",
-           "mfd_tree_attention_workspace_bytes", "mfd_tree_attention")
+           "mfd_tree_attention_workspace_bytes", "mfd_tree_attention",
+           "mfd_delta_rule", "mfd_delta_tree", "mfd_delta_commit", "mfd_gated_norm", "mfd_residual_norm")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 MFD_BF16, MFD_FP16, MFD_E4M3 = 0, 1, 2
+MFD_ACT_NONE, MFD_ACT_SIGMOID, MFD_ACT_SILU = 0, 1, 2
+_ACT = {"none": MFD_ACT_NONE, "sigmoid": MFD_ACT_SIGMOID, "silu": MFD_ACT_SILU}
 _PHASE = (torch.int64, torch.uint64)  # what holds the 64-bit words of mfd_rope_phases
 _DTYPE = {torch.bfloat16: MFD_BF16, torch.float16: MFD_FP16, torch.float8_e4m3fn: MFD_E4M3}
 
@@ -56,6 +59,12 @@ class _KvCacheStruct(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class _DeltaStateStruct(ctypes.Structure):
+    """mfd_delta_state of include/mfd.h."""
+    _fields_ = [("s", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("Hv", ctypes.c_int32), ("Dk", ctypes.c_int32),
+                ("Dv", ctypes.c_int32)]
 
 _lock = threading.Lock()
 _lib = None
@@ -152,6 +161,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.mfd_tree_attention_workspace_bytes.restype = SZ
         lib.mfd_tree_attention.argtypes = [P, I64, I, I, I, I, C, P, P, P, F, P, P, P, P, SZ, P]
         lib.mfd_tree_attention.restype = I
+        DS = ctypes.POINTER(_DeltaStateStruct)
+        lib.mfd_delta_rule.argtypes = [P, I64, P, I64, P, I64, I, I, I, I, P, P, I, F, F, P, P, DS, P, P, P, P]
+        lib.mfd_delta_rule.restype = I
+        lib.mfd_delta_tree.argtypes = [P, I64, P, I64, P, I64, I, I, I, I, P, P, I, F, F, P, P, P, DS, P, P, P]
+        lib.mfd_delta_tree.restype = I
+        lib.mfd_delta_commit.argtypes = [P, I64, P, I64, I, I, I, I, P, P, I, F, I, P, P, P, DS, P, P, P, P]
+        lib.mfd_delta_commit.restype = I
+        lib.mfd_gated_norm.argtypes = [P, I64, P, I64, I, I, I, I, P, F, I, P, P]
+        lib.mfd_gated_norm.restype = I
+        lib.mfd_residual_norm.argtypes = [P, P, I, I, I, P, P, I64, I, F, P, F, P, P, P]
+        lib.mfd_residual_norm.restype = I
         _libs[p] = lib
         if path is None:
             _lib = lib
@@ -604,6 +624,149 @@ def mfd_tree_attention(q, cache, ctx_len, n_nodes, mask, scale, out, lse, status
                                    _p(n_nodes), _p(mask), scale, _p(out), _p(lse), _p(status), _p(ws),
                                    ws.numel() * ws.element_size(), _s(stream))
     _check(rc, "mfd_tree_attention")
+
+
+# ---------------------------------------------------------------------------
+class DeltaState:
+    """The states of one recurrent layer (mfd_delta_state): s fp32 [n_slots,
+    Hv, Dk, Dv], a plain tensor the caller may fill, zero to begin with.  The
+    library gets its address, so it stays what it is."""
+
+    def __init__(self, n_slots: int, Hv: int, Dk: int, Dv: int, device="cuda"):
+        self._set(torch.zeros((n_slots, Hv, Dk, Dv), dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_tensor(cls, s) -> "DeltaState":
+        """States over a tensor the caller holds."""
+        self = cls.__new__(cls)
+        self._set(s)
+        return self
+
+    def _set(self, s):
+        assert s.dim() == 4 and s.dtype is torch.float32, "states: fp32 [n_slots, Hv, Dk, Dv]"
+        struct = _DeltaStateStruct(_p(s), *s.shape)
+        self.__dict__.update(s=s, n_slots=s.shape[0], Hv=s.shape[1], Dk=s.shape[2], Dv=s.shape[3], _lib_struct=struct,
+                             _c=ctypes.byref(struct))
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"DeltaState.{name} stays as it is: make another one (from_tensor)")
+        object.__setattr__(self, name, value)
+
+
+def _on_current_device(*tensors) -> None:
+    """Kernels run on the current device: tensors of another one are refused."""
+    here = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    for t in tensors:
+        assert t is None or t.get_device() == here, "tensors on the current device"
+
+
+def _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status):
+    """What the three forms of the delta rule ask of their common arguments:
+    (n_req, N, Hk, pointers and strides of k and v)."""
+    i32 = torch.int32
+    n_req, N, Hk, Dk = k.shape
+    assert k.dtype in (torch.bfloat16, torch.float16) and v.dtype is k.dtype, "k and v: bf16 or fp16"
+    assert Dk == state.Dk and v.shape == (n_req, N, state.Hv, state.Dv), "k [n_req, N, Hk, Dk], v [n_req, N, Hv, Dv]"
+    for t in (g, beta):
+        assert t.dtype is torch.float32 and t.shape == (n_req, N, state.Hv), "g and beta: fp32 [n_req, N, Hv]"
+    for t in (n_nodes, src, dst):
+        assert t is None or (t.dtype is i32 and t.numel() == n_req), "n_nodes, src, dst: int32 [n_req]"
+    assert status.dtype is i32, "status: int32"
+    assert (src is not None and dst is not None) or n_req <= state.n_slots, "a slot for each request"
+    kp, ks = _rows(k, Hk, Dk)
+    vp, vs = _rows(v, state.Hv, state.Dv)
+    _on_current_device(k, v, g, beta, n_nodes, src, dst, status, state.s)
+    return n_req, N, Hk, kp, ks, vp, vs
+
+
+def _delta_queries(q, k, out, state):
+    assert q.shape == k.shape and q.dtype is k.dtype, "q: as k"
+    assert out.shape == (k.shape[0], k.shape[1], state.Hv, state.Dv) and out.dtype is k.dtype, "out: [n_req, N, Hv, Dv]"
+    _on_current_device(q, out)
+    return _rows(q, q.shape[2], q.shape[3])
+
+
+def mfd_delta_rule(q, k, v, g, beta, eps, scale, n_nodes, out, state, src, dst, status, stream=None) -> None:
+    """The gated delta rule over rows q, k [n_req, N, Hk, Dk], v [n_req, N, Hv,
+    Dv] with log decays g and steps beta (fp32 [n_req, N, Hv]) into out (as v)
+    and `state` (DeltaState), from slots src to slots dst (int32 [n_req], or
+    None).  eps: of the queries' and keys' length, or None (taken as they are).
+    n_nodes may be None (all N rows live)."""
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status)
+    qp, qs = _delta_queries(q, k, out, state)
+    rc = load().mfd_delta_rule(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta),
+                               0 if eps is None else 1, eps or 0.0, scale, _p(n_nodes), _p(out), state._c, _p(src), _p(dst),
+                               _p(status), _s(stream))
+    _check(rc, "mfd_delta_rule")
+
+
+def mfd_delta_tree(q, k, v, g, beta, eps, scale, parent, n_nodes, out, state, src, status, stream=None) -> None:
+    """The same for the nodes of a tree (parent int32 [n_req, N] from
+    mfd_build_tree), each behind its own path; the states stay."""
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, src, status)
+    qp, qs = _delta_queries(q, k, out, state)
+    assert parent.dtype is torch.int32 and parent.shape == (n_req, N), "parent: int32 [n_req, N]"
+    _on_current_device(parent)
+    rc = load().mfd_delta_tree(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta),
+                               0 if eps is None else 1, eps or 0.0, scale, _p(parent), _p(n_nodes), _p(out), state._c,
+                               _p(src), _p(status), _s(stream))
+    _check(rc, "mfd_delta_tree")
+
+
+def mfd_delta_commit(k, v, g, beta, eps, accept_len, path_nodes, n_nodes, state, src, dst, status, stream=None) -> None:
+    """The state behind the accepted path (mfd_verify's accept_len and
+    path_nodes) of the rows that mfd_delta_tree was given."""
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status)
+    i32 = torch.int32
+    assert path_nodes.dtype is i32 and path_nodes.dim() == 2 and path_nodes.shape[0] == n_req, "path_nodes: int32 [n_req, L + 1]"
+    assert accept_len.dtype is i32 and accept_len.numel() == n_req, "accept_len: int32 [n_req]"
+    _on_current_device(accept_len, path_nodes)
+    rc = load().mfd_delta_commit(kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta), 0 if eps is None else 1,
+                                 eps or 0.0, path_nodes.shape[1] - 1, _p(accept_len), _p(path_nodes), _p(n_nodes), state._c,
+                                 _p(src), _p(dst), _p(status), _s(stream))
+    _check(rc, "mfd_delta_commit")
+
+
+def mfd_gated_norm(x, gate, w, eps, act, out, stream=None) -> None:
+    """out = norm of x [.., T, heads, D] over D, times w [D] and the activated
+    gate (x's shape); act: "none", "sigmoid" or "silu"."""
+    heads, D = x.shape[-2:]
+    assert x.dtype in (torch.bfloat16, torch.float16) and gate.dtype is x.dtype and out.dtype is x.dtype and w.dtype is x.dtype
+    assert gate.shape == x.shape and out.shape == x.shape and w.shape == (D,), "gate and out: as x; w: [D]"
+    assert act in _ACT, "act: none, sigmoid or silu"
+    (xp, xs), (gp, gs) = _rows(x, heads, D), _rows(gate, heads, D)
+    _on_current_device(x, gate, w, out)
+    rc = load().mfd_gated_norm(xp, xs, gp, gs, _DTYPE[x.dtype], x.numel() // (heads * D), heads, D, _p(w), eps, _ACT[act],
+                               _p(out), _s(stream))
+    _check(rc, "mfd_gated_norm")
+
+
+def mfd_residual_norm(y, residual, w_post, gate, act, scale, w_pre, eps, residual_out, x_out, stream=None) -> None:
+    """residual_out = residual + scale * act(gate) * norm(y; w_post) and x_out =
+    norm(residual_out; w_pre), rows of y [.., T, H].  w_post, gate, and w_pre
+    with x_out may be None; gate is [.., T, H] or one row."""
+    H = y.shape[-1]
+    T = y.numel() // H if H else 0
+    assert y.dtype in (torch.bfloat16, torch.float16) and residual.dtype is y.dtype and residual_out.dtype is y.dtype
+    assert residual.shape == y.shape and residual_out.shape == y.shape, "residual and residual_out: as y"
+    for w in (w_post, w_pre):
+        assert w is None or (w.dtype is y.dtype and w.shape == (H,)), "norm weights [H] of y's type"
+    assert (w_pre is None) == (x_out is None), "w_pre and x_out: both or none"
+    assert x_out is None or (x_out.shape == y.shape and x_out.dtype is y.dtype), "x_out: as y"
+    assert act in _ACT, "act: none, sigmoid or silu"
+    gp, gs = None, 0
+    if gate is not None:
+        assert gate.dtype is y.dtype, "gate of y's type"
+        if gate.numel() == H:
+            gp = _p(gate)
+        else:
+            assert gate.shape == y.shape, "gate: as y, or one row"
+            gp, gs = _rows(gate.unsqueeze(-2), 1, H)
+    _on_current_device(y, residual, w_post, gate, w_pre, residual_out, x_out)
+    rc = load().mfd_residual_norm(_p(y), _p(residual), _DTYPE[y.dtype], T, H, _p(w_post), gp, gs, _ACT[act], scale,
+                                  _p(w_pre), eps, _p(residual_out), _p(x_out), _s(stream))
+    _check(rc, "mfd_residual_norm")
 
 
 # ---------------------------------------------------------------------------
