@@ -1,5 +1,6 @@
 // delta.h -- the recurrent layers' calls as kernels see them: the gated delta
-// rule over rows, trees and accepted paths (delta_rows.cu), and the norms with
+// rule over rows, trees and accepted paths (delta_rows.cu,
+// delta_chunk.cu), and the norms with
 // gates (norms.cu).
 #pragma once
 
@@ -32,7 +33,10 @@ struct DeltaArgs {
 constexpr int DELTA_MAX_DEPTH = 16;   // of a tree's nodes, the root's being 0
 constexpr int DELTA_MAX_NODES = 513;
 
+// Rows from which the chunked form is the faster one.
+constexpr int DELTA_CHUNK_FROM = 24;
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream);
+cudaError_t launch_delta_chunk(const DeltaArgs &A, cudaStream_t stream);
 cudaError_t launch_delta_commit(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 cudaError_t launch_delta_tree(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 

@@ -1029,7 +1029,8 @@ int mfd_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_str
   DeviceInfo d;
   if ((rc = current_device_info(&d)) != MFD_OK) return rc;
   if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
-  return cuda_status(mfd::launch_delta_rows(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(N >= mfd::DELTA_CHUNK_FROM ? mfd::launch_delta_chunk(A, cs) : mfd::launch_delta_rows(A, d.n_sm, cs));
 }
 
 int mfd_delta_tree(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
