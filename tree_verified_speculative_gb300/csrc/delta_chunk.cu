@@ -25,16 +25,17 @@
 // fp32 registers.
 //
 // A block has one head's state, transposed: a column of the state is a lane of
-// tensor memory and a thread of the chain's warpgroup, so that scales, sums and
-// the state itself never cross threads.  Two warpgroups:
-//   prep   loads the rows, makes G and Q K^T, inverts I + A (it needs no state),
-//          a chunk ahead of
+// tensor memory, which two threads of the chain share, half of the column and
+// half of a chunk's rows each.  Scales, sums and the state itself never cross
+// columns.  Eight warps each (more would leave too few registers):
+//   prep   loads the rows, makes K K^T and Q K^T, inverts I + A (it needs no
+//          state), a chunk ahead of
 //   chain  S^T [K; Q]^T, b, y = (I + A)^-1 b, the state's step, outputs
 //
 // Columns of a state do not mix, but rows of a chunk do: 0 times what a later
 // row holds is no zero where that is a NaN or an infinity.  A chunk in which
 // anything is not finite, or leaves fp16's range, is done over row by row from
-// the inputs, in fp32, by the same threads.
+// the inputs, in fp32, by the chain's threads.
 #include <atomic>
 
 #include "delta.h"
@@ -48,15 +49,16 @@ namespace {
 constexpr int C = 64;         // rows of a chunk
 constexpr int MAX_DK = 128;
 constexpr int LANES = 128;    // columns of a state in a block
-constexpr int THREADS = 256;
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr int CHAIN = 256, PREP = 256, THREADS = CHAIN + PREP;
 constexpr float LEAST_LOG = -1e5f;  // of a decay: e^-1e5 is 0 in fp32, and sums of it stay finite
+constexpr float MAX_HALF = 65504.f;
 
 constexpr int BLOCK = 128 * 128;           // 64 columns of the 128 rows of keys and queries
 constexpr int TRI = C * 128;               // a 64 x 64 operand
 constexpr int PAD = C + 4;                 // floats of a row of the prep's scratch
 struct Coef {                              // of a chunk's rows
-  float rb[C], rx[C], until[C], ec[C];
+  float2 rhs[C];                           // of v and of S^T k in b
+  float until[C], ec[C];
 };
 struct alignas(1024) Stage {
   uint8_t kq[2 * BLOCK];  // keys' 64 rows, then queries': [64-column block][row][128 bytes, swizzled]
@@ -66,11 +68,14 @@ struct alignas(1024) Stage {
 };
 struct Smem {
   Stage st[2];
-  float A[C * PAD], T[C * PAD];
+  float At[C * PAD], T[C * PAD];           // A transposed; the inverse
+  uint16_t out[C * LANES];
   float n2[2 * C];                         // squared lengths
-  float chi[C], clo[C], g[C], beta[C];
+  float2 cc[C];                            // sums of log2 decays as two floats each
+  float g[C], beta[C];
   float fq[3][C];                          // outputs' factors, which are used a chunk later than the rest
-  uint64_t full[2], empty[2], gram, x, xq, u, s, o, drain;
+  float top[2][2][LANES];                  // [state, right sides][half][column]
+  uint64_t full[2], empty[2], gram, x, xq, u, s, o, drain, ps, pb, pz, py;
   uint32_t tmem;
   int bad[2], chain_bad, abort;
 };
@@ -78,11 +83,11 @@ constexpr int SMEM = sizeof(Smem) + 1024;  // and to a 1024-byte border
 static_assert(SMEM <= 232448, "shared memory of one CTA");
 
 // Tensor memory, columns.  What is written over what has been read by then.
-constexpr int TM_S = 0;      // the state's halves (64 + 64); right sides' (32 + 32); the state's step (128)
-constexpr int TM_XK = 128;   // S^T K^T; the updates
-constexpr int TM_XQ = 192;   // S^T Q^T, then outputs; two in turn
-constexpr int TM_Y = 320;    // the updates' halves (32 + 32)
-constexpr int TM_Z = 384;    // the updates' halves times their decays
+constexpr int TM_S = 0;      // the state in fp32, times a power of two for each column
+constexpr int TM_H = 128;    // its halves (64 + 64); right sides' (32 + 32), then the updates'
+constexpr int TM_Z = 192;    // the updates' halves times their decays
+constexpr int TM_XK = 256;   // S^T K^T; the updates
+constexpr int TM_XQ = 320;   // S^T Q^T, then outputs; two in turn
 constexpr int TM_G = 448;    // [K; Q] K^T
 
 __device__ __forceinline__ float max_nan(float a, float b, float c) {  // largest magnitude; NaN if there is one
@@ -105,6 +110,35 @@ __device__ __forceinline__ void halves(float a, float b, uint32_t &hi, uint32_t 
   const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// The same of x times a power of two that brings the column's largest to [2^11,
+// 2^12): hi is x to the nearest even number, 11 bits at most, lo what is left, to
+// 2^-12 of 1.  The two roundings by 1.5 * 2^24 cost no conversions back.
+__device__ __forceinline__ void halves_at(uint64_t x, uint64_t up, uint32_t &hi, uint32_t &lo) {
+  const uint64_t grid = pair(0x1.8p24f, 0x1.8p24f), back = pair(-0x1.8p24f, -0x1.8p24f), minus = pair(-1.f, -1.f);
+  const uint64_t a = add2(fma2(x, up, grid), back);
+  const float2 h = unpair(a), l = unpair(fma2(x, up, fma2(a, minus, pair(0.f, 0.f))));
+  const __half2 hh = __floats2half2_rn(h.x, h.y), ll = __floats2half2_rn(l.x, l.y);
+  hi = *reinterpret_cast<const uint32_t *>(&hh);
+  lo = *reinterpret_cast<const uint32_t *>(&ll);
+}
+// A number as the sum of two floats.
+struct Two {
+  float hi, lo;
+};
+constexpr float LOG2E_HI = 0x1.715476p+0f, LOG2E_LO = 0x1.4ae0cp-26f;  // log2 e
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x))};
+}
+__device__ __forceinline__ Two two_sum(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+__device__ __forceinline__ Two two_product(float a, float hi, float lo) {
+  const float p = __fmul_rn(a, hi);
+  return {p, __fmaf_rn(a, lo, __fmaf_rn(a, hi, -p))};
 }
 template <typename T>
 __device__ __forceinline__ float to_float(uint16_t x) { return unpack2<T>(x).x; }
@@ -135,16 +169,12 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
       sm.bad[i] = 0;
     }
-    mbar_init(&sm.gram, 1);
-    mbar_init(&sm.x, 1);
-    mbar_init(&sm.xq, 1);
-    mbar_init(&sm.u, 1);
-    mbar_init(&sm.s, 1);
-    mbar_init(&sm.o, 1);
-    mbar_init(&sm.drain, 2);
+    for (uint64_t *b : {&sm.gram, &sm.x, &sm.xq, &sm.u, &sm.s, &sm.o}) mbar_init(b, 1);
+    for (uint64_t *b : {&sm.ps, &sm.pb, &sm.pz, &sm.py}) mbar_init(b, CHAIN / 32);
+    mbar_init(&sm.drain, 5);
     sm.chain_bad = 0;
     sm.abort = 0;
     fence_mbar_init();
@@ -174,23 +204,26 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       if (!*abort_flag) report(p.status, MFD_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+  };
+  auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
+    wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
   };
 
-  if (warp >= 4) {
+  if (warp >= CHAIN / 32) {
     // ----------------------------------------------------------- prep
-    const int t = tid - 128, c8 = t & 15, r8 = t >> 4;
-    uint4 raw[16];
+    const int t = tid - CHAIN, c8 = t & 15, r16 = t >> 4;
+    uint4 raw[8];
     float graw = 0.f, braw = 0.f;
-    // rows r8, r8 + 8, .. of keys, then of queries, 8 columns each; g and beta of row t
+    // rows r16, r16 + 16, .. of keys, then of queries, 8 columns each; g and beta of row t
     auto load = [&](int n) {
       const int row0 = n * C;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = row0 + (i * 8 + r8) % C;
+      for (int i = 0; i < 8; ++i) {
+        const int row = row0 + (i * 16 + r16) % C;
         raw[i] = make_uint4(0, 0, 0, 0);
         if (row < nn && c8 * 8 < p.Dk)
-          raw[i] = __ldg(reinterpret_cast<const uint4 *>((i < 8 ? p.k + (tok0 + row) * p.k_stride : p.q + (tok0 + row) * p.q_stride) +
+          raw[i] = __ldg(reinterpret_cast<const uint4 *>((i < 4 ? p.k + (tok0 + row) * p.k_stride : p.q + (tok0 + row) * p.q_stride) +
                                                          hk * p.Dk + c8 * 8));
       }
       graw = braw = 0.f;
@@ -200,30 +233,21 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       }
     };
     if (n_chunk) load(0);
-    for (int i = t; i < C * PAD; i += 128) sm.T[i] = 0.f;  // above its diagonal blocks it stays so
+    for (int i = t; i < C * PAD; i += PREP) sm.T[i] = 0.f;  // above its diagonal blocks it stays so
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
-      wait(&sm.empty[n & 1], ((n >> 1) & 1u) ^ 1u);
+      wait_warp(&sm.empty[n & 1], ((n >> 1) & 1u) ^ 1u);
+      float most = 0.f;  // largest magnitude, NaN where there is one
       bool bad = false;
       if (t == 0) sm.bad[n & 1] = 0;
-      // values, as they are
-      for (int i = t; i < C * 16; i += 128) {
-        const int row = i >> 4, ch = i & 15, col = slice * LANES + ch * 8;
-        uint8_t *dst = reinterpret_cast<uint8_t *>(st.v) + row * (LANES * 2) + ch * 16;
-        if (!ok) continue;
-        if (n * C + row < nn && col < p.Dv)
-          cp_async16(smem_u32(dst), p.v + (tok0 + n * C + row) * p.v_stride + h * p.Dv + col);
-        else
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-      }
       if (t < C) {
         sm.g[t] = graw < LEAST_LOG ? LEAST_LOG : graw;
         sm.beta[t] = braw;
         if (!finite(braw) || !(graw < INFINITY)) bad = true;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = i * 8 + r8;
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 16 + r16;
         float x[8], ss = 0.f;
         unpack8<T>(raw[i], x);
 #pragma unroll
@@ -243,529 +267,611 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         }
       }
       fence_async_smem();
-      named_sync(2, 128);
-      if (warp == 4) {
+      named_sync(2, PREP);
+      if (warp == CHAIN / 32) {
         if (elect_one() && ok) {
           tc_fence_after();
           constexpr uint32_t id = idesc_16<__half>(128, C, false);
           const uint32_t a = desc_lo(smem_u32(st.kq), 16);
           const int steps = p.Dk / 16;
-          for (int k = 0; k < steps; ++k) {
-            const uint32_t at = (k >> 2) * (BLOCK >> 4) + (k & 3) * 2;
-            mma_ss(tmem + TM_G, a + at, a + at, id, k != 0);
-          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < steps) {
+              const uint32_t at = (k >> 2) * (BLOCK >> 4) + (k & 3) * 2;
+              mma_ss(tmem + TM_G, a + at, a + at, id, k != 0);
+            }
           tc_commit(&sm.gram);
         }
         __syncwarp();
-        // sums of the log decays, in 64 bits, two rows a lane; kept in units of log 2 as two floats
-        const double a = (double)sm.g[2 * lane], b = (double)sm.g[2 * lane + 1];
-        double run = a + b;
+      } else if (warp == CHAIN / 32 + 1) {
+        // sums of the log decays in units of log 2, two rows a lane, as two floats each
+        const Two a = two_product(sm.g[2 * lane], LOG2E_HI, LOG2E_LO), b = two_product(sm.g[2 * lane + 1], LOG2E_HI, LOG2E_LO);
+        const Two own = two_sum(a, b);
+        Two run = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double up = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += up;
+          const Two up = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+          if (lane >= o) run = two_sum(up, run);
         }
-        const double c1 = run * (double)1.4426950408889634, c0 = (run - b) * (double)1.4426950408889634;
-        sm.chi[2 * lane] = (float)c0;
-        sm.clo[2 * lane] = (float)(c0 - (double)(float)c0);
-        sm.chi[2 * lane + 1] = (float)c1;
-        sm.clo[2 * lane + 1] = (float)(c1 - (double)(float)c1);
+        Two before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+        if (lane == 0) before = {0.f, 0.f};
+        const Two first = two_sum(before, a);
+        sm.cc[2 * lane] = make_float2(first.hi, first.lo);
+        sm.cc[2 * lane + 1] = make_float2(run.hi, run.lo);
+      }
+      // values, as they are
+      for (int i = t; i < C * 16; i += PREP) {
+        const int row = i >> 4, ch = i & 15, col = slice * LANES + ch * 8;
+        uint8_t *dst = reinterpret_cast<uint8_t *>(st.v) + row * (LANES * 2) + ch * 16;
+        if (!ok) continue;
+        if (n * C + row < nn && col < p.Dv)
+          cp_async16(smem_u32(dst), p.v + (tok0 + n * C + row) * p.v_stride + h * p.Dv + col);
+        else
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
       }
       if (n + 1 < n_chunk) load(n + 1);
-      named_sync(2, 128);
-      wait(&sm.gram, n & 1u);
-      // this thread's row of [K; Q] K^T
-      const int row = t & 63;
-      const bool is_q = t >= C;
-      const float chi = sm.chi[row], clo = sm.clo[row];
-      const float ss = sm.n2[t];
+      named_sync(2, PREP);
+      wait_warp(&sm.gram, n & 1u);
+      // this thread's row of [K; Q] K^T, half of its columns
+      const int row = t & 63, j1 = (t >> 7) * 32;
+      const bool is_q = (t & 127) >= C;
+      const float2 ci = sm.cc[row];
+      const float ss = sm.n2[t & 127];
       const int half_e = ((int)(__float_as_uint(ss) >> 23) - 127) >> 1;
       const float left = (p.normalize ? rsqrtf(ss + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
       const float br = sm.beta[row] * left, brr = br * left;
-      if (!is_q) {
-        const float ec = ex2(chi + clo);
-        const float until = ex2((sm.chi[C - 1] - chi) + (sm.clo[C - 1] - clo));
-        st.c.rb[row] = br;
-        st.c.rx[row] = -brr * ec;
+      if (t < C) {
+        const float2 end = sm.cc[C - 1];
+        const float ec = ex2(ci.x + ci.y), until = ex2((end.x - ci.x) + (end.y - ci.y));
+        st.c.rhs[row] = make_float2(br, -brr * ec);
         st.c.until[row] = until;
         st.c.ec[row] = ec;
         if (!finite(br) || !finite(brr * ec) || !finite(until)) bad = true;
-      } else {
+      } else if (t < 2 * C) {
         sm.fq[n % 3][row] = left * p.scale;
         if (!finite(left)) bad = true;
       }
       if (ok) {
         tc_fence_after();
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint32_t x[32];
-          tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + TM_G + part * 32, x);
-          tmem_wait_ld();
-          tie32(x);
-#pragma unroll
-          for (int k8 = 0; k8 < 4; ++k8) {
-            const int j0 = part * 32 + k8 * 8;
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int j = j0 + e;
-              const float d = ex2((chi - sm.chi[j]) + (clo - sm.clo[j]));
-              const float z = __uint_as_float(x[k8 * 8 + e]) * (is_q ? d : d * brr);
-              y[e] = j < row || (is_q && j == row) ? z : 0.f;
-              if (!finite(y[e])) bad = true;
-            }
-            if (is_q) {
-              uint4 hi, lo;
-              halves(y[0], y[1], hi.x, lo.x);
-              halves(y[2], y[3], hi.y, lo.y);
-              halves(y[4], y[5], hi.z, lo.z);
-              halves(y[6], y[7], hi.w, lo.w);
-              const int at = row * 128 + (((j0 >> 3) ^ (row & 7)) << 4);
-              *reinterpret_cast<uint4 *>(st.ph + at) = hi;
-              *reinterpret_cast<uint4 *>(st.pl + at) = lo;
-            } else {
-              *reinterpret_cast<float4 *>(&sm.A[row * PAD + j0]) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4 *>(&sm.A[row * PAD + j0 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
-            }
-          }
-        }
+        uint32_t x[32];
+        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + TM_G + j1, x);
+        tmem_wait_ld();
+        tie32(x);
         tc_fence_before();
-      }
-      named_sync(2, 128);
-      // (I + A)^-1: of the four 16 x 16 blocks on the diagonal, a column a thread ..
-      if (t < C) {
-        const int b = t >> 4, col = t & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float acc = i == col ? 1.f : 0.f;
-#pragma unroll
-          for (int m = 0; m < i; ++m) acc = fmaf(-sm.A[(16 * b + i) * PAD + 16 * b + m], x[m], acc);
-          x[i] = i < col ? 0.f : acc;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sm.T[(16 * b + i) * PAD + 16 * b + col] = x[i];
-      }
-      named_sync(2, 128);
-      // .. then of blocks twice as large, twice: the lower left part of a pair is
-      // -T_below A_left T_above.  A's upper right parts, which nothing reads, hold
-      // the first product.
-#pragma unroll 1
-      for (int size = 16; size <= 32; size *= 2) {
-        // a thread's 4 columns of a row: pairs * size * size / 4 of them
-        const int quads = size / 4, per = size * quads;
-        for (int i = t; i < (C / (2 * size)) * per; i += 128) {
-          const int b = i / per * 2 * size, row = i % per / quads, col = i % quads * 4;
-          float4 acc = make_float4(0, 0, 0, 0);
-          for (int m = 0; m < size; ++m) {
-            const float a = sm.A[(b + size + row) * PAD + b + m];
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.T[(b + m) * PAD + b + col]);
-            acc.x = fmaf(a, x.x, acc.x);
-            acc.y = fmaf(a, x.y, acc.y);
-            acc.z = fmaf(a, x.z, acc.z);
-            acc.w = fmaf(a, x.w, acc.w);
-          }
-          *reinterpret_cast<float4 *>(&sm.A[(b + row) * PAD + b + size + col]) = acc;
-        }
-        named_sync(2, 128);
-        for (int i = t; i < (C / (2 * size)) * per; i += 128) {
-          const int b = i / per * 2 * size, row = i % per / quads, col = i % quads * 4;
-          float4 acc = make_float4(0, 0, 0, 0);
-          for (int m = 0; m <= row; ++m) {
-            const float a = -sm.T[(b + size + row) * PAD + b + size + m];
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.A[(b + m) * PAD + b + size + col]);
-            acc.x = fmaf(a, x.x, acc.x);
-            acc.y = fmaf(a, x.y, acc.y);
-            acc.z = fmaf(a, x.z, acc.z);
-            acc.w = fmaf(a, x.w, acc.w);
-          }
-          *reinterpret_cast<float4 *>(&sm.T[(b + size + row) * PAD + b + col]) = acc;
-        }
-        named_sync(2, 128);
-      }
-      {
-        // its halves: half a row a thread; what lies above the diagonal is zero
-        const int row = t >> 1, j1 = (t & 1) * 32;
+        const float f = is_q ? 1.f : brr;
 #pragma unroll
         for (int k8 = 0; k8 < 4; ++k8) {
           const int j0 = j1 + k8 * 8;
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = j0 + e <= row ? sm.T[row * PAD + j0 + e] : 0.f;
+          for (int e = 0; e < 8; ++e) {
+            const int j = j0 + e;
+            const float2 cj = sm.cc[j];
+            const float z = __uint_as_float(x[k8 * 8 + e]) * (f * ex2((ci.x - cj.x) + (ci.y - cj.y)));
+            y[e] = j < row || (is_q && j == row) ? z : 0.f;
+          }
+          most = max_nan(most, y[0], y[1]);
+          most = max_nan(most, y[2], y[3]);
+          most = max_nan(most, y[4], y[5]);
+          most = max_nan(most, y[6], y[7]);
+          if (is_q) {
+            uint4 hi, lo;
+            halves(y[0], y[1], hi.x, lo.x);
+            halves(y[2], y[3], hi.y, lo.y);
+            halves(y[4], y[5], hi.z, lo.z);
+            halves(y[6], y[7], hi.w, lo.w);
+            const int at = row * 128 + (((j0 >> 3) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(st.ph + at) = hi;
+            *reinterpret_cast<uint4 *>(st.pl + at) = lo;
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!(fabsf(y[e]) < 65504.f)) bad = true;
+            for (int e = 0; e < 8; ++e) sm.At[(j0 + e) * PAD + row] = y[e];
+          }
+        }
+      }
+      named_sync(2, PREP);
+      // (I + A)^-1: of the four 16 x 16 blocks on the diagonal, a column a thread: an
+      // element that is known goes out to all below it ..
+      if ((warp & 3) == 2) {
+        const int b = (t >> 7) * 32 + (lane & 16), col = lane & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.f : 0.f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m)
+#pragma unroll
+          for (int i = (m + 1) & ~3; i < 16; i += 4) {  // A is 0 on and above its diagonal
+            const float4 a = *reinterpret_cast<const float4 *>(&sm.At[(b + m) * PAD + b + i]);
+            x[i] = fmaf(-a.x, x[m], x[i]);
+            x[i + 1] = fmaf(-a.y, x[m], x[i + 1]);
+            x[i + 2] = fmaf(-a.z, x[m], x[i + 2]);
+            x[i + 3] = fmaf(-a.w, x[m], x[i + 3]);
+          }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sm.T[(b + i) * PAD + b + col] = x[i];
+      }
+      named_sync(2, PREP);
+      // .. then of blocks twice as large, twice: the lower left part of a pair is
+      // -T_22 A_21 T_11.  The first product goes where A's transpose has its empty
+      // block.
+      {
+        const int b = (t >> 7) * 32, i = b + 16 + ((t & 127) >> 3), j = b + (t & 7) * 2;
+        float2 acc = make_float2(0, 0);
+#pragma unroll 8
+        for (int m = 0; m < 16; ++m) {
+          const float a = sm.At[(b + m) * PAD + i];
+          const float2 x = *reinterpret_cast<const float2 *>(&sm.T[(b + m) * PAD + j]);
+          acc.x = fmaf(a, x.x, acc.x);
+          acc.y = fmaf(a, x.y, acc.y);
+        }
+        *reinterpret_cast<float2 *>(&sm.At[i * PAD + j]) = acc;
+        named_sync(2, PREP);
+        acc = make_float2(0, 0);
+#pragma unroll 8
+        for (int m = 0; m < 16; ++m) {
+          const float a = -sm.T[i * PAD + b + 16 + m];
+          const float2 x = *reinterpret_cast<const float2 *>(&sm.At[(b + 16 + m) * PAD + j]);
+          acc.x = fmaf(a, x.x, acc.x);
+          acc.y = fmaf(a, x.y, acc.y);
+        }
+        *reinterpret_cast<float2 *>(&sm.T[i * PAD + j]) = acc;
+      }
+      named_sync(2, PREP);
+      {
+        const int i = 32 + (t >> 3), j = (t & 7) * 4;
+        float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+          const float a = sm.At[m * PAD + i];
+          const float4 x = *reinterpret_cast<const float4 *>(&sm.T[m * PAD + j]);
+          acc.x = fmaf(a, x.x, acc.x);
+          acc.y = fmaf(a, x.y, acc.y);
+          acc.z = fmaf(a, x.z, acc.z);
+          acc.w = fmaf(a, x.w, acc.w);
+        }
+        *reinterpret_cast<float4 *>(&sm.At[i * PAD + j]) = acc;
+        named_sync(2, PREP);
+        acc = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int m = 0; m < 32; ++m) {
+          const float a = -sm.T[i * PAD + 32 + m];
+          const float4 x = *reinterpret_cast<const float4 *>(&sm.At[(32 + m) * PAD + j]);
+          acc.x = fmaf(a, x.x, acc.x);
+          acc.y = fmaf(a, x.y, acc.y);
+          acc.z = fmaf(a, x.z, acc.z);
+          acc.w = fmaf(a, x.w, acc.w);
+        }
+        *reinterpret_cast<float4 *>(&sm.T[i * PAD + j]) = acc;
+      }
+      named_sync(2, PREP);
+      {
+        // its halves: a quarter of a row a thread
+        const int i = t >> 2, j1 = (t & 3) * 16;
+#pragma unroll
+        for (int k8 = 0; k8 < 2; ++k8) {
+          const int j0 = j1 + k8 * 8;
+          const float4 a = *reinterpret_cast<const float4 *>(&sm.T[i * PAD + j0]);
+          const float4 b = *reinterpret_cast<const float4 *>(&sm.T[i * PAD + j0 + 4]);
+          most = max_nan(most, a.x, a.y);
+          most = max_nan(most, a.z, a.w);
+          most = max_nan(most, b.x, b.y);
+          most = max_nan(most, b.z, b.w);
           uint4 hi, lo;
-          halves(y[0], y[1], hi.x, lo.x);
-          halves(y[2], y[3], hi.y, lo.y);
-          halves(y[4], y[5], hi.z, lo.z);
-          halves(y[6], y[7], hi.w, lo.w);
-          const int at = row * 128 + (((j0 >> 3) ^ (row & 7)) << 4);
+          halves(a.x, a.y, hi.x, lo.x);
+          halves(a.z, a.w, hi.y, lo.y);
+          halves(b.x, b.y, hi.z, lo.z);
+          halves(b.z, b.w, hi.w, lo.w);
+          const int at = i * 128 + (((j0 >> 3) ^ (i & 7)) << 4);
           if (ok) {
             *reinterpret_cast<uint4 *>(st.th + at) = hi;
             *reinterpret_cast<uint4 *>(st.tl + at) = lo;
           }
         }
       }
-      if (bad) sm.bad[n & 1] = 1;
+      if (bad || !(most < MAX_HALF)) sm.bad[n & 1] = 1;
       cp_async_wait();
       fence_async_smem();
-      named_sync(2, 128);
+      named_sync(2, PREP);
       if (t == 0 && ok) mbar_arrive(&sm.full[n & 1]);
-    }
-    if (warp == 4) {
-      if (elect_one()) tc_commit(&sm.drain);
-      __syncwarp();
     }
   } else {
     // ----------------------------------------------------------- chain
-    const int col = slice * LANES + tid;
+    // A thread has rows 64 half .. of its column of the state, and rows 32 half ..
+    // of a chunk.
+    constexpr int SD = MAX_DK / 2, SC = C / 2;
+    const int half = warp >> 2, l = tid & 127;  // column in the block
+    const int d0 = half * SD, i0 = half * SC;
+    const int col = slice * LANES + l;
     const bool have = col < p.Dv;
-    const uint32_t me = tmem + ((uint32_t)(warp * 32) << 16);
-    float s[MAX_DK];
+    const uint32_t me = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // the state to tensor memory; `back`: what its numbers there are times
+    float back = 1.f;
     {
-      const float *from = p.s + ((int64_t)q.src * p.Hv + h) * p.Dk * p.Dv + col;
-#pragma unroll
-      for (int d = 0; d < MAX_DK; ++d) s[d] = q.ok && q.src >= 0 && have && d < p.Dk ? from[(int64_t)d * p.Dv] : 0.f;
-    }
-    uint16_t *out = p.out + (tok0 * p.Hv + h) * p.Dv + col;
-    const int64_t out_row = (int64_t)p.Hv * p.Dv;
-    if (!q.ok && tid == 0) report(p.status, MFD_ERR_INPUT);
-    if (have)
-      for (int i = nn; i < p.N; ++i) out[i * out_row] = 0;
-
-    uint32_t n_x = 0, n_u = 0, n_s = 0, n_o = 0;  // uses of each barrier
-    bool pending = false;  // outputs of the chunk before wait in tensor memory
-    float out_scale = 0.f;
-    uint32_t pending_xq = 0;
-    int pending_n = 0;
-    // outputs of a chunk that are left: scale s_i times what the products gave
-    auto put_outputs = [&]() {
-      if (!pending) return;
-      pending = false;
-      wait(&sm.o, (n_o - 1u) & 1u);
-      if (!ok) return;
-      tc_fence_after();
-      const float *fq = sm.fq[pending_n % 3];
-      const int rows = min(C, nn - pending_n * C);
-      uint16_t *to = out + (int64_t)pending_n * C * out_row;
+      const float *from = p.s + (((int64_t)q.src * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+      const bool some = q.ok && q.src >= 0 && have;
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        uint32_t x[32];
-        tmem_ld32(me + TM_XQ + pending_xq * C + part * 32, x);
+      for (int d = 0; d < SD; d += 16) {
+        uint32_t x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = some && d0 + d + e < p.Dk ? __float_as_uint(from[(int64_t)(d + e) * p.Dv]) : 0u;
+        tmem_st16(me + TM_S + d0 + d, x);
+      }
+      tmem_wait_st();
+    }
+    if (!q.ok && tid == 0) report(p.status, MFD_ERR_INPUT);
+    {  // rows that are not live
+      const int ch = tid & 15;
+      if (slice * LANES + ch * 8 < p.Dv)
+        for (int i = nn + (tid >> 4); i < p.N; i += CHAIN / 16)
+          st_global16(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + slice * LANES + ch * 8, make_uint4(0, 0, 0, 0));
+    }
+    bool slow = false;
+    int pending = -1;  // chunk whose outputs wait in tensor memory
+    float out_scale = 0.f;
+    // Outputs of that chunk: scale s_i times what the products gave, through shared
+    // memory for whole 16 bytes (two bytes a lane took 6,000 cycles a chunk).
+    auto put_outputs = [&]() {
+      if (pending < 0) return;
+      wait_warp(&sm.o, pending & 1u);
+      const float *fq = sm.fq[pending % 3];
+      if (ok) {
+        tc_fence_after();
+        uint32_t x[SC];
+        tmem_ld32(me + TM_XQ + (pending & 1) * C + i0, x);
         tmem_wait_ld();
         tie32(x);
+        tc_fence_before();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float y = __uint_as_float(x[i]) * out_scale * fq[part * 32 + i];
-          if (have && part * 32 + i < rows) to[(part * 32 + i) * out_row] = (uint16_t)pack2<T>(y, 0.f);
+        for (int i = 0; i < SC; ++i)
+          sm.out[(i0 + i) * LANES + l] = (uint16_t)pack2<T>(__uint_as_float(x[i]) * out_scale * fq[i0 + i], 0.f);
+      }
+      named_sync(3 + half, 128);
+      const int rows = nn - pending * C, ch = l & 15;
+      if (ok && slice * LANES + ch * 8 < p.Dv) {
+#pragma unroll
+        for (int k = 0; k < SC / 8; ++k) {
+          const int i = i0 + k * 8 + (l >> 4);
+          if (i < rows)
+            st_global16(p.out + ((tok0 + pending * C + i) * p.Hv + h) * p.Dv + slice * LANES + ch * 8,
+                        *reinterpret_cast<const uint4 *>(&sm.out[i * LANES + ch * 8]));
         }
       }
+      pending = -1;
     };
-    // whether any thread of the chain says so; also a barrier
-    auto any = [&](bool x) {
-      uint32_t y;
+    // the larger of this thread's and the column's other thread's
+    auto of_both = [&](int which, float x) {
+      sm.top[which][half][l] = x;
+      named_sync(5 + (warp & 3), 64);
+      return max_nan(x, sm.top[which][half ^ 1][l], 0.f);
+    };
+    auto arrive = [&](uint64_t *bar) {
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t"
-          "setp.ne.u32 p, %1, 0;\n\t"
-          "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-          "selp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(y)
-          : "r"((uint32_t)x)
-          : "memory");
-      return y != 0;
+      if (lane == 0 && ok) mbar_arrive(bar);
+    };
+
+    constexpr uint32_t id = idesc_16<__half>(128, C, false), id_kd = idesc_16<__half>(128, 128, true);
+    const int steps = p.Dk / 16;
+    // Products: one lane of warp `who` issues them once all of the chain's warps have
+    // arrived; a warp for each kind, so that none is held up for long.
+    auto products = [&](int who, uint64_t *ready, uint32_t par, auto issue) {
+      if (warp != who) return;
+      wait_warp(ready, par);
+      if (elect_one() && ok) {
+        tc_fence_after();
+        issue();
+      }
+      __syncwarp();
     };
 
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
-      const uint32_t xq = me + TM_XQ + (n & 1) * C;
-      // the state's halves
+      const uint32_t xq = me + TM_XQ + (n & 1) * C + i0;
+      const uint32_t par = n & 1u;
+      bool bad = false;
+      // the state's halves; the updates' of the chunk before, which they go over, have
+      // been read with its outputs
+      if (pending >= 0) wait_warp(&sm.o, pending & 1u);
+      tc_fence_after();
       float top = 0.f;
+      if (ok)
+#pragma unroll 1
+        for (int d = 0; d < SD; d += 32) {
+          uint32_t x[32];
+          tmem_ld32(me + TM_S + d0 + d, x);
+          tmem_wait_ld();
+          tie32(x);
 #pragma unroll
-      for (int d = 0; d < MAX_DK; d += 2) top = max_nan(top, s[d], s[d + 1]);
-      float back_s;
-      const float up_s = power_for(top, 11, back_s);
+          for (int e = 0; e < 32; e += 2) top = max_nan(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        }
+      top = of_both(0, top);
+      const bool was_finite = finite(top);  // a column that is not has nothing more to lose
+      float down;  // of the halves, to the state's numbers in tensor memory
+      const float up = power_for(top, 11, down);
       if (ok) {
-#pragma unroll
-        for (int d = 0; d < MAX_DK; d += 32) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) halves(s[d + 2 * e] * up_s, s[d + 2 * e + 1] * up_s, hi[e], lo[e]);
-          tmem_st16(me + TM_S + d / 2, hi);
-          tmem_st16(me + TM_S + 64 + d / 2, lo);
-        }
-        tmem_wait_st();
-      }
-      wait(&sm.full[n & 1], (n >> 1) & 1u);
-      tc_fence_before();
-      bool slow = any(!finite(top) || (ok && *(volatile int *)&sm.bad[n & 1]));
-      if (!slow) {
-        if (warp == 0) {
-          if (elect_one() && ok) {
-            tc_fence_after();
-            constexpr uint32_t id = idesc_16<__half>(128, C, false);
-            const int steps = p.Dk / 16;
+        const uint64_t up2 = pair(up, up);
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {  // keys, then queries
-              const uint32_t b = desc_lo(smem_u32(st.kq), 16) + half * (C * 128 >> 4);
-              const uint32_t d = tmem + (half ? TM_XQ + (n & 1) * C : TM_XK);
-              for (int k = 0; k < 2 * steps; ++k) {
-                const int kk = k < steps ? k : k - steps;
-                mma_ts(d, tmem + TM_S + (k < steps ? 0 : 64) + kk * 8, b + (kk >> 2) * (BLOCK >> 4) + (kk & 3) * 2, id, k != 0);
-              }
-              tc_commit(half ? &sm.xq : &sm.x);
-            }
-          }
-          __syncwarp();
+        for (int d = 0; d < SD; d += 16) {
+          uint32_t x[16], hi[8], lo[8];
+          tmem_ld16(me + TM_S + d0 + d, x);
+          tmem_wait_ld();
+          tie16(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            halves_at(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), up2, hi[e], lo[e]);
+          tmem_st8(me + TM_H + (d0 + d) / 2, hi);
+          tmem_st8(me + TM_H + 64 + (d0 + d) / 2, lo);
         }
-        put_outputs();
-        // right sides
-        wait(&sm.x, n_x & 1u);
+      }
+      const float back_s = down * back;  // of S^T K^T to true numbers
+      arrive(&sm.ps);
+      wait_warp(&sm.full[n & 1], (n >> 1) & 1u);
+      products(0, &sm.ps, par, [&]() {  // S^T K^T, then S^T Q^T
+        const uint32_t kq = desc_lo(smem_u32(st.kq), 16), d = tmem + TM_XQ + (n & 1) * C;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if ((k & 7) < steps)
+            mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, kq + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id, k != 0);
+        tc_commit(&sm.x);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if ((k & 7) < steps)
+            mma_ts(d, tmem + TM_H + k * 8, kq + (C * 128 >> 4) + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id, k != 0);
+        tc_commit(&sm.xq);
+      });
+      put_outputs();
+      // right sides
+      wait_warp(&sm.x, par);
+      tc_fence_after();
+      float b[SC];
+#pragma unroll
+      for (int part = 0; part < SC; part += 16) {
+        uint32_t x[16];
+        if (ok) {
+          tmem_ld16(me + TM_XK + i0 + part, x);
+          tmem_wait_ld();
+          tie16(x);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = st.c.rhs[i0 + part + i];
+          const float v = to_float<T>(st.v[(i0 + part + i) * LANES + l]);
+          b[part + i] = ok ? fmaf(f.y, __uint_as_float(x[i]) * back_s, f.x * v) : 0.f;
+        }
+      }
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < SC; i += 2) top = max_nan(top, b[i], b[i + 1]);
+      top = of_both(1, top);
+      if (!finite(top) && was_finite) bad = true;
+      float back_b;
+      float up_b = power_for(top, 11, back_b);
+      if (back_b < back_s * 0x1p-60f) {  // nothing to add: the outputs' common scale stays near the state's
+        back_b = back_s * 0x1p-60f;
+        up_b = 1.f / back_b;  // a power of two
+      }
+      wait_warp(&sm.xq, par);  // the state's halves have been read
+      tc_fence_after();
+      {
+        const uint64_t up = pair(up_b, up_b);
+#pragma unroll
+        for (int i = 0; i < SC; i += 16) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) halves_at(pair(b[i + 2 * e], b[i + 2 * e + 1]), up, hi[e], lo[e]);
+          if (ok) {
+            tmem_st8(me + TM_H + (i0 + i) / 2, hi);
+            tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
+          }
+        }
+      }
+      arrive(&sm.pb);
+      products(1, &sm.pb, par, [&]() {
+        const uint32_t th = desc_lo(smem_u32(st.th), 16), tl = desc_lo(smem_u32(st.tl), 16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, th + (k & 3) * 2, id, k != 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, tl + k * 2, id, 1);
+        tc_commit(&sm.u);
+      });
+      // meanwhile the outputs' first part, to the updates' scale (2^3 less than the right sides')
+      up_b *= 0.125f;
+      back_b *= 8.f;
+      if (ok) {
+        const float f = up_b * back_s;
+        uint32_t x[SC];
+        tmem_ld32(xq, x);
+        tmem_wait_ld();
+        tie32(x);
+#pragma unroll
+        for (int i = 0; i < SC; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * (f * st.c.ec[i0 + i]));
+        tmem_st16(xq, x);
+        tmem_st16(xq + 16, x + 16);
+      }
+      // and the state, decayed
+      if (ok) {
+        const float f = st.c.ec[C - 1] * (up_b * back);
+#pragma unroll 1
+        for (int d = 0; d < SD; d += 16) {
+          uint32_t x[16];
+          tmem_ld16(me + TM_S + d0 + d, x);
+          tmem_wait_ld();
+          tie16(x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+          tmem_st16(me + TM_S + d0 + d, x);
+        }
+      }
+      back = back_b;
+      // the updates
+      wait_warp(&sm.u, par);
+      if (ok) {
         tc_fence_after();
-        float b[C];
-        top = 0.f;
+        uint32_t x[SC];
+        tmem_ld32(me + TM_XK + i0, x);
+        tmem_wait_ld();
+        tie32(x);
+#pragma unroll
+        for (int i = 0; i < SC; ++i) b[i] = __uint_as_float(x[i]) * 0.125f;
+      }
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < SC; i += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + i + 2 * e]);
+          const float z0 = b[i + 2 * e] * f.x, z1 = b[i + 2 * e + 1] * f.y;
+          most = max_nan(most, z0, z1);
+          most = max_nan(most, b[i + 2 * e], b[i + 2 * e + 1]);
+          halves(z0, z1, hi[e], lo[e]);
+        }
         if (ok) {
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint32_t x[32];
-            tmem_ld32(me + TM_XK + part * 32, x);
-            tmem_wait_ld();
-            tie32(x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int row = part * 32 + i;
-              const float v = to_float<T>(st.v[row * LANES + tid]);
-              b[row] = fmaf(st.c.rx[row], __uint_as_float(x[i]) * back_s, st.c.rb[row] * v);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < C; i += 2) top = max_nan(top, b[i], b[i + 1]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < C; ++i) b[i] = 0.f;
+          tmem_st8(me + TM_Z + (i0 + i) / 2, hi);
+          tmem_st8(me + TM_Z + 32 + (i0 + i) / 2, lo);
         }
-        float back_b;
-        float up_b = power_for(top, 8, back_b);
-        if (up_b > up_s * 0x1p60f) {  // nothing to add: the outputs' common scale stays near the state's
-          up_b = up_s * 0x1p60f;
-          back_b = back_s * 0x1p-60f;
-        }
-        wait(&sm.xq, n_x & 1u);  // the state's halves have been read
-        ++n_x;
+      }
+      if (bad || (was_finite && !(most < MAX_HALF))) *(volatile int *)&sm.chain_bad = n + 1;
+      arrive(&sm.pz);
+      products(2, &sm.pz, par, [&]() {
+        const uint32_t kd = desc_lo(smem_u32(st.kq), BLOCK);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ts(tmem + TM_S, tmem + TM_Z + k * 8, kd + (k & 3) * (2048 >> 4), id_kd, 1);
+        tc_commit(&sm.s);
+        tc_commit(&sm.empty[n & 1]);
+      });
+#pragma unroll
+      for (int i = 0; i < SC; i += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) halves(b[i + 2 * e], b[i + 2 * e + 1], hi[e], lo[e]);
         if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < C; i += 32) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) halves(b[i + 2 * e] * up_b, b[i + 2 * e + 1] * up_b, hi[e], lo[e]);
-            tmem_st16(me + TM_S + i / 2, hi);
-            tmem_st16(me + TM_S + 32 + i / 2, lo);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        slow = any(!finite(top));
-        if (!slow) {
-          if (warp == 0) {
-            if (elect_one() && ok) {
-              tc_fence_after();
-              constexpr uint32_t id = idesc_16<__half>(128, C, false);
-              const uint32_t th = desc_lo(smem_u32(st.th), 16), tl = desc_lo(smem_u32(st.tl), 16);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_ts(tmem + TM_XK, tmem + TM_S + k * 8, th + k * 2, id, k != 0);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_ts(tmem + TM_XK, tmem + TM_S + 32 + k * 8, th + k * 2, id, 1);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_ts(tmem + TM_XK, tmem + TM_S + k * 8, tl + k * 2, id, 1);
-              tc_commit(&sm.u);
-            }
-            __syncwarp();
-          }
-          // meanwhile the outputs' first part, to the updates' scale
-          if (ok) {
-            const float f = up_b * back_s;
-#pragma unroll
-            for (int part = 0; part < 4; ++part) {
-              uint32_t x[16];
-              tmem_ld16(xq + part * 16, x);
-              tmem_wait_ld();
-              tie16(x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f * st.c.ec[part * 16 + i]);
-              tmem_st16(xq + part * 16, x);
-            }
-          }
-          // the updates
-          wait(&sm.u, n_u & 1u);
-          ++n_u;
-          if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t x[32];
-              tmem_ld32(me + TM_XK + part * 32, x);
-              tmem_wait_ld();
-              tie32(x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) b[part * 32 + i] = __uint_as_float(x[i]);
-            }
-            top = 0.f;
-#pragma unroll
-            for (int i = 0; i < C; i += 2) top = max_nan(top, b[i], b[i + 1]);
-#pragma unroll
-            for (int i = 0; i < C; i += 32) {
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                halves(b[i + 2 * e] * st.c.until[i + 2 * e], b[i + 2 * e + 1] * st.c.until[i + 2 * e + 1], hi[e], lo[e]);
-              tmem_st16(me + TM_Z + i / 2, hi);
-              tmem_st16(me + TM_Z + 32 + i / 2, lo);
-            }
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          slow = any(!(top < 65504.f));
-          if (!slow) {
-            if (warp == 0) {
-              if (elect_one() && ok) {
-                tc_fence_after();
-                constexpr uint32_t id = idesc_16<__half>(128, 128, true);
-                const uint32_t kd = desc_lo(smem_u32(st.kq), BLOCK);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_ts(tmem + TM_S, tmem + TM_Z + (k >> 2) * 32 + (k & 3) * 8, kd + (k & 3) * (2048 >> 4), id, k != 0);
-                tc_commit(&sm.s);
-              }
-              __syncwarp();
-            }
-            if (ok) {
-#pragma unroll
-              for (int i = 0; i < C; i += 32) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) halves(b[i + 2 * e], b[i + 2 * e + 1], hi[e], lo[e]);
-                tmem_st16(me + TM_Y + i / 2, hi);
-                tmem_st16(me + TM_Y + 32 + i / 2, lo);
-              }
-              tmem_wait_st();
-            }
-            const float d = st.c.ec[C - 1];
-            tc_fence_before();
-            named_sync(1, 128);
-            if (warp == 0) {
-              if (elect_one() && ok) {
-                tc_fence_after();
-                constexpr uint32_t id = idesc_16<__half>(128, C, false);
-                const uint32_t ph = desc_lo(smem_u32(st.ph), 16), pl = desc_lo(smem_u32(st.pl), 16);
-                const uint32_t d = tmem + TM_XQ + (n & 1) * C;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(d, tmem + TM_Y + k * 8, ph + k * 2, id, 1);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(d, tmem + TM_Y + 32 + k * 8, ph + k * 2, id, 1);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(d, tmem + TM_Y + k * 8, pl + k * 2, id, 1);
-                tc_commit(&sm.o);
-                tc_commit(&sm.empty[n & 1]);  // all that reads this stage is done by then
-              }
-              __syncwarp();
-            }
-            ++n_o;
-            pending = true;
-            pending_xq = n & 1;
-            pending_n = n;
-            out_scale = back_b;
-            wait(&sm.s, n_s & 1u);
-            ++n_s;
-            if (ok) {
-              tc_fence_after();
-#pragma unroll
-              for (int part = 0; part < 4; ++part) {
-                uint32_t x[32];
-                tmem_ld32(me + TM_S + part * 32, x);
-                tmem_wait_ld();
-                tie32(x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[part * 32 + i] = fmaf(s[part * 32 + i], d, __uint_as_float(x[i]) * back_b);
-              }
-            }
-          }
+          tmem_st8(me + TM_H + (i0 + i) / 2, hi);
+          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
         }
       }
-      if (slow) {
-        // row by row from the inputs, as delta_rows.cu does it
-        put_outputs();
-        const int rows = min(C, nn - n * C);
+      const bool slow_prep = *(volatile int *)&sm.bad[n & 1] != 0;
+      arrive(&sm.py);
+      products(3, &sm.py, par, [&]() {
+        const uint32_t ph = desc_lo(smem_u32(st.ph), 16), pl = desc_lo(smem_u32(st.pl), 16), d = tmem + TM_XQ + (n & 1) * C;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ts(d, tmem + TM_H + k * 8, ph + (k & 3) * 2, id, 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_ts(d, tmem + TM_H + k * 8, pl + k * 2, id, 1);
+        tc_commit(&sm.o);
+        tc_commit(&sm.empty[n & 1]);  // with the state's step the last to read this stage
+      });
+      wait_warp(&sm.s, par);
+      if (slow_prep || *(volatile int *)&sm.chain_bad == n + 1) {
+        wait_warp(&sm.o, par);  // its outputs are not wanted, and no product runs on
+        slow = true;
+        break;
+      }
+      pending = n;
+      out_scale = back_b;
+    }
+    if (slow) {
+      // The prep goes through the rest of its loop without waiting or touching
+      // anything.  All rows again, from the inputs and the state, which is not written
+      // before the end; as delta_rows.cu does it, the column's two threads exchanging
+      // their sums.
+      *abort_flag = 1;
+      float s[SD];
+      const float *from = p.s + (((int64_t)q.src * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+#pragma unroll
+      for (int d = 0; d < SD; ++d) s[d] = q.src >= 0 && have && d0 + d < p.Dk ? from[(int64_t)d * p.Dv] : 0.f;
 #pragma unroll 1
-        for (int i = 0; i < rows; ++i) {
-          const int64_t tok = tok0 + n * C + i;
-          const uint4 *kr = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride + hk * p.Dk);
-          const uint4 *qr = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + hk * p.Dk);
-          float fk = 1.f, fq = 1.f, x[8], y[8];
-          if (p.normalize) {
-            float a = 0.f, b = 0.f;
+      for (int i = 0; i < nn; ++i) {
+        const int64_t tok = tok0 + i;
+        const uint4 *kr = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride + hk * p.Dk);
+        const uint4 *qr = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + hk * p.Dk);
+        float fk = 1.f, fq = 1.f, x[8], y[8];
+        float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < p.Dk / 8; ++c) {
-              unpack8<T>(__ldg(kr + c), x);
-              unpack8<T>(__ldg(qr + c), y);
+        for (int c = 0; c < p.Dk / 8; ++c) {
+          unpack8<T>(__ldg(kr + c), x);
+          unpack8<T>(__ldg(qr + c), y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                a = fmaf(x[e], x[e], a);
-                b = fmaf(y[e], y[e], b);
-              }
-            }
-            fk = rsqrtf(a + p.eps);
-            fq = rsqrtf(b + p.eps);
+          for (int e = 0; e < 8; ++e) {
+            kk = fmaf(x[e], x[e], kk);
+            qq = fmaf(y[e], y[e], qq);
           }
-          float ks = 0.f, qs = 0.f, kq = 0.f;
-#pragma unroll
-          for (int c = 0; c < MAX_DK / 8; ++c)
-            if (c * 8 < p.Dk) {
-              unpack8<T>(__ldg(kr + c), x);
-              unpack8<T>(__ldg(qr + c), y);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float k = x[e] * fk, qq = y[e] * fq;
-                ks = fmaf(k, s[c * 8 + e], ks);
-                qs = fmaf(qq, s[c * 8 + e], qs);
-                kq = fmaf(k, qq, kq);
-              }
-            }
-          const float d = expf(__ldg(p.g + tok * p.Hv + h)), beta = __ldg(p.beta + tok * p.Hv + h);
-          const float v = have ? to_float<T>(p.v[tok * p.v_stride + h * p.Dv + col]) : 0.f;
-          const float u = beta * fmaf(-d, ks, v);
-#pragma unroll
-          for (int c = 0; c < MAX_DK / 8; ++c)
-            if (c * 8 < p.Dk) {
-              unpack8<T>(__ldg(kr + c), x);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) s[c * 8 + e] = fmaf(x[e] * fk, u, d * s[c * 8 + e]);
-            }
-          if (have) out[(n * C + i) * out_row] = (uint16_t)pack2<T>(p.scale * fmaf(kq, u, d * qs), 0.f);
         }
-        named_sync(1, 128);  // all have read the stage
-        if (warp == 0) {
-          if (elect_one() && ok) tc_commit(&sm.empty[n & 1]);
-          __syncwarp();
+        if (p.normalize) {
+          fk = rsqrtf(kk + p.eps);
+          fq = rsqrtf(qq + p.eps);
+        }
+#pragma unroll 1
+        for (int c = 0; c < p.Dk / 8; ++c) {
+          unpack8<T>(__ldg(kr + c), x);
+          unpack8<T>(__ldg(qr + c), y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) kq = fmaf(x[e] * fk, y[e] * fq, kq);
+        }
+        float ks = 0.f, qs = 0.f;
+#pragma unroll
+        for (int c = 0; c < SD / 8; ++c)
+          if (d0 + c * 8 < p.Dk) {
+            unpack8<T>(__ldg(kr + d0 / 8 + c), x);
+            unpack8<T>(__ldg(qr + d0 / 8 + c), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              ks = fmaf(x[e] * fk, s[c * 8 + e], ks);
+              qs = fmaf(y[e] * fq, s[c * 8 + e], qs);
+            }
+          }
+        sm.top[0][half][l] = ks;
+        sm.top[1][half][l] = qs;
+        named_sync(5 + (warp & 3), 64);
+        ks = sm.top[0][0][l] + sm.top[0][1][l];
+        qs = sm.top[1][0][l] + sm.top[1][1][l];
+        named_sync(5 + (warp & 3), 64);
+        const float decay = expf(__ldg(p.g + tok * p.Hv + h)), beta = __ldg(p.beta + tok * p.Hv + h);
+        const float v = have ? to_float<T>(p.v[tok * p.v_stride + h * p.Dv + col]) : 0.f;
+        const float u = beta * fmaf(-decay, ks, v);
+#pragma unroll
+        for (int c = 0; c < SD / 8; ++c)
+          if (d0 + c * 8 < p.Dk) {
+            unpack8<T>(__ldg(kr + d0 / 8 + c), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[c * 8 + e] = fmaf(x[e] * fk, u, decay * s[c * 8 + e]);
+          }
+        if (have && half == 0)
+          p.out[(tok * p.Hv + h) * p.Dv + col] = (uint16_t)pack2<T>(p.scale * fmaf(kq, u, decay * qs), 0.f);
+      }
+      if (ok && q.dst >= 0 && have) {
+        float *to = p.s + (((int64_t)q.dst * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+#pragma unroll
+        for (int d = 0; d < SD; ++d)
+          if (d0 + d < p.Dk) to[(int64_t)d * p.Dv] = s[d];
+      }
+    } else {
+      put_outputs();
+      if (ok && q.ok && q.dst >= 0) {
+        float *to = p.s + (((int64_t)q.dst * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+        tc_fence_after();
+#pragma unroll 1
+        for (int d = 0; d < SD; d += 16) {
+          uint32_t x[16];
+          tmem_ld16(me + TM_S + d0 + d, x);
+          tmem_wait_ld();
+          tie16(x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (have && d0 + d + e < p.Dk) to[(int64_t)(d + e) * p.Dv] = __uint_as_float(x[e]) * back;
         }
       }
     }
-    put_outputs();
-    if (ok && q.ok && q.dst >= 0 && have) {
-      float *to = p.s + ((int64_t)q.dst * p.Hv + h) * p.Dk * p.Dv + col;
-#pragma unroll
-      for (int d = 0; d < MAX_DK; ++d)
-        if (d < p.Dk) to[(int64_t)d * p.Dv] = s[d];
+  }
+  // no product runs on when tensor memory is given back
+  if (warp < 4 || warp == CHAIN / 32) {
+    if (elect_one()) {
+      tc_commit(&sm.drain);
+      int never = 0;
+      mbar_wait(&sm.drain, 0, &never);
     }
-    if (warp == 0) {  // no product runs on when tensor memory is given back
-      if (elect_one()) {
-        tc_commit(&sm.drain);
-        int never = 0;
-        mbar_wait(&sm.drain, 0, &never);
-      }
-      __syncwarp();
-    }
+    __syncwarp();
   }
   tc_fence_before();
   block_sync();
