@@ -18,9 +18,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmfd.so")
 LIB_CHECKED = os.path.join(BUILD, "libmfd_checked.so")
 SOURCES = ["lmhead.cu", "topk.cu", "tree.cu", "verify.cu", "analytics.cu", "kvcache.cu", "attention.cu",
-           "delta_rows.cu", "delta_chunk.cu", "norms.cu", "mfd_api.cu"]
+           "delta_rows.cu", "delta_chunk.cu", "delta_tree.cu", "norms.cu", "mfd_api.cu"]
 CHECKED_SOURCES = ["tree.cu"]  # the sources with bounds checks under -DMFD_CHECKED
-HEADERS = ["lmhead.h", "kvcache.h", "join_note.h", "delta.h", "tc16.cuh", "mfd_device.cuh"]
+HEADERS = ["lmhead.h", "kvcache.h", "join_note.h", "delta.h", "tc16.cuh", "delta_tc.cuh", "mfd_device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

@@ -394,33 +394,6 @@ struct Segment {
 // so that either every role gets an entry or none does.
 constexpr unsigned long long SEG_LIMIT_NS = 4 * kWaitLimitNs;
 
-// A waiting warp is put to sleep for up to a microsecond at a time: a dozen
-// waiting warps that poll take the issue slots of those that work.
-__device__ __forceinline__ bool try_wait_sleep(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
-      : "memory");
-  return ok != 0;
-}
-// Waits for the phase with `parity`; false when the limit passes or *abort is
-// set.  Out of line, like all that is not taken for every tile: the roles' hot
-// code shares an instruction cache that is small for it.
-__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, volatile int *abort) {
-  const unsigned long long t0 = globaltimer();
-  for (;;) {
-    if (try_wait_sleep(bar, parity)) return true;
-    if (*abort || globaltimer() - t0 > limit_ns) return false;
-  }
-}
-__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
-                                           volatile int *abort) {
-  return try_wait_sleep(bar, parity) || wait_long(bar, parity, limit_ns, abort);
-}
 // A pipeline wait that ran out, or was told to stop.
 __device__ __noinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
   if (wait_long(bar, parity, kWaitLimitNs, abort_flag)) return true;

@@ -1,6 +1,6 @@
 // delta.h -- the recurrent layers' calls as kernels see them: the gated delta
 // rule over rows, trees and accepted paths (delta_rows.cu,
-// delta_chunk.cu), and the norms with
+// delta_chunk.cu, delta_tree.cu), and the norms with
 // gates (norms.cu).
 #pragma once
 
@@ -38,7 +38,7 @@ constexpr int DELTA_CHUNK_FROM = 24;
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaArgs &A, cudaStream_t stream);
 cudaError_t launch_delta_commit(const DeltaArgs &A, int n_sm, cudaStream_t stream);
-cudaError_t launch_delta_tree(const DeltaArgs &A, int n_sm, cudaStream_t stream);
+cudaError_t launch_delta_tree(const DeltaArgs &A, cudaStream_t stream);
 
 struct GatedNormArgs {
   const uint16_t *x, *gate, *w;

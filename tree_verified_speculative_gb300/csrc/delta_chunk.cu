@@ -38,10 +38,7 @@
 // the inputs, in fp32, by the chain's threads.
 #include <atomic>
 
-#include "delta.h"
-#include "kvcache.h"
-#include "mfd_device.cuh"
-#include "tc16.cuh"
+#include "delta_tc.cuh"
 
 namespace mfd {
 namespace {
@@ -50,7 +47,6 @@ constexpr int C = 64;         // rows of a chunk
 constexpr int MAX_DK = 128;
 constexpr int LANES = 128;    // columns of a state in a block
 constexpr int CHAIN = 256, PREP = 256, THREADS = CHAIN + PREP;
-constexpr float LEAST_LOG = -1e5f;  // of a decay: e^-1e5 is 0 in fp32, and sums of it stay finite
 constexpr float MAX_HALF = 65504.f;
 
 constexpr int BLOCK = 128 * 128;           // 64 columns of the 128 rows of keys and queries
@@ -71,7 +67,7 @@ struct Smem {
   float At[C * PAD], T[C * PAD];           // A transposed; the inverse
   uint16_t out[C * LANES];
   float n2[2 * C];                         // squared lengths
-  float2 cc[C];                            // sums of log2 decays as two floats each
+  alignas(16) float2 cc[C];                // sums of log2 decays as two floats each
   float g[C], beta[C];
   float fq[3][C];                          // outputs' factors, which are used a chunk later than the rest
   float top[2][2][LANES];                  // [state, right sides][half][column]
@@ -90,27 +86,6 @@ constexpr int TM_XK = 256;   // S^T K^T; the updates
 constexpr int TM_XQ = 320;   // S^T Q^T, then outputs; two in turn
 constexpr int TM_G = 448;    // [K; Q] K^T
 
-__device__ __forceinline__ float max_nan(float a, float b, float c) {  // largest magnitude; NaN if there is one
-  float y;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
-  return y;
-}
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
-// 2^n and its inverse so that m * 2^n has exponent `to`: from m's bits, both normal.
-__device__ __forceinline__ float power_for(float m, int to, float &inverse) {
-  int b = 254 + to - (int)(__float_as_uint(m) >> 23);
-  b = max(1, min(253, b));
-  inverse = __uint_as_float((uint32_t)(254 - b) << 23);
-  return __uint_as_float((uint32_t)b << 23);
-}
-// Two numbers as halves: hi + lo.
-__device__ __forceinline__ void halves(float a, float b, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-  hi = *reinterpret_cast<const uint32_t *>(&h);
-  lo = *reinterpret_cast<const uint32_t *>(&l);
-}
 // The same of x times a power of two that brings the column's largest to [2^11,
 // 2^12): hi is x to the nearest even number, 11 bits at most, lo what is left, to
 // 2^-12 of 1.  The two roundings by 1.5 * 2^24 cost no conversions back.
@@ -122,43 +97,6 @@ __device__ __forceinline__ void halves_at(uint64_t x, uint64_t up, uint32_t &hi,
   hi = *reinterpret_cast<const uint32_t *>(&hh);
   lo = *reinterpret_cast<const uint32_t *>(&ll);
 }
-// A number as the sum of two floats.
-struct Two {
-  float hi, lo;
-};
-constexpr float LOG2E_HI = 0x1.715476p+0f, LOG2E_LO = 0x1.4ae0cp-26f;  // log2 e
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x))};
-}
-__device__ __forceinline__ Two two_sum(Two a, Two b) {
-  const Two s = two_sum(a.hi, b.hi);
-  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
-  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
-}
-__device__ __forceinline__ Two two_product(float a, float hi, float lo) {
-  const float p = __fmul_rn(a, hi);
-  return {p, __fmaf_rn(a, lo, __fmaf_rn(a, hi, -p))};
-}
-template <typename T>
-__device__ __forceinline__ float to_float(uint16_t x) { return unpack2<T>(x).x; }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-
-// Lengths and slots of request r.
-struct Request {
-  int nn, src, dst;
-  bool ok;
-};
-__device__ __forceinline__ Request request(const DeltaArgs &p, int r) {
-  Request q;
-  q.nn = p.n_nodes ? __ldg(p.n_nodes + r) : p.N;
-  q.src = p.src ? __ldg(p.src + r) : r;
-  q.dst = p.dst ? __ldg(p.dst + r) : q.src;
-  q.ok = q.nn >= 0 && q.nn <= p.N && q.src >= -1 && q.src < p.n_slots && q.dst >= -1 && q.dst < p.n_slots;
-  return q;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs p, int slices) {
   extern __shared__ uint8_t raw_smem[];
@@ -245,17 +183,26 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         sm.beta[t] = braw;
         if (!finite(braw) || !(graw < INFINITY)) bad = true;
       }
+      float ss[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[8];
+        unpack8<T>(raw[i], x);
+        ss[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss[i] = fmaf(x[e], x[e], ss[i]);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int row = i * 16 + r16;
-        float x[8], ss = 0.f;
+        float x[8];
         unpack8<T>(raw[i], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!finite(ss)) bad = true;
-        const int half_e = ((int)(__float_as_uint(ss) >> 23) - 127) >> 1;  // floor(log2 of the length)
+        if (!finite(ss[i])) bad = true;
+        const int half_e = ((int)(__float_as_uint(ss[i]) >> 23) - 127) >> 1;  // floor(log2 of the length)
         const float f = __uint_as_float((uint32_t)(127 - half_e) << 23);
         __half2 y[4];
 #pragma unroll
@@ -263,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (ok) {
           *reinterpret_cast<uint4 *>(st.kq + (c8 >> 3) * BLOCK + row * 128 + (((c8 & 7) ^ (row & 7)) << 4)) =
               *reinterpret_cast<const uint4 *>(y);
-          if (c8 == 0) sm.n2[row] = ss;
+          if (c8 == 0) sm.n2[row] = ss[i];
         }
       }
       fence_async_smem();
@@ -316,9 +263,9 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       const int row = t & 63, j1 = (t >> 7) * 32;
       const bool is_q = (t & 127) >= C;
       const float2 ci = sm.cc[row];
-      const float ss = sm.n2[t & 127];
-      const int half_e = ((int)(__float_as_uint(ss) >> 23) - 127) >> 1;
-      const float left = (p.normalize ? rsqrtf(ss + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
+      const float len2 = sm.n2[t & 127];
+      const int half_e = ((int)(__float_as_uint(len2) >> 23) - 127) >> 1;
+      const float left = (p.normalize ? rsqrtf(len2 + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
       const float br = sm.beta[row] * left, brr = br * left;
       if (t < C) {
         const float2 end = sm.cc[C - 1];
@@ -339,34 +286,30 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tie32(x);
         tc_fence_before();
         const float f = is_q ? 1.f : brr;
+        const int last = is_q ? row : row - 1;
 #pragma unroll
-        for (int k8 = 0; k8 < 4; ++k8) {
-          const int j0 = j1 + k8 * 8;
-          float y[8];
+        for (int e = 0; e < 32; e += 2) {
+          const float4 cj = *reinterpret_cast<const float4 *>(&sm.cc[j1 + e]);
+          const float z0 = __uint_as_float(x[e]) * (f * ex2((ci.x - cj.x) + (ci.y - cj.y)));
+          const float z1 = __uint_as_float(x[e + 1]) * (f * ex2((ci.x - cj.z) + (ci.y - cj.w)));
+          x[e] = j1 + e <= last ? __float_as_uint(z0) : 0u;
+          x[e + 1] = j1 + e + 1 <= last ? __float_as_uint(z1) : 0u;
+          most = max_nan(most, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        }
+        if (is_q) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = j0 + e;
-            const float2 cj = sm.cc[j];
-            const float z = __uint_as_float(x[k8 * 8 + e]) * (f * ex2((ci.x - cj.x) + (ci.y - cj.y)));
-            y[e] = j < row || (is_q && j == row) ? z : 0.f;
+          for (int k8 = 0; k8 < 4; ++k8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              halves(__uint_as_float(x[k8 * 8 + 2 * e]), __uint_as_float(x[k8 * 8 + 2 * e + 1]), hi[e], lo[e]);
+            const int at = row * 128 + ((((j1 >> 3) + k8) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4 *>(st.ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(st.pl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          most = max_nan(most, y[0], y[1]);
-          most = max_nan(most, y[2], y[3]);
-          most = max_nan(most, y[4], y[5]);
-          most = max_nan(most, y[6], y[7]);
-          if (is_q) {
-            uint4 hi, lo;
-            halves(y[0], y[1], hi.x, lo.x);
-            halves(y[2], y[3], hi.y, lo.y);
-            halves(y[4], y[5], hi.z, lo.z);
-            halves(y[6], y[7], hi.w, lo.w);
-            const int at = row * 128 + (((j0 >> 3) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(st.ph + at) = hi;
-            *reinterpret_cast<uint4 *>(st.pl + at) = lo;
-          } else {
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sm.At[(j0 + e) * PAD + row] = y[e];
-          }
+          for (int e = 0; e < 32; ++e) sm.At[(j1 + e) * PAD + row] = __uint_as_float(x[e]);
         }
       }
       named_sync(2, PREP);
@@ -521,20 +464,22 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tmem_wait_ld();
         tie32(x);
         tc_fence_before();
+        // all that is read before all that is written: a load does not pass a store
 #pragma unroll
-        for (int i = 0; i < SC; ++i)
-          sm.out[(i0 + i) * LANES + l] = (uint16_t)pack2<T>(__uint_as_float(x[i]) * out_scale * fq[i0 + i], 0.f);
+        for (int i = 0; i < SC; ++i) x[i] = pack2<T>(__uint_as_float(x[i]) * out_scale * fq[i0 + i], 0.f);
+#pragma unroll
+        for (int i = 0; i < SC; ++i) sm.out[(i0 + i) * LANES + l] = (uint16_t)x[i];
       }
       named_sync(3 + half, 128);
       const int rows = nn - pending * C, ch = l & 15;
       if (ok && slice * LANES + ch * 8 < p.Dv) {
+        uint4 y[SC / 8];
 #pragma unroll
-        for (int k = 0; k < SC / 8; ++k) {
-          const int i = i0 + k * 8 + (l >> 4);
-          if (i < rows)
-            st_global16(p.out + ((tok0 + pending * C + i) * p.Hv + h) * p.Dv + slice * LANES + ch * 8,
-                        *reinterpret_cast<const uint4 *>(&sm.out[i * LANES + ch * 8]));
-        }
+        for (int k = 0; k < SC / 8; ++k) y[k] = *reinterpret_cast<const uint4 *>(&sm.out[(i0 + k * 8 + (l >> 4)) * LANES + ch * 8]);
+        uint16_t *to = p.out + ((tok0 + pending * C + i0 + (l >> 4)) * p.Hv + h) * p.Dv + slice * LANES + ch * 8;
+#pragma unroll
+        for (int k = 0; k < SC / 8; ++k)
+          if (i0 + k * 8 + (l >> 4) < rows) st_global16(to + (int64_t)k * 8 * p.Hv * p.Dv, y[k]);
       }
       pending = -1;
     };
@@ -592,16 +537,16 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       if (ok) {
         const uint64_t up2 = pair(up, up);
 #pragma unroll 1
-        for (int d = 0; d < SD; d += 16) {
-          uint32_t x[16], hi[8], lo[8];
-          tmem_ld16(me + TM_S + d0 + d, x);
+        for (int d = 0; d < SD; d += 32) {
+          uint32_t x[32], hi[16], lo[16];
+          tmem_ld32(me + TM_S + d0 + d, x);
           tmem_wait_ld();
-          tie16(x);
+          tie32(x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 16; ++e)
             halves_at(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), up2, hi[e], lo[e]);
-          tmem_st8(me + TM_H + (d0 + d) / 2, hi);
-          tmem_st8(me + TM_H + 64 + (d0 + d) / 2, lo);
+          tmem_st16(me + TM_H + (d0 + d) / 2, hi);
+          tmem_st16(me + TM_H + 64 + (d0 + d) / 2, lo);
         }
       }
       const float back_s = down * back;  // of S^T K^T to true numbers
@@ -625,19 +570,20 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       wait_warp(&sm.x, par);
       tc_fence_after();
       float b[SC];
+      {
+        uint32_t x[SC];
 #pragma unroll
-      for (int part = 0; part < SC; part += 16) {
-        uint32_t x[16];
+        for (int i = 0; i < SC; ++i) x[i] = 0u;
         if (ok) {
-          tmem_ld16(me + TM_XK + i0 + part, x);
+          tmem_ld32(me + TM_XK + i0, x);
           tmem_wait_ld();
-          tie16(x);
+          tie32(x);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = st.c.rhs[i0 + part + i];
-          const float v = to_float<T>(st.v[(i0 + part + i) * LANES + l]);
-          b[part + i] = ok ? fmaf(f.y, __uint_as_float(x[i]) * back_s, f.x * v) : 0.f;
+        for (int i = 0; i < SC; ++i) {
+          const float2 f = st.c.rhs[i0 + i];
+          const float v = to_float<T>(st.v[(i0 + i) * LANES + l]);
+          b[i] = fmaf(f.y, __uint_as_float(x[i]) * back_s, f.x * v);
         }
       }
       top = 0.f;
@@ -655,15 +601,12 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       tc_fence_after();
       {
         const uint64_t up = pair(up_b, up_b);
+        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < SC; i += 16) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) halves_at(pair(b[i + 2 * e], b[i + 2 * e + 1]), up, hi[e], lo[e]);
-          if (ok) {
-            tmem_st8(me + TM_H + (i0 + i) / 2, hi);
-            tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
-          }
+        for (int e = 0; e < 16; ++e) halves_at(pair(b[2 * e], b[2 * e + 1]), up, hi[e], lo[e]);
+        if (ok) {
+          tmem_st16(me + TM_H + i0 / 2, hi);
+          tmem_st16(me + TM_H + 32 + i0 / 2, lo);
         }
       }
       arrive(&sm.pb);
@@ -693,14 +636,15 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       if (ok) {
         const float f = st.c.ec[C - 1] * (up_b * back);
 #pragma unroll 1
-        for (int d = 0; d < SD; d += 16) {
-          uint32_t x[16];
-          tmem_ld16(me + TM_S + d0 + d, x);
+        for (int d = 0; d < SD; d += 32) {
+          uint32_t x[32];
+          tmem_ld32(me + TM_S + d0 + d, x);
           tmem_wait_ld();
-          tie16(x);
+          tie32(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
           tmem_st16(me + TM_S + d0 + d, x);
+          tmem_st16(me + TM_S + d0 + d + 16, x + 16);
         }
       }
       back = back_b;
@@ -716,20 +660,19 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         for (int i = 0; i < SC; ++i) b[i] = __uint_as_float(x[i]) * 0.125f;
       }
       float most = 0.f;
+      {
+        uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < SC; i += 16) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + i + 2 * e]);
-          const float z0 = b[i + 2 * e] * f.x, z1 = b[i + 2 * e + 1] * f.y;
+        for (int e = 0; e < 16; ++e) {
+          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + 2 * e]);
+          const float z0 = b[2 * e] * f.x, z1 = b[2 * e + 1] * f.y;
           most = max_nan(most, z0, z1);
-          most = max_nan(most, b[i + 2 * e], b[i + 2 * e + 1]);
+          most = max_nan(most, b[2 * e], b[2 * e + 1]);
           halves(z0, z1, hi[e], lo[e]);
         }
         if (ok) {
-          tmem_st8(me + TM_Z + (i0 + i) / 2, hi);
-          tmem_st8(me + TM_Z + 32 + (i0 + i) / 2, lo);
+          tmem_st16(me + TM_Z + i0 / 2, hi);
+          tmem_st16(me + TM_Z + 32 + i0 / 2, lo);
         }
       }
       if (bad || (was_finite && !(most < MAX_HALF))) *(volatile int *)&sm.chain_bad = n + 1;
@@ -741,14 +684,13 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tc_commit(&sm.s);
         tc_commit(&sm.empty[n & 1]);
       });
+      {
+        uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < SC; i += 16) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) halves(b[i + 2 * e], b[i + 2 * e + 1], hi[e], lo[e]);
+        for (int e = 0; e < 16; ++e) halves(b[2 * e], b[2 * e + 1], hi[e], lo[e]);
         if (ok) {
-          tmem_st8(me + TM_H + (i0 + i) / 2, hi);
-          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
+          tmem_st16(me + TM_H + i0 / 2, hi);
+          tmem_st16(me + TM_H + 32 + i0 / 2, lo);
         }
       }
       const bool slow_prep = *(volatile int *)&sm.bad[n & 1] != 0;

@@ -1,5 +1,6 @@
-// delta_rows.cu -- the gated delta rule row after row (the target's recurrent
-// layers; the method's pages name hybrid targets and tree kernels for them).
+// delta_rows.cu -- the gated delta rule row after row: few rows, and accepted paths
+// (the target's recurrent layers; the method's pages name hybrid targets: model
+// card "MFD drafter for Qwen3.5-4B").
 //
 //   S' = e^g S,  u = beta (v - S'^T k),  S = S' + k u^T,  o = scale S^T q
 //
@@ -22,7 +23,7 @@ constexpr int THREADS = 256;
 constexpr int BATCH = 16;    // rows whose vectors are in shared memory at once
 constexpr int MAX_DK = 128;
 
-enum { RULE = 0, COMMIT = 1, TREE = 2 };
+enum { RULE = 0, COMMIT = 1 };
 
 __device__ __forceinline__ float4 fma4(float a, float4 b, float4 c) {
   return make_float4(fmaf(a, b.x, c.x), fmaf(a, b.y, c.y), fmaf(a, b.z, c.z), fmaf(a, b.w, c.w));
@@ -38,9 +39,9 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
   constexpr int LW = W / 4, RG = THREADS / LW;      // lanes of a row, groups
   constexpr int PER = MAX_DK / RG;                  // rows of the state a thread holds
   constexpr int WARPS = THREADS / 32;
-  __shared__ float k_s[BATCH + 1][MAX_DK], q_s[BATCH + 1][MAX_DK];
-  __shared__ float4 v_s[BATCH + 1][LW];
-  __shared__ float decay_s[BATCH + 1], beta_s[BATCH + 1], qk_s[BATCH + 1];
+  __shared__ float k_s[BATCH][MAX_DK], q_s[BATCH][MAX_DK];
+  __shared__ float4 v_s[BATCH][LW];
+  __shared__ float decay_s[BATCH], beta_s[BATCH], qk_s[BATCH];
   __shared__ float4 sum_s[2][2][WARPS][LW];  // [row mod 2][keys, queries][warp][lane]
   __shared__ int row_s[DELTA_MAX_DEPTH + 1], bad_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
   // lengths and slots; a request whose numbers are wrong has no rows and keeps no state
   int nn = p.n_nodes ? __ldg(p.n_nodes + r) : p.N;
   const int src = p.src ? __ldg(p.src + r) : r;
-  const int dst = MODE == TREE ? -1 : p.dst ? __ldg(p.dst + r) : src;
+  const int dst = p.dst ? __ldg(p.dst + r) : src;
   bool ok = nn >= 0 && nn <= p.N && src >= -1 && src < p.n_slots && dst >= -1 && dst < p.n_slots;
   const int64_t tok0 = (int64_t)r * p.N;
   if (tid == 0) bad_s = 0;
@@ -71,12 +72,6 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
       row_s[tid] = node;
     }
   }
-  if (MODE == TREE && ok)
-    for (int i = tid; i < nn; i += THREADS) {
-      const int32_t *parent = p.parent + tok0;
-      const int up = __ldg(parent + i);
-      if (i == 0 ? up != -1 : (up < 0 || up >= i)) bad_s = 1;
-    }
   block_sync();
   if (bad_s) ok = false;
   if (!ok) {
@@ -91,14 +86,12 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
   if (!ok) return;
 
   float4 S[PER];
-  auto load_state = [&]() {
-    const float *from = p.s + ((int64_t)src * p.Hv + h) * p.Dk * p.Dv + col;
+  const float *from = p.s + ((int64_t)src * p.Hv + h) * p.Dk * p.Dv + col;
 #pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      const int row = rg + RG * t;
-      S[t] = src >= 0 && have && row < p.Dk ? *reinterpret_cast<const float4 *>(from + (int64_t)row * p.Dv) : make_float4(0, 0, 0, 0);
-    }
-  };
+  for (int t = 0; t < PER; ++t) {
+    const int row = rg + RG * t;
+    S[t] = src >= 0 && have && row < p.Dk ? *reinterpret_cast<const float4 *>(from + (int64_t)row * p.Dv) : make_float4(0, 0, 0, 0);
+  }
   // vectors of rows at(first) .. at(first + n - 1): half a warp for a key, half for a query
   auto load_rows = [&](int first, int n, auto at) {
     for (int i = warp; i < n; i += WARPS) {
@@ -185,29 +178,6 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
   };
   auto out_of = [&](int i) { return p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col; };
 
-  if (MODE == TREE) {
-    for (int i = 0; i < nn; ++i) {
-      if (tid == 0) {  // the node's path, itself first
-        int n = 0, j = i;
-        for (; j >= 0 && n <= DELTA_MAX_DEPTH; j = __ldg(p.parent + tok0 + j)) row_s[n++] = j;
-        bad_s = j >= 0 ? -1 : n;
-      }
-      block_sync();
-      const int n = bad_s;
-      if (n < 0) {  // deeper than a tree may be
-        if (tid == 0) report(p.status, MFD_ERR_INPUT);
-        for (int j = rg; j < nn && have; j += RG) *reinterpret_cast<uint2 *>(out_of(j)) = make_uint2(0, 0);
-        return;
-      }
-      load_rows(0, n, [&](int j) { return row_s[n - 1 - j]; });
-      load_state();
-      block_sync();
-      for (int j = 0; j < n; ++j) step(j, j == n - 1 ? out_of(i) : nullptr);
-      block_sync();
-    }
-    return;
-  }
-  load_state();
   for (int first = 0; first < rows; first += BATCH) {
     const int n = min(BATCH, rows - first);
     if (first) block_sync();
@@ -258,6 +228,5 @@ cudaError_t launch_type(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
 
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream) { return launch_type<RULE>(A, n_sm, stream); }
 cudaError_t launch_delta_commit(const DeltaArgs &A, int n_sm, cudaStream_t stream) { return launch_type<COMMIT>(A, n_sm, stream); }
-cudaError_t launch_delta_tree(const DeltaArgs &A, int n_sm, cudaStream_t stream) { return launch_type<TREE>(A, n_sm, stream); }
 
 }  // namespace mfd

@@ -32,6 +32,33 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// A waiting warp is put to sleep for up to a microsecond at a time: a dozen
+// waiting warps that poll take the issue slots of those that work.
+__device__ __forceinline__ bool try_wait_sleep(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase with `parity`; false when the limit passes or *abort is
+// set.  Out of line, like all that is not taken for every tile: the roles' hot
+// code shares an instruction cache that is small for it.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, unsigned long long limit_ns, volatile int *abort) {
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (try_wait_sleep(bar, parity)) return true;
+    if (*abort || globaltimer() - t0 > limit_ns) return false;
+  }
+}
+__device__ __forceinline__ bool wait_limit(uint64_t *bar, uint32_t parity, unsigned long long limit_ns,
+                                           volatile int *abort) {
+  return try_wait_sleep(bar, parity) || wait_long(bar, parity, limit_ns, abort);
+}
 // One lane of the warp; the branch it guards runs in uniform registers, which
 // is where the MMA takes its operands from.
 __device__ __forceinline__ bool elect_one() {
