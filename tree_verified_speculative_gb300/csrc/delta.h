@@ -38,7 +38,7 @@ constexpr int DELTA_CHUNK_FROM = 24;
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaArgs &A, cudaStream_t stream);
 cudaError_t launch_delta_commit(const DeltaArgs &A, int n_sm, cudaStream_t stream);
-cudaError_t launch_delta_tree(const DeltaArgs &A, cudaStream_t stream);
+cudaError_t launch_delta_tree(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 
 struct GatedNormArgs {
   const uint16_t *x, *gate, *w;

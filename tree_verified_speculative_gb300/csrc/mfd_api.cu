@@ -1043,8 +1043,10 @@ int mfd_delta_tree(const void *q, int64_t q_stride, const void *k, int64_t k_str
   if (!parent || !aligned(parent, 4)) return MFD_ERR_INVALID_ARG;
   if (N > mfd::DELTA_MAX_NODES) return MFD_ERR_UNSUPPORTED;
   A.parent = parent;
-  if ((rc = need_sm103()) != MFD_OK) return rc;
-  return cuda_status(mfd::launch_delta_tree(A, reinterpret_cast<cudaStream_t>(stream)));
+  DeviceInfo d;
+  if ((rc = current_device_info(&d)) != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
+  return cuda_status(mfd::launch_delta_tree(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int mfd_delta_commit(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int dtype, int n_req, int N,
