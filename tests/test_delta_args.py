@@ -105,7 +105,7 @@ def _call(form, **kw):
     a = dict(q=torch.zeros((R, N, Hk, Dk), dtype=torch.bfloat16), k=torch.zeros((R, N, Hk, Dk), dtype=torch.bfloat16),
              v=torch.zeros((R, N, Hv, Dv), dtype=torch.bfloat16), g=torch.zeros((R, N, Hv)), beta=torch.zeros((R, N, Hv)),
              nodes=torch.zeros(R, dtype=torch.int32), out=torch.zeros((R, N, Hv, Dv), dtype=torch.bfloat16), src=None, dst=None,
-             state=SimpleNamespace(n_slots=2, Hv=Hv, Dk=Dk, Dv=Dv, _c=None, s=torch.zeros(1)), status=torch.zeros(1, dtype=torch.int32),
+             state=SimpleNamespace(n_slots=2, Hv=Hv, Dk=Dk, Dv=Dv, _c=None, device=0, s=torch.zeros(1)), status=torch.zeros(1, dtype=torch.int32),
              parent=torch.zeros((R, N), dtype=torch.int32), accept=torch.zeros(R, dtype=torch.int32),
              path=torch.zeros((R, 4), dtype=torch.int32))
     a.update(kw)
@@ -122,7 +122,7 @@ BAD = [(dict(k=torch.zeros((2, 3, 2, 64))), "bf16 or fp16"), (dict(v=torch.zeros
        (dict(g=torch.zeros((2, 3, 4), dtype=torch.float64)), "g and beta"), (dict(beta=torch.zeros((2, 3, 2))), "g and beta"),
        (dict(nodes=torch.zeros(2, dtype=torch.int64)), "n_nodes"), (dict(src=torch.zeros(1, dtype=torch.int32)), "n_nodes"),
        (dict(status=torch.zeros(1)), "status"),
-       (dict(state=SimpleNamespace(n_slots=1, Hv=4, Dk=64, Dv=32, _c=None, s=torch.zeros(1))), "slot for each")]
+       (dict(state=SimpleNamespace(n_slots=1, Hv=4, Dk=64, Dv=32, _c=None, device=0, s=torch.zeros(1))), "slot for each")]
 
 
 @pytest.mark.parametrize("form", ["rule", "tree", "commit"])

@@ -56,6 +56,6 @@ struct ResidualNormArgs {
   float scale, eps;
   uint16_t *residual_out, *x_out;
 };
-cudaError_t launch_residual_norm(const ResidualNormArgs &A, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormArgs &A, int n_sm, cudaStream_t stream);
 
 }  // namespace mfd

@@ -4,14 +4,16 @@
 //
 //   S' = e^g S,  u = beta (v - S'^T k),  S = S' + k u^T,  o = scale S^T q
 //
-// A block holds W columns of one head's state in registers, a thread a float4
-// of Dk / RG rows (RG groups of threads share the columns).  With both sums of
-// a row made from the state before it, kS = S^T k and qS = S^T q,
+// A warp has 16 columns of one head's state in registers: 4 lanes a float4 of
+// each, 8 groups of lanes Dk / 8 rows each.  With both sums of a row made from
+// the state before it, kS = S^T k and qS = S^T q,
 //
 //   u = beta (v - e^g kS),  o = scale (e^g qS + (q . k) u),
 //
-// one exchange between the groups serves a row, and a row's dot product q . k
-// does not wait for the state.
+// three exchanges between the groups serve a row, and warps do not wait for each
+// other: a block's warps share the rows' vectors, BATCH of them at a time.  (With
+// the groups in different warps and a barrier for each row, 32 accepted paths took
+// 48 us.)
 #include "delta.h"
 #include "kvcache.h"
 #include "mfd_device.cuh"
@@ -19,36 +21,40 @@
 namespace mfd {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int BATCH = 16;    // rows whose vectors are in shared memory at once
+constexpr int COLS = 16;     // of a warp
+constexpr int BATCH = 17;    // rows whose vectors are in shared memory at once: all of a path
 constexpr int MAX_DK = 128;
+constexpr int PER = MAX_DK / 8;  // rows of the state a lane holds
 
 enum { RULE = 0, COMMIT = 1 };
 
 __device__ __forceinline__ float4 fma4(float a, float4 b, float4 c) {
   return make_float4(fmaf(a, b.x, c.x), fmaf(a, b.y, c.y), fmaf(a, b.z, c.z), fmaf(a, b.w, c.w));
 }
-__device__ __forceinline__ float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
-__device__ __forceinline__ float4 shfl4(float4 v, int o) {
-  return make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
-                     __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
+// The sum over the eight groups of lanes.
+__device__ __forceinline__ float4 group_sum(float4 v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  return v;
 }
 
-template <typename T, int W, int MODE>
-__global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, int slices) {
-  constexpr int LW = W / 4, RG = THREADS / LW;      // lanes of a row, groups
-  constexpr int PER = MAX_DK / RG;                  // rows of the state a thread holds
-  constexpr int WARPS = THREADS / 32;
-  __shared__ float k_s[BATCH][MAX_DK], q_s[BATCH][MAX_DK];
-  __shared__ float4 v_s[BATCH][LW];
+template <typename T, int WARPS, int MODE>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(const DeltaArgs p, int slices) {
+  constexpr int W = WARPS * COLS;
+  __shared__ float4 k_s[BATCH][MAX_DK / 4], q_s[MODE == COMMIT ? 1 : BATCH][MAX_DK / 4];
+  __shared__ uint4 v_s[BATCH][W / 8];
   __shared__ float decay_s[BATCH], beta_s[BATCH], qk_s[BATCH];
-  __shared__ float4 sum_s[2][2][WARPS][LW];  // [row mod 2][keys, queries][warp][lane]
-  __shared__ int row_s[DELTA_MAX_DEPTH + 1], bad_s;
+  __shared__ int row_s[BATCH], bad_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.Hv, r = blockIdx.x / slices / p.Hv;
-  const int col = slice * W + (tid % LW) * 4, rg = tid / LW;
+  const int group = lane >> 2, col = slice * W + warp * COLS + (lane & 3) * 4;
   const bool have = col < p.Dv;
-  const int hk = h / (p.Hv / p.Hk);
+  const int hk = h / (p.Hv / p.Hk), per = p.Dk / 8;  // rows of a group: even
   pdl_launch_dependents();
   pdl_wait();
 
@@ -57,11 +63,18 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
   const int src = p.src ? __ldg(p.src + r) : r;
   const int dst = p.dst ? __ldg(p.dst + r) : src;
   bool ok = nn >= 0 && nn <= p.N && src >= -1 && src < p.n_slots && dst >= -1 && dst < p.n_slots;
+  float4 S[PER];
+  {
+    const float *from = p.s + (((int64_t)src * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
+#pragma unroll
+    for (int t = 0; t < PER; ++t)
+      S[t] = ok && src >= 0 && have && t < per ? *reinterpret_cast<const float4 *>(from + (int64_t)t * p.Dv) : make_float4(0, 0, 0, 0);
+  }
   const int64_t tok0 = (int64_t)r * p.N;
-  if (tid == 0) bad_s = 0;
-  block_sync();
   int rows = nn;
   if (MODE == COMMIT) {
+    if (tid == 0) bad_s = 0;
+    block_sync();
     rows = ok ? __ldg(p.accept_len + r) + 1 : 0;
     if (rows < 1 || rows > p.L + 1) ok = false;
     const int32_t *path = p.path + (int64_t)r * (p.L + 1);
@@ -71,40 +84,35 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
       if (!good) bad_s = 1;
       row_s[tid] = node;
     }
+    block_sync();
+    if (bad_s) ok = false;
   }
-  block_sync();
-  if (bad_s) ok = false;
   if (!ok) {
     if (tid == 0) report(p.status, MFD_ERR_INPUT);
-    rows = 0;
-    nn = 0;
+    rows = nn = 0;
   }
   // rows that are not live
-  if (MODE != COMMIT && have)
-    for (int i = nn + rg; i < p.N; i += RG)
+  if (MODE == RULE && have)
+    for (int i = nn + group; i < p.N; i += 8)
       *reinterpret_cast<uint2 *>(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col) = make_uint2(0, 0);
   if (!ok) return;
 
-  float4 S[PER];
-  const float *from = p.s + ((int64_t)src * p.Hv + h) * p.Dk * p.Dv + col;
-#pragma unroll
-  for (int t = 0; t < PER; ++t) {
-    const int row = rg + RG * t;
-    S[t] = src >= 0 && have && row < p.Dk ? *reinterpret_cast<const float4 *>(from + (int64_t)row * p.Dv) : make_float4(0, 0, 0, 0);
-  }
-  // vectors of rows at(first) .. at(first + n - 1): half a warp for a key, half for a query
-  auto load_rows = [&](int first, int n, auto at) {
+  for (int first = 0; first < rows; first += BATCH) {
+    const int n = min(BATCH, rows - first);
+    if (first) block_sync();
+    for (int i = tid; i < n * (W / 8); i += WARPS * 32) {
+      const int row = i / (W / 8), c = i % (W / 8), at = slice * W + c * 8;
+      const int64_t tok = tok0 + (MODE == COMMIT ? row_s[row] : first + row);
+      if (at < p.Dv) v_s[row][c] = __ldg(reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride + h * p.Dv + at));
+    }
+    // half a warp for a key, half for a query
     for (int i = warp; i < n; i += WARPS) {
-      const int64_t tok = tok0 + at(first + i);
+      const int64_t tok = tok0 + (MODE == COMMIT ? row_s[i] : first + i);
       const int c = lane & 15;
       const bool is_q = lane >= 16;
       uint4 raw = make_uint4(0, 0, 0, 0);
       if (c * 8 < p.Dk && (!is_q || MODE != COMMIT))
-        raw = *reinterpret_cast<const uint4 *>(is_q ? p.q + tok * p.q_stride + hk * p.Dk + c * 8
-                                                    : p.k + tok * p.k_stride + hk * p.Dk + c * 8);
-      uint2 vr = make_uint2(0, 0);
-      if (lane < LW && slice * W + lane * 4 < p.Dv)
-        vr = *reinterpret_cast<const uint2 *>(p.v + tok * p.v_stride + h * p.Dv + slice * W + lane * 4);
+        raw = __ldg(reinterpret_cast<const uint4 *>((is_q ? p.q + tok * p.q_stride : p.k + tok * p.k_stride) + hk * p.Dk + c * 8));
       const float g = __ldg(p.g + tok * p.Hv + h), b = __ldg(p.beta + tok * p.Hv + h);
       float x[8], ss = 0.f, qk = 0.f;
       unpack8<T>(raw, x);
@@ -117,16 +125,21 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= f;
       }
+      if (MODE != COMMIT) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qk = fmaf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16), qk);
+        for (int e = 0; e < 8; ++e) qk = fmaf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16), qk);
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
-      float *to = (is_q ? q_s[i] : k_s[i]) + c * 8;
-      *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
-      if (lane < LW) {
-        const float2 a = unpack2<T>(vr.x), d = unpack2<T>(vr.y);
-        v_s[i][lane] = make_float4(a.x, a.y, d.x, d.y);
+        for (int o = 1; o < 16; o <<= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
+      }
+      if (!is_q || MODE != COMMIT) {
+        // element e of the vector is element e % per of group e / per; rows of groups are
+        // PER floats apart in shared memory, whatever Dk is
+        float *to = reinterpret_cast<float *>(is_q ? q_s[i] : k_s[i]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const int at = c * 8 + e;
+          if (at < p.Dk) *reinterpret_cast<float2 *>(to + at / per * PER + at % per) = make_float2(x[e], x[e + 1]);
+        }
       }
       if (lane == 0) {
         decay_s[i] = expf(g);
@@ -134,70 +147,64 @@ __global__ void __launch_bounds__(THREADS) delta_rows_kernel(const DeltaArgs p, 
         qk_s[i] = qk;
       }
     }
-  };
-  uint32_t turn = 0;
-  // one row from shared memory; `out`: where this slice's columns of its output go, or NULL
-  auto step = [&](int i, uint16_t *out) {
-    float4 a = make_float4(0, 0, 0, 0), b = a;
-#pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      a = fma4(k_s[i][rg + RG * t], S[t], a);
-      if (MODE != COMMIT) b = fma4(q_s[i][rg + RG * t], S[t], b);
-    }
-#pragma unroll
-    for (int o = LW; o < 32; o <<= 1) {
-      a = add4(a, shfl4(a, o));
-      if (MODE != COMMIT) b = add4(b, shfl4(b, o));
-    }
-    float4(*sum)[WARPS][LW] = sum_s[turn & 1];
-    ++turn;
-    if (lane < LW) {
-      sum[0][warp][lane] = a;
-      if (MODE != COMMIT) sum[1][warp][lane] = b;
-    }
     block_sync();
-    a = b = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < n; ++i) {
+      const uint2 raw = reinterpret_cast<const uint2 *>(v_s[i])[warp * (COLS / 4) + (lane & 3)];
+      const float2 v0 = unpack2<T>(raw.x), v1 = unpack2<T>(raw.y);
+      const float4 v = make_float4(v0.x, v0.y, v1.x, v1.y);
+      float4 a = make_float4(0, 0, 0, 0), b = a;
+      const float4 *kv = k_s[i] + group * (PER / 4), *qv = q_s[MODE == COMMIT ? 0 : i] + group * (PER / 4);
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      a = add4(a, sum[0][w][tid % LW]);
-      if (MODE != COMMIT) b = add4(b, sum[1][w][tid % LW]);
-    }
-    const float d = decay_s[i], beta = beta_s[i], qk = qk_s[i];
-    const float4 v = v_s[i][tid % LW];
-    const float4 u = make_float4(beta * fmaf(-d, a.x, v.x), beta * fmaf(-d, a.y, v.y), beta * fmaf(-d, a.z, v.z),
-                                 beta * fmaf(-d, a.w, v.w));
+      for (int t = 0; t < PER; t += 4)
+        if (t < per) {
+          const float4 k = kv[t / 4];
+          a = fma4(k.x, S[t], a);
+          if (t + 1 < per) a = fma4(k.y, S[t + 1], a);
+          if (t + 2 < per) a = fma4(k.z, S[t + 2], a);
+          if (t + 3 < per) a = fma4(k.w, S[t + 3], a);
+          if (MODE != COMMIT) {
+            const float4 q = qv[t / 4];
+            b = fma4(q.x, S[t], b);
+            if (t + 1 < per) b = fma4(q.y, S[t + 1], b);
+            if (t + 2 < per) b = fma4(q.z, S[t + 2], b);
+            if (t + 3 < per) b = fma4(q.w, S[t + 3], b);
+          }
+        }
+      a = group_sum(a);
+      if (MODE != COMMIT) b = group_sum(b);
+      const float d = decay_s[i], beta = beta_s[i];
+      const float4 u = make_float4(beta * fmaf(-d, a.x, v.x), beta * fmaf(-d, a.y, v.y), beta * fmaf(-d, a.z, v.z),
+                                   beta * fmaf(-d, a.w, v.w));
 #pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      const float k = k_s[i][rg + RG * t];
-      S[t] = make_float4(fmaf(k, u.x, d * S[t].x), fmaf(k, u.y, d * S[t].y), fmaf(k, u.z, d * S[t].z), fmaf(k, u.w, d * S[t].w));
+      for (int t = 0; t < PER; t += 4)
+        if (t < per) {
+          const float4 k = kv[t / 4];
+          const float kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (t + e < per)
+              S[t + e] = make_float4(fmaf(kk[e], u.x, d * S[t + e].x), fmaf(kk[e], u.y, d * S[t + e].y), fmaf(kk[e], u.z, d * S[t + e].z),
+                                     fmaf(kk[e], u.w, d * S[t + e].w));
+        }
+      if (MODE != COMMIT && group == 0 && have) {
+        const float qk = qk_s[i];
+        *reinterpret_cast<uint2 *>(p.out + ((tok0 + first + i) * p.Hv + h) * p.Dv + col) =
+            make_uint2(pack2<T>(p.scale * fmaf(qk, u.x, d * b.x), p.scale * fmaf(qk, u.y, d * b.y)),
+                       pack2<T>(p.scale * fmaf(qk, u.z, d * b.z), p.scale * fmaf(qk, u.w, d * b.w)));
+      }
     }
-    if (out && rg == 0 && have)
-      *reinterpret_cast<uint2 *>(out) =
-          make_uint2(pack2<T>(p.scale * fmaf(qk, u.x, d * b.x), p.scale * fmaf(qk, u.y, d * b.y)),
-                     pack2<T>(p.scale * fmaf(qk, u.z, d * b.z), p.scale * fmaf(qk, u.w, d * b.w)));
-  };
-  auto out_of = [&](int i) { return p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col; };
-
-  for (int first = 0; first < rows; first += BATCH) {
-    const int n = min(BATCH, rows - first);
-    if (first) block_sync();
-    load_rows(first, n, [&](int j) { return MODE == COMMIT ? row_s[j] : j; });
-    block_sync();
-    for (int i = 0; i < n; ++i) step(i, MODE == COMMIT ? nullptr : out_of(first + i));
   }
   if (dst >= 0 && have) {
-    float *to = p.s + ((int64_t)dst * p.Hv + h) * p.Dk * p.Dv + col;
+    float *to = p.s + (((int64_t)dst * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
 #pragma unroll
-    for (int t = 0; t < PER; ++t) {
-      const int row = rg + RG * t;
-      if (row < p.Dk) *reinterpret_cast<float4 *>(to + (int64_t)row * p.Dv) = S[t];
-    }
+    for (int t = 0; t < PER; ++t)
+      if (t < per) *reinterpret_cast<float4 *>(to + (int64_t)t * p.Dv) = S[t];
   }
 }
 
-template <typename T, int W, int MODE>
+template <typename T, int WARPS, int MODE>
 cudaError_t launch_width(const DeltaArgs &A, cudaStream_t stream) {
-  const int slices = (A.Dv + W - 1) / W;
+  const int slices = (A.Dv + WARPS * COLS - 1) / (WARPS * COLS);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -205,9 +212,9 @@ cudaError_t launch_width(const DeltaArgs &A, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)((int64_t)A.n_req * A.Hv * slices));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_rows_kernel<T, W, MODE>, A, slices);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_rows_kernel<T, WARPS, MODE>, A, slices);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -215,9 +222,8 @@ template <typename T, int MODE>
 cudaError_t launch_mode(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
   // narrower slices where heads alone leave SMs without work
   const int64_t heads = (int64_t)A.n_req * A.Hv;
-  if (heads * ((A.Dv + 63) / 64) <= n_sm) return launch_width<T, 32, MODE>(A, stream);
-  if (heads * ((A.Dv + 127) / 128) <= n_sm) return launch_width<T, 64, MODE>(A, stream);
-  return launch_width<T, 128, MODE>(A, stream);
+  if (heads * ((A.Dv + 63) / 64) <= n_sm) return launch_width<T, 2, MODE>(A, stream);
+  return launch_width<T, 4, MODE>(A, stream);
 }
 template <int MODE>
 cudaError_t launch_type(const DeltaArgs &A, int n_sm, cudaStream_t stream) {

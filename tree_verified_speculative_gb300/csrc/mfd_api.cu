@@ -1106,8 +1106,10 @@ int mfd_residual_norm(const void *y, const void *residual, int dtype, int T, int
   if (gate && gate_stride != 0 && (gate_stride < H || gate_stride % 8 != 0 || gate_stride >= ((int64_t)1 << 40)))
     return MFD_ERR_INVALID_ARG;
   if (residual_out == x_out) return MFD_ERR_INVALID_ARG;
-  const int rc = need_sm103();
+  DeviceInfo d;
+  const int rc = current_device_info(&d);
   if (rc != MFD_OK) return rc;
+  if (!is_sm103(d)) return MFD_ERR_UNSUPPORTED;
   mfd::ResidualNormArgs A;
   A.y = static_cast<const uint16_t *>(y);
   A.residual = static_cast<const uint16_t *>(residual);
@@ -1123,7 +1125,7 @@ int mfd_residual_norm(const void *y, const void *residual, int dtype, int T, int
   A.eps = eps;
   A.residual_out = static_cast<uint16_t *>(residual_out);
   A.x_out = static_cast<uint16_t *>(x_out);
-  return cuda_status(mfd::launch_residual_norm(A, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(mfd::launch_residual_norm(A, d.n_sm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

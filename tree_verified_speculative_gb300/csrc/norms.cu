@@ -18,7 +18,7 @@ namespace {
 
 __device__ __forceinline__ float activate(float x, int act) {
   if (act == MFD_ACT_NONE) return x;
-  const float s = 1.f / (1.f + __expf(-x));  // x below -88: 1 / inf
+  const float s = __fdividef(1.f, 1.f + __expf(-x));  // to 0 for x far below 0
   return act == MFD_ACT_SIGMOID ? s : x * s;
 }
 // silu of -inf is 0 * -inf otherwise; its limit is 0, but the formula's value is NaN, and stays so.
@@ -35,16 +35,15 @@ __global__ void __launch_bounds__(GATED_THREADS) gated_norm_kernel(const GatedNo
   pdl_wait();
   const int c = threadIdx.x & (LR - 1);
   const bool in_row = c * 8 < p.D;
-  const int64_t rows = (int64_t)p.T * p.heads;
-  const int64_t row0 = (int64_t)blockIdx.x * (PER * U) + threadIdx.x / LR;
+  const uint32_t rows = (uint32_t)p.T * p.heads;  // below 2^31
+  const uint32_t row0 = blockIdx.x * (PER * U) + threadIdx.x / LR;
   uint4 x[U], z[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t row = row0 + u * PER;
+    const uint32_t row = row0 + u * PER;
     x[u] = z[u] = make_uint4(0, 0, 0, 0);
     if (in_row && row < rows) {
-      const int64_t t = row / p.heads;
-      const int h = (int)(row - t * p.heads);
+      const uint32_t t = row / (uint32_t)p.heads, h = row - t * p.heads;
       x[u] = *reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + h * p.D + c * 8);
       z[u] = *reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride + h * p.D + c * 8);
     }
@@ -54,7 +53,7 @@ __global__ void __launch_bounds__(GATED_THREADS) gated_norm_kernel(const GatedNo
   const float per_d = 1.f / (float)p.D;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t row = row0 + u * PER;
+    const uint32_t row = row0 + u * PER;
     float a[8], b[8], ss = 0.f;
     unpack8<T>(x[u], a);
     unpack8<T>(z[u], b);
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(GATED_THREADS) gated_norm_kernel(const GatedNo
     const float r = rsqrtf(fmaf(ss, per_d, p.eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w[i] * activate(b[i], p.act);
-    if (in_row && row < rows) *reinterpret_cast<uint4 *>(p.out + row * p.D + c * 8) = pack8<T>(a);
+    if (in_row && row < rows) *reinterpret_cast<uint4 *>(p.out + (int64_t)row * p.D + c * 8) = pack8<T>(a);
   }
 }
 
@@ -97,91 +96,109 @@ __device__ __forceinline__ float block_sum(float x, float *buf) {
   return warp_sum(lane < warps ? buf[lane] : 0.f);
 }
 
-// A block for each token, CH chunks of 8 elements a thread.
+// A block walks tokens, CH chunks of 8 elements a thread, with the next token's
+// loads in flight and the weights in registers.
 template <typename T, int CH>
 __global__ void __launch_bounds__(512) residual_norm_kernel(const ResidualNormArgs p) {
-  __shared__ float sum_s[2][16];
+  __shared__ float sum_s[2][2][16];  // [token mod 2][norm]
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t t = blockIdx.x, at = t * p.H;
   uint4 y[CH], r[CH], z[CH], wa[CH], wb[CH];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+      if (e < p.H) {
+        y[i] = *reinterpret_cast<const uint4 *>(p.y + t * p.H + e);
+        r[i] = *reinterpret_cast<const uint4 *>(p.residual + t * p.H + e);
+        if (p.gate) z[i] = *reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride + e);
+      }
+    }
+  };
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
     y[i] = r[i] = z[i] = wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
-    if (e < p.H) {
-      y[i] = *reinterpret_cast<const uint4 *>(p.y + at + e);
-      r[i] = *reinterpret_cast<const uint4 *>(p.residual + at + e);
-      if (p.gate) z[i] = *reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride + e);
-      if (p.w_post) wa[i] = __ldg(reinterpret_cast<const uint4 *>(p.w_post + e));
-      if (p.w_pre) wb[i] = __ldg(reinterpret_cast<const uint4 *>(p.w_pre + e));
-    }
+    if (e < p.H && p.w_post) wa[i] = __ldg(reinterpret_cast<const uint4 *>(p.w_post + e));
+    if (e < p.H && p.w_pre) wb[i] = __ldg(reinterpret_cast<const uint4 *>(p.w_pre + e));
   }
   const float per_h = 1.f / (float)p.H;
-  float norm = 1.f;
-  if (p.w_post) {
-    float ss = 0.f;
+  load(blockIdx.x);
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    const int64_t at = t * p.H;
+    float norm = 1.f;
+    if (p.w_post) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        float a[8];
+        unpack8<T>(y[i], a);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], ss);
+      }
+      norm = rsqrtf(fmaf(block_sum(ss, sum_s[turn][0]), per_h, p.eps));
+    }
+    float sum[CH][8], ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      float a[8];
+      const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+      float a[8], b[8], c[8];
       unpack8<T>(y[i], a);
+      unpack8<T>(r[i], b);
+      if (p.w_post) {
+        unpack8<T>(wa[i], c);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], ss);
+        for (int k = 0; k < 8; ++k) a[k] = a[k] * norm * c[k];
+      }
+      if (p.gate) {
+        unpack8<T>(z[i], c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] *= activate(c[k], p.act);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum[i][k] = e < p.H ? fmaf(p.scale, a[k], b[k]) : 0.f;
+        ss = fmaf(sum[i][k], sum[i][k], ss);
+      }
     }
-    norm = rsqrtf(fmaf(block_sum(ss, sum_s[0]), per_h, p.eps));
-  }
-  float sum[CH][8], ss = 0.f;
+    // The next token's rows: other rows than this token's outputs, also where those go
+    // over the inputs.
+    if (t + gridDim.x < p.T) load(t + gridDim.x);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
-    float a[8], b[8], c[8];
-    unpack8<T>(y[i], a);
-    unpack8<T>(r[i], b);
-    if (p.w_post) {
-      unpack8<T>(wa[i], c);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] = a[k] * norm * c[k];
+    for (int i = 0; i < CH; ++i) {
+      const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+      if (e < p.H) *reinterpret_cast<uint4 *>(p.residual_out + at + e) = pack8<T>(sum[i]);
     }
-    if (p.gate) {
-      unpack8<T>(z[i], c);
+    if (!p.w_pre) continue;
+    norm = rsqrtf(fmaf(block_sum(ss, sum_s[turn][1]), per_h, p.eps));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a[k] *= activate(c[k], p.act);
+    for (int i = 0; i < CH; ++i) {
+      const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
+      float c[8];
+      unpack8<T>(wb[i], c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = sum[i][k] * norm * c[k];
+      if (e < p.H) *reinterpret_cast<uint4 *>(p.x_out + at + e) = pack8<T>(c);
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      sum[i][k] = e < p.H ? fmaf(p.scale, a[k], b[k]) : 0.f;
-      ss = fmaf(sum[i][k], sum[i][k], ss);
-    }
-    if (e < p.H) *reinterpret_cast<uint4 *>(p.residual_out + at + e) = pack8<T>(sum[i]);
-  }
-  if (!p.w_pre) return;
-  norm = rsqrtf(fmaf(block_sum(ss, sum_s[1]), per_h, p.eps));
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int e = (i * (int)blockDim.x + (int)threadIdx.x) * 8;
-    float c[8];
-    unpack8<T>(wb[i], c);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = sum[i][k] * norm * c[k];
-    if (e < p.H) *reinterpret_cast<uint4 *>(p.x_out + at + e) = pack8<T>(c);
   }
 }
 
+template <typename T, int CH>
+cudaError_t launch_chunks(const ResidualNormArgs &A, int n_sm, cudaLaunchConfig_t &cfg) {
+  const int threads = (A.H / 8 + CH * 32 - 1) / (CH * 32) * 32;
+  // as many blocks as are resident: their threads times 64 registers, or 96 with more chunks
+  const int fit = 65536 / (threads * (CH == 1 ? 64 : CH == 2 ? 96 : 128)), blocks = n_sm * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3((unsigned)(A.T < blocks ? A.T : blocks));
+  return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, CH>, A);
+}
 template <typename T>
-cudaError_t launch_residual(const ResidualNormArgs &A, cudaLaunchConfig_t &cfg) {
+cudaError_t launch_residual(const ResidualNormArgs &A, int n_sm, cudaLaunchConfig_t &cfg) {
   const int chunks = A.H / 8;
-  cfg.gridDim = dim3((unsigned)A.T);
-  auto threads = [&](int ch) { return dim3((unsigned)((chunks + ch * 32 - 1) / (ch * 32) * 32)); };
-  if (chunks <= 512) {
-    cfg.blockDim = threads(1);
-    return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, 1>, A);
-  }
-  if (chunks <= 1024) {
-    cfg.blockDim = threads(2);
-    return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, 2>, A);
-  }
-  cfg.blockDim = threads(4);
-  return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, 4>, A);
+  if (chunks <= 512) return launch_chunks<T, 1>(A, n_sm, cfg);
+  if (chunks <= 1024) return launch_chunks<T, 2>(A, n_sm, cfg);
+  return launch_chunks<T, 4>(A, n_sm, cfg);
 }
 
 cudaError_t done(cudaError_t e) { return e != cudaSuccess ? e : cudaGetLastError(); }
@@ -199,7 +216,7 @@ cudaError_t launch_gated_norm(const GatedNormArgs &A, cudaStream_t stream) {
   return done(A.dtype == MFD_BF16 ? launch_gated_width<__nv_bfloat16>(A, cfg) : launch_gated_width<__half>(A, cfg));
 }
 
-cudaError_t launch_residual_norm(const ResidualNormArgs &A, cudaStream_t stream) {
+cudaError_t launch_residual_norm(const ResidualNormArgs &A, int n_sm, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -207,7 +224,7 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &A, cudaStream_t stream)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  return done(A.dtype == MFD_BF16 ? launch_residual<__nv_bfloat16>(A, cfg) : launch_residual<__half>(A, cfg));
+  return done(A.dtype == MFD_BF16 ? launch_residual<__nv_bfloat16>(A, n_sm, cfg) : launch_residual<__half>(A, n_sm, cfg));
 }
 
 }  // namespace mfd

@@ -645,8 +645,8 @@ class DeltaState:
     def _set(self, s):
         assert s.dim() == 4 and s.dtype is torch.float32, "states: fp32 [n_slots, Hv, Dk, Dv]"
         struct = _DeltaStateStruct(_p(s), *s.shape)
-        self.__dict__.update(s=s, n_slots=s.shape[0], Hv=s.shape[1], Dk=s.shape[2], Dv=s.shape[3], _lib_struct=struct,
-                             _c=ctypes.byref(struct))
+        self.__dict__.update(s=s, n_slots=s.shape[0], Hv=s.shape[1], Dk=s.shape[2], Dv=s.shape[3], device=s.get_device(),
+                             _lib_struct=struct, _c=ctypes.byref(struct))
 
     def __setattr__(self, name, value):
         if name in self.__dict__:
@@ -654,37 +654,58 @@ class DeltaState:
         object.__setattr__(self, name, value)
 
 
-def _on_current_device(*tensors) -> None:
-    """Kernels run on the current device: tensors of another one are refused."""
-    here = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _here() -> int:
+    """The current device, where kernels run; none without a GPU."""
+    try:
+        return _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    except RuntimeError:
+        return -2
+
+
+def _ptrs(here, *tensors):
+    """Addresses of contiguous tensors (or None) on device `here`."""
+    out = []
     for t in tensors:
-        assert t is None or t.get_device() == here, "tensors on the current device"
+        if t is None:
+            out.append(None)
+        elif t.get_device() == here and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            raise AssertionError("device tensors, contiguous, on the current device")
+    return out
 
 
-def _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status):
+def _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status, here):
     """What the three forms of the delta rule ask of their common arguments:
-    (n_req, N, Hk, pointers and strides of k and v)."""
-    i32 = torch.int32
+    (n_req, N, Hk, k and v with their strides)."""
+    dt, i32, f32 = k.dtype, torch.int32, torch.float32
     n_req, N, Hk, Dk = k.shape
-    assert k.dtype in (torch.bfloat16, torch.float16) and v.dtype is k.dtype, "k and v: bf16 or fp16"
-    assert Dk == state.Dk and v.shape == (n_req, N, state.Hv, state.Dv), "k [n_req, N, Hk, Dk], v [n_req, N, Hv, Dv]"
-    for t in (g, beta):
-        assert t.dtype is torch.float32 and t.shape == (n_req, N, state.Hv), "g and beta: fp32 [n_req, N, Hv]"
+    Hv, Dv = state.Hv, state.Dv
+    heads = (n_req, N, Hv)
+    assert dt in _HALF and v.dtype is dt, "k and v: bf16 or fp16"
+    assert Dk == state.Dk and v.shape == (n_req, N, Hv, Dv), "k [n_req, N, Hk, Dk], v [n_req, N, Hv, Dv]"
+    assert g.dtype is f32 and beta.dtype is f32 and g.shape == heads and beta.shape == heads, "g and beta: fp32 [n_req, N, Hv]"
     for t in (n_nodes, src, dst):
         assert t is None or (t.dtype is i32 and t.numel() == n_req), "n_nodes, src, dst: int32 [n_req]"
     assert status.dtype is i32, "status: int32"
-    assert (src is not None and dst is not None) or n_req <= state.n_slots, "a slot for each request"
+    assert n_req <= state.n_slots or (src is not None and dst is not None), "a slot for each request"
+    assert k.get_device() == here and v.get_device() == here and state.device == here, "device tensors, on the current device"
     kp, ks = _rows(k, Hk, Dk)
-    vp, vs = _rows(v, state.Hv, state.Dv)
-    _on_current_device(k, v, g, beta, n_nodes, src, dst, status, state.s)
+    vp, vs = _rows(v, Hv, Dv)
     return n_req, N, Hk, kp, ks, vp, vs
 
 
-def _delta_queries(q, k, out, state):
+def _delta_queries(q, k, v, out, ks, here):
+    """q with its stride."""
     assert q.shape == k.shape and q.dtype is k.dtype, "q: as k"
-    assert out.shape == (k.shape[0], k.shape[1], state.Hv, state.Dv) and out.dtype is k.dtype, "out: [n_req, N, Hv, Dv]"
-    _on_current_device(q, out)
-    return _rows(q, q.shape[2], q.shape[3])
+    assert out.shape == v.shape and out.dtype is k.dtype, "out: [n_req, N, Hv, Dv]"
+    assert q.get_device() == here, "device tensors, on the current device"
+    if q.stride() == k.stride():  # checked with k
+        return q.data_ptr(), ks
+    return _rows(q, k.shape[2], k.shape[3])
 
 
 def mfd_delta_rule(q, k, v, g, beta, eps, scale, n_nodes, out, state, src, dst, status, stream=None) -> None:
@@ -693,52 +714,54 @@ def mfd_delta_rule(q, k, v, g, beta, eps, scale, n_nodes, out, state, src, dst, 
     and `state` (DeltaState), from slots src to slots dst (int32 [n_req], or
     None).  eps: of the queries' and keys' length, or None (taken as they are).
     n_nodes may be None (all N rows live)."""
-    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status)
-    qp, qs = _delta_queries(q, k, out, state)
-    rc = load().mfd_delta_rule(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta),
-                               0 if eps is None else 1, eps or 0.0, scale, _p(n_nodes), _p(out), state._c, _p(src), _p(dst),
-                               _p(status), _s(stream))
+    here = _here()
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status, here)
+    qp, qs = _delta_queries(q, k, v, out, ks, here)
+    gp, bp, np, op, sp, dp, tp = _ptrs(here, g, beta, n_nodes, out, src, dst, status)
+    rc = load().mfd_delta_rule(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, gp, bp, 0 if eps is None else 1, eps or 0.0,
+                               scale, np, op, state._c, sp, dp, tp, _s(stream))
     _check(rc, "mfd_delta_rule")
 
 
 def mfd_delta_tree(q, k, v, g, beta, eps, scale, parent, n_nodes, out, state, src, status, stream=None) -> None:
     """The same for the nodes of a tree (parent int32 [n_req, N] from
     mfd_build_tree), each behind its own path; the states stay."""
-    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, src, status)
-    qp, qs = _delta_queries(q, k, out, state)
+    here = _here()
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, src, status, here)
+    qp, qs = _delta_queries(q, k, v, out, ks, here)
     assert parent.dtype is torch.int32 and parent.shape == (n_req, N), "parent: int32 [n_req, N]"
-    _on_current_device(parent)
-    rc = load().mfd_delta_tree(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta),
-                               0 if eps is None else 1, eps or 0.0, scale, _p(parent), _p(n_nodes), _p(out), state._c,
-                               _p(src), _p(status), _s(stream))
+    gp, bp, pp, np, op, sp, tp = _ptrs(here, g, beta, parent, n_nodes, out, src, status)
+    rc = load().mfd_delta_tree(qp, qs, kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, gp, bp, 0 if eps is None else 1, eps or 0.0,
+                               scale, pp, np, op, state._c, sp, tp, _s(stream))
     _check(rc, "mfd_delta_tree")
 
 
 def mfd_delta_commit(k, v, g, beta, eps, accept_len, path_nodes, n_nodes, state, src, dst, status, stream=None) -> None:
     """The state behind the accepted path (mfd_verify's accept_len and
     path_nodes) of the rows that mfd_delta_tree was given."""
-    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status)
-    i32 = torch.int32
-    assert path_nodes.dtype is i32 and path_nodes.dim() == 2 and path_nodes.shape[0] == n_req, "path_nodes: int32 [n_req, L + 1]"
+    here, i32 = _here(), torch.int32
+    n_req, N, Hk, kp, ks, vp, vs = _delta_rows(k, v, g, beta, n_nodes, state, src, dst, status, here)
+    n, L1 = path_nodes.shape
+    assert path_nodes.dtype is i32 and n == n_req, "path_nodes: int32 [n_req, L + 1]"
     assert accept_len.dtype is i32 and accept_len.numel() == n_req, "accept_len: int32 [n_req]"
-    _on_current_device(accept_len, path_nodes)
-    rc = load().mfd_delta_commit(kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, _p(g), _p(beta), 0 if eps is None else 1,
-                                 eps or 0.0, path_nodes.shape[1] - 1, _p(accept_len), _p(path_nodes), _p(n_nodes), state._c,
-                                 _p(src), _p(dst), _p(status), _s(stream))
+    gp, bp, ap, pp, np, sp, dp, tp = _ptrs(here, g, beta, accept_len, path_nodes, n_nodes, src, dst, status)
+    rc = load().mfd_delta_commit(kp, ks, vp, vs, _DTYPE[k.dtype], n_req, N, Hk, gp, bp, 0 if eps is None else 1, eps or 0.0, L1 - 1,
+                                 ap, pp, np, state._c, sp, dp, tp, _s(stream))
     _check(rc, "mfd_delta_commit")
 
 
 def mfd_gated_norm(x, gate, w, eps, act, out, stream=None) -> None:
     """out = norm of x [.., T, heads, D] over D, times w [D] and the activated
     gate (x's shape); act: "none", "sigmoid" or "silu"."""
-    heads, D = x.shape[-2:]
-    assert x.dtype in (torch.bfloat16, torch.float16) and gate.dtype is x.dtype and out.dtype is x.dtype and w.dtype is x.dtype
-    assert gate.shape == x.shape and out.shape == x.shape and w.shape == (D,), "gate and out: as x; w: [D]"
+    here, shape, dt = _here(), x.shape, x.dtype
+    heads, D = shape[-2:]
+    assert dt in _HALF and gate.dtype is dt and out.dtype is dt and w.dtype is dt, "bf16 or fp16, all the same"
+    assert gate.shape == shape and out.shape == shape and w.shape == (D,), "gate and out: as x; w: [D]"
     assert act in _ACT, "act: none, sigmoid or silu"
+    assert x.get_device() == here and gate.get_device() == here, "device tensors, on the current device"
     (xp, xs), (gp, gs) = _rows(x, heads, D), _rows(gate, heads, D)
-    _on_current_device(x, gate, w, out)
-    rc = load().mfd_gated_norm(xp, xs, gp, gs, _DTYPE[x.dtype], x.numel() // (heads * D), heads, D, _p(w), eps, _ACT[act],
-                               _p(out), _s(stream))
+    wp, op = _ptrs(here, w, out)
+    rc = load().mfd_gated_norm(xp, xs, gp, gs, _DTYPE[dt], x.numel() // (heads * D), heads, D, wp, eps, _ACT[act], op, _s(stream))
     _check(rc, "mfd_gated_norm")
 
 
@@ -746,26 +769,26 @@ def mfd_residual_norm(y, residual, w_post, gate, act, scale, w_pre, eps, residua
     """residual_out = residual + scale * act(gate) * norm(y; w_post) and x_out =
     norm(residual_out; w_pre), rows of y [.., T, H].  w_post, gate, and w_pre
     with x_out may be None; gate is [.., T, H] or one row."""
-    H = y.shape[-1]
-    T = y.numel() // H if H else 0
-    assert y.dtype in (torch.bfloat16, torch.float16) and residual.dtype is y.dtype and residual_out.dtype is y.dtype
-    assert residual.shape == y.shape and residual_out.shape == y.shape, "residual and residual_out: as y"
+    here, shape, dt = _here(), y.shape, y.dtype
+    H = shape[-1]
+    assert dt in _HALF and residual.dtype is dt and residual_out.dtype is dt, "bf16 or fp16, all the same"
+    assert residual.shape == shape and residual_out.shape == shape, "residual and residual_out: as y"
     for w in (w_post, w_pre):
-        assert w is None or (w.dtype is y.dtype and w.shape == (H,)), "norm weights [H] of y's type"
+        assert w is None or (w.dtype is dt and w.shape == (H,)), "norm weights [H] of y's type"
     assert (w_pre is None) == (x_out is None), "w_pre and x_out: both or none"
-    assert x_out is None or (x_out.shape == y.shape and x_out.dtype is y.dtype), "x_out: as y"
+    assert x_out is None or (x_out.shape == shape and x_out.dtype is dt), "x_out: as y"
     assert act in _ACT, "act: none, sigmoid or silu"
     gp, gs = None, 0
     if gate is not None:
-        assert gate.dtype is y.dtype, "gate of y's type"
+        assert gate.dtype is dt and gate.get_device() == here, "gate of y's type, on the current device"
         if gate.numel() == H:
-            gp = _p(gate)
+            gp, = _ptrs(here, gate)
         else:
-            assert gate.shape == y.shape, "gate: as y, or one row"
+            assert gate.shape == shape, "gate: as y, or one row"
             gp, gs = _rows(gate.unsqueeze(-2), 1, H)
-    _on_current_device(y, residual, w_post, gate, w_pre, residual_out, x_out)
-    rc = load().mfd_residual_norm(_p(y), _p(residual), _DTYPE[y.dtype], T, H, _p(w_post), gp, gs, _ACT[act], scale,
-                                  _p(w_pre), eps, _p(residual_out), _p(x_out), _s(stream))
+    yp, rp, ap, bp, op, xp = _ptrs(here, y, residual, w_post, w_pre, residual_out, x_out)
+    rc = load().mfd_residual_norm(yp, rp, _DTYPE[dt], y.numel() // H if H else 0, H, ap, gp, gs, _ACT[act], scale, bp, eps, op, xp,
+                                  _s(stream))
     _check(rc, "mfd_residual_norm")
 
 
