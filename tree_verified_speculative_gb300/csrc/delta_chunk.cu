@@ -73,7 +73,7 @@ struct Smem {
   float top[2][2][LANES];                  // [state, right sides][half][column]
   uint64_t full[2], empty[2], gram, x, xq, u, s, o, drain, ps, pb, pz, py;
   uint32_t tmem;
-  int bad[2], chain_bad, abort;
+  int bad[2], chain_bad, abort, request;
 };
 constexpr int SMEM = sizeof(Smem) + 1024;  // and to a 1024-byte border
 static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
   extern __shared__ uint8_t raw_smem[];
   Smem &sm = *reinterpret_cast<Smem *>(raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.Hv, r = blockIdx.x / slices / p.Hv;
+  const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.Hv;
   const int hk = h / (p.Hv / p.Hk);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
     }
     for (uint64_t *b : {&sm.gram, &sm.x, &sm.xq, &sm.u, &sm.s, &sm.o}) mbar_init(b, 1);
     for (uint64_t *b : {&sm.ps, &sm.pb, &sm.pz, &sm.py}) mbar_init(b, CHAIN / 32);
-    mbar_init(&sm.drain, 5);
+    mbar_init(&sm.drain, 6);
     sm.chain_bad = 0;
     sm.abort = 0;
     fence_mbar_init();
@@ -129,6 +129,22 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
   // ask for some on the same SM and keep it until this grid has ended
   pdl_launch_dependents();
   pdl_wait();
+  // The longest requests' blocks come first (while a thread a request orders them): a
+  // short one's fit where the long ones leave SMs free at the end.
+  int r = blockIdx.x / slices / p.Hv;
+  if (p.n_nodes && p.n_req > 1 && p.n_req <= THREADS) {
+    int *len = reinterpret_cast<int *>(sm.At);
+    const int own = tid < p.n_req ? __ldg(p.n_nodes + tid) : 0;
+    if (tid < p.n_req) len[tid] = own;
+    block_sync();
+    if (tid < p.n_req) {
+      int place = 0;
+      for (int i = 0; i < p.n_req; ++i) place += len[i] > own || (len[i] == own && i < tid);
+      if (place == r) sm.request = tid;
+    }
+    block_sync();
+    r = sm.request;
+  }
   const Request q = request(p, r);
   const int nn = q.ok ? q.nn : 0, n_chunk = (nn + C - 1) / C;
   const int64_t tok0 = (int64_t)r * p.N;
@@ -340,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       {
         const int b = (t >> 7) * 32, i = b + 16 + ((t & 127) >> 3), j = b + (t & 7) * 2;
         float2 acc = make_float2(0, 0);
-#pragma unroll 8
+#pragma unroll
         for (int m = 0; m < 16; ++m) {
           const float a = sm.At[(b + m) * PAD + i];
           const float2 x = *reinterpret_cast<const float2 *>(&sm.T[(b + m) * PAD + j]);
@@ -350,41 +366,59 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         *reinterpret_cast<float2 *>(&sm.At[i * PAD + j]) = acc;
         named_sync(2, PREP);
         acc = make_float2(0, 0);
-#pragma unroll 8
-        for (int m = 0; m < 16; ++m) {
-          const float a = -sm.T[i * PAD + b + 16 + m];
-          const float2 x = *reinterpret_cast<const float2 *>(&sm.At[(b + 16 + m) * PAD + j]);
-          acc.x = fmaf(a, x.x, acc.x);
-          acc.y = fmaf(a, x.y, acc.y);
+#pragma unroll
+        for (int m = 0; m < 16; m += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(&sm.T[i * PAD + b + 16 + m]);
+          const float aa[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = *reinterpret_cast<const float2 *>(&sm.At[(b + 16 + m + e) * PAD + j]);
+            acc.x = fmaf(-aa[e], x.x, acc.x);
+            acc.y = fmaf(-aa[e], x.y, acc.y);
+          }
         }
         *reinterpret_cast<float2 *>(&sm.T[i * PAD + j]) = acc;
       }
       named_sync(2, PREP);
-      {
-        const int i = 32 + (t >> 3), j = (t & 7) * 4;
-        float4 acc = make_float4(0, 0, 0, 0);
+      if (t < 128) {  // eight elements a thread, two rows: a load for every five products
+        const int i = 32 + (t >> 3) * 2, j = (t & 7) * 4;
+        float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
 #pragma unroll 8
         for (int m = 0; m < 32; ++m) {
-          const float a = sm.At[m * PAD + i];
+          const float2 a = *reinterpret_cast<const float2 *>(&sm.At[m * PAD + i]);
           const float4 x = *reinterpret_cast<const float4 *>(&sm.T[m * PAD + j]);
-          acc.x = fmaf(a, x.x, acc.x);
-          acc.y = fmaf(a, x.y, acc.y);
-          acc.z = fmaf(a, x.z, acc.z);
-          acc.w = fmaf(a, x.w, acc.w);
+          acc[0].x = fmaf(a.x, x.x, acc[0].x);
+          acc[0].y = fmaf(a.x, x.y, acc[0].y);
+          acc[0].z = fmaf(a.x, x.z, acc[0].z);
+          acc[0].w = fmaf(a.x, x.w, acc[0].w);
+          acc[1].x = fmaf(a.y, x.x, acc[1].x);
+          acc[1].y = fmaf(a.y, x.y, acc[1].y);
+          acc[1].z = fmaf(a.y, x.z, acc[1].z);
+          acc[1].w = fmaf(a.y, x.w, acc[1].w);
         }
-        *reinterpret_cast<float4 *>(&sm.At[i * PAD + j]) = acc;
-        named_sync(2, PREP);
-        acc = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int m = 0; m < 32; ++m) {
-          const float a = -sm.T[i * PAD + 32 + m];
-          const float4 x = *reinterpret_cast<const float4 *>(&sm.At[(32 + m) * PAD + j]);
-          acc.x = fmaf(a, x.x, acc.x);
-          acc.y = fmaf(a, x.y, acc.y);
-          acc.z = fmaf(a, x.z, acc.z);
-          acc.w = fmaf(a, x.w, acc.w);
+        *reinterpret_cast<float4 *>(&sm.At[i * PAD + j]) = acc[0];
+        *reinterpret_cast<float4 *>(&sm.At[(i + 1) * PAD + j]) = acc[1];
+        named_sync(9, 128);
+        acc[0] = acc[1] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+        for (int m = 0; m < 32; m += 4) {
+          const float4 a0 = *reinterpret_cast<const float4 *>(&sm.T[i * PAD + 32 + m]);
+          const float4 a1 = *reinterpret_cast<const float4 *>(&sm.T[(i + 1) * PAD + 32 + m]);
+          const float a[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.At[(32 + m + e) * PAD + j]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              acc[k].x = fmaf(-a[k][e], x.x, acc[k].x);
+              acc[k].y = fmaf(-a[k][e], x.y, acc[k].y);
+              acc[k].z = fmaf(-a[k][e], x.z, acc[k].z);
+              acc[k].w = fmaf(-a[k][e], x.w, acc[k].w);
+            }
+          }
         }
-        *reinterpret_cast<float4 *>(&sm.T[i * PAD + j]) = acc;
+        *reinterpret_cast<float4 *>(&sm.T[i * PAD + j]) = acc[0];
+        *reinterpret_cast<float4 *>(&sm.T[(i + 1) * PAD + j]) = acc[1];
       }
       named_sync(2, PREP);
       {
@@ -553,12 +587,16 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       arrive(&sm.ps);
       wait_warp(&sm.full[n & 1], (n >> 1) & 1u);
       products(0, &sm.ps, par, [&]() {  // S^T K^T, then S^T Q^T
-        const uint32_t kq = desc_lo(smem_u32(st.kq), 16), d = tmem + TM_XQ + (n & 1) * C;
+        const uint32_t kq = desc_lo(smem_u32(st.kq), 16);
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if ((k & 7) < steps)
             mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, kq + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id, k != 0);
         tc_commit(&sm.x);
+      });
+      // by another warp, behind the first: issuing them takes as long as they run
+      products(4, &sm.x, par, [&]() {
+        const uint32_t kq = desc_lo(smem_u32(st.kq), 16), d = tmem + TM_XQ + (n & 1) * C;
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if ((k & 7) < steps)
@@ -807,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
     }
   }
   // no product runs on when tensor memory is given back
-  if (warp < 4 || warp == CHAIN / 32) {
+  if (warp < 5 || warp == CHAIN / 32) {
     if (elect_one()) {
       tc_commit(&sm.drain);
       int never = 0;
