@@ -12,17 +12,19 @@
 //   o_i = scale s_i (e^(c_i) S^T q_i + sum_{j <= i} e^(c_i - c_j) (q_i . k_j) y_j)
 //   S  <- e^(c_end) S + sum_j e^(c_end - c_j) k_j y_j^T
 //
-// where rows of K and Q are held times a power of two that gives them lengths in
-// [1, 2), and r_i, s_i are what is left of their factors (the norm's among
-// them).
+// where k_j and q_i are taken times a power of two that gives them lengths in
+// [1, 2), and r_i, s_i are what is left of their factors (the norm's among them).
 //
-// Operands.  The tensor cores take 16-bit factors.  Keys and queries are fp16
-// (bf16's 8 bits fit exactly; only elements below 2^-17 of their row lose bits,
-// 2^-25 of the row's length at most).  Everything computed (states, right sides,
-// the system's inverse, updates) goes in as the sum of two fp16 numbers, 22 bits,
-// scaled by a power of two for each column of the state, so that results are
-// fp32's: the product of the two low halves is left out (2^-22).  States stay in
-// fp32 registers.
+// Operands.  The tensor cores take 16-bit factors.  Keys and queries go in as
+// they are; their powers are in the other factors.  The state, and what its step
+// takes of the updates, go in as sums of numbers of their type: three of bf16,
+// each the front of what is left (24 bits), or two of fp16 after a power of two
+// for each column (22 bits).  What meets no key or query (the right sides, the
+// system's inverse, the updates) is two fp16 numbers, 22 bits, under a power of
+// two for each column.  So results are fp32's: products of two low halves are
+// left out (2^-22).  The state itself stays in fp32 registers: the tensor cores' sums
+// cut off what they cannot hold, and a step added to it there, sixteen rows at a time,
+// left slow heads' states 3e-6 off after some thousand rows.
 //
 // A block has one head's state, transposed: a column of the state is a lane of
 // tensor memory, which two threads of the chain share, half of the column and
@@ -37,6 +39,7 @@
 // anything is not finite, or leaves fp16's range, is done over row by row from
 // the inputs, in fp32, by the chain's threads.
 #include <atomic>
+#include <type_traits>
 
 #include "delta_tc.cuh"
 
@@ -48,13 +51,16 @@ constexpr int MAX_DK = 128;
 constexpr int LANES = 128;    // columns of a state in a block
 constexpr int CHAIN = 256, PREP = 256, THREADS = CHAIN + PREP;
 constexpr float MAX_HALF = 65504.f;
+// Registers of the two roles' threads: what the one gives up the other takes.
+constexpr int LAUNCH_REGS = 128, PREP_REGS = 96, CHAIN_REGS = 160;
+static_assert(PREP * PREP_REGS + CHAIN * CHAIN_REGS == THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS == 65536, "registers of an SM");
 
 constexpr int BLOCK = 128 * 128;           // 64 columns of the 128 rows of keys and queries
 constexpr int TRI = C * 128;               // a 64 x 64 operand
 constexpr int PAD = C + 4;                 // floats of a row of the prep's scratch
 struct Coef {                              // of a chunk's rows
   float2 rhs[C];                           // of v and of S^T k in b
-  float until[C], ec[C];
+  float until[C], eq[C], end;              // of the updates in the step, of S^T q in o, of the state
 };
 struct alignas(1024) Stage {
   uint8_t kq[2 * BLOCK];  // keys' 64 rows, then queries': [64-column block][row][128 bytes, swizzled]
@@ -67,11 +73,11 @@ struct Smem {
   float At[C * PAD], T[C * PAD];           // A transposed; the inverse
   uint16_t out[C * LANES];
   float n2[2 * C];                         // squared lengths
-  alignas(16) float2 cc[C];                // sums of log2 decays as two floats each
+  float4 cc[C];                            // sums of log2 decays as two floats each; the key's power
   float g[C], beta[C];
   float fq[3][C];                          // outputs' factors, which are used a chunk later than the rest
   float top[2][2][LANES];                  // [state, right sides][half][column]
-  uint64_t full[2], empty[2], gram, x, xq, u, s, o, drain, ps, pb, pz, py;
+  uint64_t full[2], empty[2], gram, x, xq, u, s, o, drain, ps, pq, pb, pz, py;
   uint32_t tmem;
   int bad[2], chain_bad, abort, request;
 };
@@ -79,11 +85,11 @@ constexpr int SMEM = sizeof(Smem) + 1024;  // and to a 1024-byte border
 static_assert(SMEM <= 232448, "shared memory of one CTA");
 
 // Tensor memory, columns.  What is written over what has been read by then.
-constexpr int TM_S = 0;      // the state in fp32, times a power of two for each column
-constexpr int TM_H = 128;    // its halves (64 + 64); right sides' (32 + 32), then the updates'
-constexpr int TM_Z = 192;    // the updates' halves times their decays
-constexpr int TM_XK = 256;   // S^T K^T; the updates
-constexpr int TM_XQ = 320;   // S^T Q^T, then outputs; two in turn
+constexpr int TM_S = 0;      // the state's step
+constexpr int TM_H = 128;    // the state's parts (64 each); right sides' halves (32 + 32), then the updates'
+constexpr int TM_Z = 192;    // the parts of the updates times their decays (32 each)
+constexpr int TM_XK = 320;   // S^T K^T; the updates
+constexpr int TM_XQ = 384;   // S^T Q^T, then outputs
 constexpr int TM_G = 448;    // [K; Q] K^T
 
 // The same of x times a power of two that brings the column's largest to [2^11,
@@ -97,8 +103,21 @@ __device__ __forceinline__ void halves_at(uint64_t x, uint64_t up, uint32_t &hi,
   hi = *reinterpret_cast<const uint32_t *>(&hh);
   lo = *reinterpret_cast<const uint32_t *>(&ll);
 }
+// Three bf16 numbers of two floats: each the front of what is left.
+__device__ __forceinline__ void thirds(float a, float b, uint32_t &x, uint32_t &y, uint32_t &z) {
+  x = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  a -= __uint_as_float(x << 16);
+  b -= __uint_as_float(x & 0xFFFF0000u);
+  y = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  a -= __uint_as_float(y << 16);
+  b -= __uint_as_float(y & 0xFFFF0000u);
+  z = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs p, int slices) {
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int PARTS = BF16 ? 3 : 2;
   extern __shared__ uint8_t raw_smem[];
   Smem &sm = *reinterpret_cast<Smem *>(raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -111,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       sm.bad[i] = 0;
     }
     for (uint64_t *b : {&sm.gram, &sm.x, &sm.xq, &sm.u, &sm.s, &sm.o}) mbar_init(b, 1);
-    for (uint64_t *b : {&sm.ps, &sm.pb, &sm.pz, &sm.py}) mbar_init(b, CHAIN / 32);
+    for (uint64_t *b : {&sm.ps, &sm.pq, &sm.pb, &sm.pz, &sm.py}) mbar_init(b, CHAIN / 32);
     mbar_init(&sm.drain, 6);
     sm.chain_bad = 0;
     sm.abort = 0;
@@ -166,75 +185,59 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
 
   if (warp >= CHAIN / 32) {
     // ----------------------------------------------------------- prep
-    const int t = tid - CHAIN, c8 = t & 15, r16 = t >> 4;
-    uint4 raw[8];
-    float graw = 0.f, braw = 0.f;
-    // rows r16, r16 + 16, .. of keys, then of queries, 8 columns each; g and beta of row t
-    auto load = [&](int n) {
-      const int row0 = n * C;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = row0 + (i * 16 + r16) % C;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (row < nn && c8 * 8 < p.Dk)
-          raw[i] = __ldg(reinterpret_cast<const uint4 *>((i < 4 ? p.k + (tok0 + row) * p.k_stride : p.q + (tok0 + row) * p.q_stride) +
-                                                         hk * p.Dk + c8 * 8));
-      }
-      graw = braw = 0.f;
-      if (t < C && row0 + t < nn) {
-        graw = __ldg(p.g + (tok0 + row0 + t) * p.Hv + h);
-        braw = __ldg(p.beta + (tok0 + row0 + t) * p.Hv + h);
-      }
-    };
-    if (n_chunk) load(0);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PREP_REGS));
+    const int t = tid - CHAIN;
     for (int i = t; i < C * PAD; i += PREP) sm.T[i] = 0.f;  // above its diagonal blocks it stays so
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
+      const int row0 = n * C;
       wait_warp(&sm.empty[n & 1], ((n >> 1) & 1u) ^ 1u);
       float most = 0.f;  // largest magnitude, NaN where there is one
       bool bad = false;
       if (t == 0) sm.bad[n & 1] = 0;
+      // keys, queries and values as they are, zeros past the end
+      {
+        const int c8 = t & 15, r16 = t >> 4;
+        const int64_t tok = tok0 + row0 + r16;
+        const uint16_t *kr = p.k + tok * p.k_stride + hk * p.Dk + c8 * 8, *qr = p.q + tok * p.q_stride + hk * p.Dk + c8 * 8;
+        const uint16_t *vr = p.v + tok * p.v_stride + h * p.Dv + slice * LANES + c8 * 8;
+        const bool dk = c8 * 8 < p.Dk, dv = slice * LANES + c8 * 8 < p.Dv;
+        const uint32_t to = smem_u32(st.kq) + (c8 >> 3) * BLOCK + r16 * 128 + (((c8 & 7) ^ (r16 & 7)) << 4);
+        const uint32_t tv = smem_u32(st.v) + r16 * (LANES * 2) + c8 * 16;
+        if (ok)
+#pragma unroll
+          for (int i = 0; i < C / 16; ++i) {
+            const bool live = row0 + i * 16 + r16 < nn;
+            if (live && dk) {
+              cp_async16(to + i * (16 * 128), kr + i * 16 * p.k_stride);
+              cp_async16(to + (C + i * 16) * 128, qr + i * 16 * p.q_stride);
+            } else {
+              st_shared16(to + i * (16 * 128), make_uint4(0, 0, 0, 0));
+              st_shared16(to + (C + i * 16) * 128, make_uint4(0, 0, 0, 0));
+            }
+            if (live && dv)
+              cp_async16(tv + i * (16 * LANES * 2), vr + i * 16 * p.v_stride);
+            else
+              st_shared16(tv + i * (16 * LANES * 2), make_uint4(0, 0, 0, 0));
+          }
+      }
       if (t < C) {
-        sm.g[t] = graw < LEAST_LOG ? LEAST_LOG : graw;
-        sm.beta[t] = braw;
-        if (!finite(braw) || !(graw < INFINITY)) bad = true;
-      }
-      float ss[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float x[8];
-        unpack8<T>(raw[i], x);
-        ss[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss[i] = fmaf(x[e], x[e], ss[i]);
-      }
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + r16;
-        float x[8];
-        unpack8<T>(raw[i], x);
-        if (!finite(ss[i])) bad = true;
-        const int half_e = ((int)(__float_as_uint(ss[i]) >> 23) - 127) >> 1;  // floor(log2 of the length)
-        const float f = __uint_as_float((uint32_t)(127 - half_e) << 23);
-        __half2 y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __floats2half2_rn(x[2 * e] * f, x[2 * e + 1] * f);
-        if (ok) {
-          *reinterpret_cast<uint4 *>(st.kq + (c8 >> 3) * BLOCK + row * 128 + (((c8 & 7) ^ (row & 7)) << 4)) =
-              *reinterpret_cast<const uint4 *>(y);
-          if (c8 == 0) sm.n2[row] = ss[i];
+        float g = 0.f, beta = 0.f;
+        if (row0 + t < nn) {
+          g = __ldg(p.g + (tok0 + row0 + t) * p.Hv + h);
+          beta = __ldg(p.beta + (tok0 + row0 + t) * p.Hv + h);
         }
+        if (!finite(beta) || !(g < INFINITY)) bad = true;
+        sm.g[t] = g < LEAST_LOG ? LEAST_LOG : g;
+        sm.beta[t] = beta;
       }
+      cp_async_wait();
       fence_async_smem();
       named_sync(2, PREP);
       if (warp == CHAIN / 32) {
         if (elect_one() && ok) {
           tc_fence_after();
-          constexpr uint32_t id = idesc_16<__half>(128, C, false);
+          constexpr uint32_t id = idesc_16<T>(128, C, false);
           const uint32_t a = desc_lo(smem_u32(st.kq), 16);
           const int steps = p.Dk / 16;
 #pragma unroll
@@ -259,40 +262,52 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         Two before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
         if (lane == 0) before = {0.f, 0.f};
         const Two first = two_sum(before, a);
-        sm.cc[2 * lane] = make_float2(first.hi, first.lo);
-        sm.cc[2 * lane + 1] = make_float2(run.hi, run.lo);
+        *reinterpret_cast<float2 *>(&sm.cc[2 * lane]) = make_float2(first.hi, first.lo);
+        *reinterpret_cast<float2 *>(&sm.cc[2 * lane + 1]) = make_float2(run.hi, run.lo);
       }
-      // values, as they are
-      for (int i = t; i < C * 16; i += PREP) {
-        const int row = i >> 4, ch = i & 15, col = slice * LANES + ch * 8;
-        uint8_t *dst = reinterpret_cast<uint8_t *>(st.v) + row * (LANES * 2) + ch * 16;
-        if (!ok) continue;
-        if (n * C + row < nn && col < p.Dv)
-          cp_async16(smem_u32(dst), p.v + (tok0 + n * C + row) * p.v_stride + h * p.Dv + col);
-        else
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+      {  // squared lengths, two threads a row
+        const int row = t >> 1, part = t & 1;
+        float ss[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x[8];
+          unpack8<T>(ld_shared16(smem_u32(st.kq) + part * BLOCK + row * 128 + ((e ^ (row & 7)) << 4)), x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) ss[k & 3] = fmaf(x[k], x[k], ss[k & 3]);
+        }
+        float len2 = (ss[0] + ss[1]) + (ss[2] + ss[3]);
+        len2 += __shfl_xor_sync(0xffffffffu, len2, 1);
+        if (!finite(len2)) bad = true;
+        if (part == 0) {
+          sm.n2[row] = len2;
+          if (row < C) sm.cc[row].z = __uint_as_float((uint32_t)(127 - (((int)(__float_as_uint(len2) >> 23) - 127) >> 1)) << 23);
+        }
       }
-      if (n + 1 < n_chunk) load(n + 1);
       named_sync(2, PREP);
       wait_warp(&sm.gram, n & 1u);
       // this thread's row of [K; Q] K^T, half of its columns
       const int row = t & 63, j1 = (t >> 7) * 32;
       const bool is_q = (t & 127) >= C;
-      const float2 ci = sm.cc[row];
-      const float len2 = sm.n2[t & 127];
-      const int half_e = ((int)(__float_as_uint(len2) >> 23) - 127) >> 1;
+      const float4 ci = sm.cc[row];
+      const float len2 = row0 + row < nn ? sm.n2[t & 127] : 1.f;
+      const int half_e = ((int)(__float_as_uint(len2) >> 23) - 127) >> 1;  // floor(log2 of the length)
       const float left = (p.normalize ? rsqrtf(len2 + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
+      const float power = __uint_as_float((uint32_t)(127 - half_e) << 23);
       const float br = sm.beta[row] * left, brr = br * left;
-      if (t < C) {
-        const float2 end = sm.cc[C - 1];
-        const float ec = ex2(ci.x + ci.y), until = ex2((end.x - ci.x) + (end.y - ci.y));
-        st.c.rhs[row] = make_float2(br, -brr * ec);
-        st.c.until[row] = until;
-        st.c.ec[row] = ec;
-        if (!finite(br) || !finite(brr * ec) || !finite(until)) bad = true;
-      } else if (t < 2 * C) {
-        sm.fq[n % 3][row] = left * p.scale;
-        if (!finite(left)) bad = true;
+      if (t < 2 * C) {
+        const float ec = ex2(ci.x + ci.y);
+        if (!is_q) {
+          const float4 end = sm.cc[C - 1];
+          const float until = ex2((end.x - ci.x) + (end.y - ci.y)) * power;
+          st.c.rhs[row] = make_float2(br, -brr * ec * power);
+          st.c.until[row] = until;
+          if (row == C - 1) st.c.end = ec;
+          if (!finite(br) || !finite(brr * ec * power) || !finite(until)) bad = true;
+        } else {
+          st.c.eq[row] = ec * power;
+          sm.fq[n % 3][row] = left * p.scale;
+          if (!finite(left) || !finite(ec)) bad = true;
+        }
       }
       if (ok) {
         tc_fence_after();
@@ -301,17 +316,16 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tmem_wait_ld();
         tie32(x);
         tc_fence_before();
-        const float f = is_q ? 1.f : brr;
+        const float f = is_q ? power : brr * power;
         const int last = is_q ? row : row - 1;
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float4 cj = *reinterpret_cast<const float4 *>(&sm.cc[j1 + e]);
-          const float z0 = __uint_as_float(x[e]) * (f * ex2((ci.x - cj.x) + (ci.y - cj.y)));
-          const float z1 = __uint_as_float(x[e + 1]) * (f * ex2((ci.x - cj.z) + (ci.y - cj.w)));
-          x[e] = j1 + e <= last ? __float_as_uint(z0) : 0u;
-          x[e + 1] = j1 + e + 1 <= last ? __float_as_uint(z1) : 0u;
-          most = max_nan(most, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        for (int e = 0; e < 32; ++e) {
+          const float4 cj = sm.cc[j1 + e];
+          const float z = __uint_as_float(x[e]) * (f * (cj.z * ex2((ci.x - cj.x) + (ci.y - cj.y))));
+          x[e] = j1 + e <= last ? __float_as_uint(z) : 0u;
         }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) most = max_nan(most, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
         if (is_q) {
 #pragma unroll
           for (int k8 = 0; k8 < 4; ++k8) {
@@ -446,13 +460,13 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         }
       }
       if (bad || !(most < MAX_HALF)) sm.bad[n & 1] = 1;
-      cp_async_wait();
       fence_async_smem();
       named_sync(2, PREP);
       if (t == 0 && ok) mbar_arrive(&sm.full[n & 1]);
     }
   } else {
     // ----------------------------------------------------------- chain
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CHAIN_REGS));
     // A thread has rows 64 half .. of its column of the state, and rows 32 half ..
     // of a chunk.
     constexpr int SD = MAX_DK / 2, SC = C / 2;
@@ -461,19 +475,11 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
     const int col = slice * LANES + l;
     const bool have = col < p.Dv;
     const uint32_t me = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // the state to tensor memory; `back`: what its numbers there are times
-    float back = 1.f;
+    float s[SD];
     {
       const float *from = p.s + (((int64_t)q.src * p.Hv + h) * p.Dk + d0) * p.Dv + col;
-      const bool some = q.ok && q.src >= 0 && have;
-#pragma unroll 1
-      for (int d = 0; d < SD; d += 16) {
-        uint32_t x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = some && d0 + d + e < p.Dk ? __float_as_uint(from[(int64_t)(d + e) * p.Dv]) : 0u;
-        tmem_st16(me + TM_S + d0 + d, x);
-      }
-      tmem_wait_st();
+      for (int d = 0; d < SD; ++d) s[d] = q.ok && q.src >= 0 && have && d0 + d < p.Dk ? from[(int64_t)d * p.Dv] : 0.f;
     }
     if (!q.ok && tid == 0) report(p.status, MFD_ERR_INPUT);
     {  // rows that are not live
@@ -482,22 +488,31 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         for (int i = nn + (tid >> 4); i < p.N; i += CHAIN / 16)
           st_global16(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + slice * LANES + ch * 8, make_uint4(0, 0, 0, 0));
     }
-    bool slow = false;
     int pending = -1;  // chunk whose outputs wait in tensor memory
     float out_scale = 0.f;
+    auto arrive = [&](uint64_t *bar) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(bar);
+    };
     // Outputs of that chunk: scale s_i times what the products gave, through shared
     // memory for whole 16 bytes (two bytes a lane took 6,000 cycles a chunk).
-    auto put_outputs = [&]() {
-      if (pending < 0) return;
+    // `next`: the products of the chunk after may go over them once they are read.
+    auto put_outputs = [&](bool next) {
+      if (pending < 0) {
+        if (next) arrive(&sm.pq);
+        return;
+      }
       wait_warp(&sm.o, pending & 1u);
       const float *fq = sm.fq[pending % 3];
       if (ok) {
         tc_fence_after();
         uint32_t x[SC];
-        tmem_ld32(me + TM_XQ + (pending & 1) * C + i0, x);
+        tmem_ld32(me + TM_XQ + i0, x);
         tmem_wait_ld();
         tie32(x);
-        tc_fence_before();
+        if (next) arrive(&sm.pq);
         // all that is read before all that is written: a load does not pass a store
 #pragma unroll
         for (int i = 0; i < SC; ++i) x[i] = pack2<T>(__uint_as_float(x[i]) * out_scale * fq[i0 + i], 0.f);
@@ -523,14 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       named_sync(5 + (warp & 3), 64);
       return max_nan(x, sm.top[which][half ^ 1][l], 0.f);
     };
-    auto arrive = [&](uint64_t *bar) {
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(bar);
-    };
-
-    constexpr uint32_t id = idesc_16<__half>(128, C, false), id_kd = idesc_16<__half>(128, 128, true);
+    constexpr uint32_t id = idesc_16<__half>(128, C, false), id_t = idesc_16<T>(128, C, false), id_kd = idesc_16<T>(128, 128, true);
     const int steps = p.Dk / 16;
     // Products: one lane of warp `who` issues them once all of the chain's warps have
     // arrived; a warp for each kind, so that none is held up for long.
@@ -546,89 +554,95 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
 
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
-      const uint32_t xq = me + TM_XQ + (n & 1) * C + i0;
+      const uint32_t xq = me + TM_XQ + i0;
       const uint32_t par = n & 1u;
       bool bad = false;
       // the state's halves; the updates' of the chunk before, which they go over, have
       // been read with its outputs
       if (pending >= 0) wait_warp(&sm.o, pending & 1u);
       tc_fence_after();
-      float top = 0.f;
-      if (ok)
-#pragma unroll 1
-        for (int d = 0; d < SD; d += 32) {
-          uint32_t x[32];
-          tmem_ld32(me + TM_S + d0 + d, x);
-          tmem_wait_ld();
-          tie32(x);
+      float top = 0.f, back_s = 1.f;  // back_s: S^T K^T to true numbers
+      if (BF16) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) top = max_nan(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        for (int d = 0; d < SD; d += 16) {
+          uint32_t x[8], y[8], z[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) thirds(s[d + 2 * e], s[d + 2 * e + 1], x[e], y[e], z[e]);
+          if (ok) {
+            tmem_st8(me + TM_H + (d0 + d) / 2, x);
+            tmem_st8(me + TM_H + 64 + (d0 + d) / 2, y);
+            tmem_st8(me + TM_H + 128 + (d0 + d) / 2, z);
+          }
         }
-      top = of_both(0, top);
-      const bool was_finite = finite(top);  // a column that is not has nothing more to lose
-      float down;  // of the halves, to the state's numbers in tensor memory
-      const float up = power_for(top, 11, down);
-      if (ok) {
-        const uint64_t up2 = pair(up, up);
-#pragma unroll 1
-        for (int d = 0; d < SD; d += 32) {
-          uint32_t x[32], hi[16], lo[16];
-          tmem_ld32(me + TM_S + d0 + d, x);
-          tmem_wait_ld();
-          tie32(x);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            halves_at(pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), up2, hi[e], lo[e]);
-          tmem_st16(me + TM_H + (d0 + d) / 2, hi);
-          tmem_st16(me + TM_H + 64 + (d0 + d) / 2, lo);
+        for (int d = 0; d < SD; d += 2) top = max_nan(top, s[d], s[d + 1]);
+        top = of_both(0, top);
+        const float up = power_for(top, 11, back_s);
+        const uint64_t up2 = pair(up, up);
+#pragma unroll
+        for (int d = 0; d < SD; d += 16) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) halves_at(pair(s[d + 2 * e], s[d + 2 * e + 1]), up2, hi[e], lo[e]);
+          if (ok) {
+            tmem_st8(me + TM_H + (d0 + d) / 2, hi);
+            tmem_st8(me + TM_H + 64 + (d0 + d) / 2, lo);
+          }
         }
       }
-      const float back_s = down * back;  // of S^T K^T to true numbers
       arrive(&sm.ps);
       wait_warp(&sm.full[n & 1], (n >> 1) & 1u);
       products(0, &sm.ps, par, [&]() {  // S^T K^T, then S^T Q^T
         const uint32_t kq = desc_lo(smem_u32(st.kq), 16);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 8 * PARTS; ++k)
           if ((k & 7) < steps)
-            mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, kq + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id, k != 0);
+            mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, kq + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id_t, k != 0);
         tc_commit(&sm.x);
       });
-      // by another warp, behind the first: issuing them takes as long as they run
-      products(4, &sm.x, par, [&]() {
-        const uint32_t kq = desc_lo(smem_u32(st.kq), 16), d = tmem + TM_XQ + (n & 1) * C;
+      put_outputs(true);
+      // by another warp: issuing them takes as long as they run
+      if (warp == 4) wait_warp(&sm.ps, par);
+      products(4, &sm.pq, par, [&]() {
+        const uint32_t kq = desc_lo(smem_u32(st.kq), 16);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 8 * PARTS; ++k)
           if ((k & 7) < steps)
-            mma_ts(d, tmem + TM_H + k * 8, kq + (C * 128 >> 4) + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id, k != 0);
+            mma_ts(tmem + TM_XQ, tmem + TM_H + k * 8, kq + (C * 128 >> 4) + ((k & 7) >> 2) * (BLOCK >> 4) + (k & 3) * 2, id_t, k != 0);
         tc_commit(&sm.xq);
       });
-      put_outputs();
       // right sides
       wait_warp(&sm.x, par);
       tc_fence_after();
-      float b[SC];
-      {
-        uint32_t x[SC];
+      float b[SC], x_top = 0.f;
 #pragma unroll
-        for (int i = 0; i < SC; ++i) x[i] = 0u;
+      for (int part = 0; part < SC; part += 16) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0u;
         if (ok) {
-          tmem_ld32(me + TM_XK + i0, x);
+          tmem_ld16(me + TM_XK + i0 + part, x);
           tmem_wait_ld();
-          tie32(x);
+          tie16(x);
         }
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
-          const float2 f = st.c.rhs[i0 + i];
-          const float v = to_float<T>(st.v[(i0 + i) * LANES + l]);
-          b[i] = fmaf(f.y, __uint_as_float(x[i]) * back_s, f.x * v);
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = st.c.rhs[i0 + part + i];
+          const float v = to_float<T>(st.v[(i0 + part + i) * LANES + l]);
+          b[part + i] = fmaf(f.y, BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_s, f.x * v);
         }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) x_top = max_nan(x_top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       }
       top = 0.f;
 #pragma unroll
       for (int i = 0; i < SC; i += 2) top = max_nan(top, b[i], b[i + 1]);
+      // A column of the state that is not finite has nothing more to lose; one that leaves
+      // the outputs' common scale no room goes row by row too.
+      const bool had = finite(x_top);
+      if (had && (!finite(top) || x_top * back_s > 0x1p60f)) bad = true;
       top = of_both(1, top);
-      if (!finite(top) && was_finite) bad = true;
       float back_b;
       float up_b = power_for(top, 11, back_b);
       if (back_b < back_s * 0x1p-60f) {  // nothing to add: the outputs' common scale stays near the state's
@@ -639,12 +653,15 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       tc_fence_after();
       {
         const uint64_t up = pair(up_b, up_b);
-        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) halves_at(pair(b[2 * e], b[2 * e + 1]), up, hi[e], lo[e]);
-        if (ok) {
-          tmem_st16(me + TM_H + i0 / 2, hi);
-          tmem_st16(me + TM_H + 32 + i0 / 2, lo);
+        for (int i = 0; i < SC; i += 16) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) halves_at(pair(b[i + 2 * e], b[i + 2 * e + 1]), up, hi[e], lo[e]);
+          if (ok) {
+            tmem_st8(me + TM_H + (i0 + i) / 2, hi);
+            tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
+          }
         }
       }
       arrive(&sm.pb);
@@ -661,80 +678,78 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       back_b *= 8.f;
       if (ok) {
         const float f = up_b * back_s;
-        uint32_t x[SC];
-        tmem_ld32(xq, x);
-        tmem_wait_ld();
-        tie32(x);
 #pragma unroll
-        for (int i = 0; i < SC; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * (f * st.c.ec[i0 + i]));
-        tmem_st16(xq, x);
-        tmem_st16(xq + 16, x + 16);
-      }
-      // and the state, decayed
-      if (ok) {
-        const float f = st.c.ec[C - 1] * (up_b * back);
-#pragma unroll 1
-        for (int d = 0; d < SD; d += 32) {
-          uint32_t x[32];
-          tmem_ld32(me + TM_S + d0 + d, x);
+        for (int part = 0; part < SC; part += 16) {
+          uint32_t x[16];
+          tmem_ld16(xq + part, x);
           tmem_wait_ld();
-          tie32(x);
+          tie16(x);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-          tmem_st16(me + TM_S + d0 + d, x);
-          tmem_st16(me + TM_S + d0 + d + 16, x + 16);
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * (f * st.c.eq[i0 + part + i]));
+          tmem_st16(xq + part, x);
         }
       }
-      back = back_b;
       // the updates
       wait_warp(&sm.u, par);
       if (ok) {
         tc_fence_after();
-        uint32_t x[SC];
-        tmem_ld32(me + TM_XK + i0, x);
-        tmem_wait_ld();
-        tie32(x);
 #pragma unroll
-        for (int i = 0; i < SC; ++i) b[i] = __uint_as_float(x[i]) * 0.125f;
+        for (int part = 0; part < SC; part += 16) {
+          uint32_t x[16];
+          tmem_ld16(me + TM_XK + i0 + part, x);
+          tmem_wait_ld();
+          tie16(x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) b[part + i] = __uint_as_float(x[i]) * 0.125f;
+        }
       }
       float most = 0.f;
-      {
-        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + 2 * e]);
-          const float z0 = b[2 * e] * f.x, z1 = b[2 * e + 1] * f.y;
-          most = max_nan(most, z0, z1);
-          most = max_nan(most, b[2 * e], b[2 * e + 1]);
-          halves(z0, z1, hi[e], lo[e]);
+      for (int e = 0; e < SC; e += 2) most = max_nan(most, b[e], b[e + 1]);
+#pragma unroll
+      for (int i = 0; i < SC; i += 16) {
+        uint32_t x[8], y[8], z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + i + 2 * e]);
+          if (BF16) {
+            thirds(b[i + 2 * e] * back_b * f.x, b[i + 2 * e + 1] * back_b * f.y, x[e], y[e], z[e]);
+          } else {
+            const float z0 = b[i + 2 * e] * f.x, z1 = b[i + 2 * e + 1] * f.y;
+            most = max_nan(most, z0, z1);
+            halves(z0, z1, x[e], y[e]);
+          }
         }
         if (ok) {
-          tmem_st16(me + TM_Z + i0 / 2, hi);
-          tmem_st16(me + TM_Z + 32 + i0 / 2, lo);
+          tmem_st8(me + TM_Z + (i0 + i) / 2, x);
+          tmem_st8(me + TM_Z + 32 + (i0 + i) / 2, y);
+          if (BF16) tmem_st8(me + TM_Z + 64 + (i0 + i) / 2, z);
         }
       }
-      if (bad || (was_finite && !(most < MAX_HALF))) *(volatile int *)&sm.chain_bad = n + 1;
+      if (bad || (had && !(most < MAX_HALF))) *(volatile int *)&sm.chain_bad = n + 1;
       arrive(&sm.pz);
       products(2, &sm.pz, par, [&]() {
         const uint32_t kd = desc_lo(smem_u32(st.kq), BLOCK);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts(tmem + TM_S, tmem + TM_Z + k * 8, kd + (k & 3) * (2048 >> 4), id_kd, 1);
+        for (int k = 0; k < 4 * PARTS; ++k) mma_ts(tmem + TM_S, tmem + TM_Z + k * 8, kd + (k & 3) * (2048 >> 4), id_kd, k != 0);
         tc_commit(&sm.s);
         tc_commit(&sm.empty[n & 1]);
       });
-      {
-        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) halves(b[2 * e], b[2 * e + 1], hi[e], lo[e]);
+      for (int i = 0; i < SC; i += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) halves(b[i + 2 * e], b[i + 2 * e + 1], hi[e], lo[e]);
         if (ok) {
-          tmem_st16(me + TM_H + i0 / 2, hi);
-          tmem_st16(me + TM_H + 32 + i0 / 2, lo);
+          tmem_st8(me + TM_H + (i0 + i) / 2, hi);
+          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
         }
       }
       const bool slow_prep = *(volatile int *)&sm.bad[n & 1] != 0;
+      const float end = st.c.end;
       arrive(&sm.py);
       products(3, &sm.py, par, [&]() {
-        const uint32_t ph = desc_lo(smem_u32(st.ph), 16), pl = desc_lo(smem_u32(st.pl), 16), d = tmem + TM_XQ + (n & 1) * C;
+        const uint32_t ph = desc_lo(smem_u32(st.ph), 16), pl = desc_lo(smem_u32(st.pl), 16), d = tmem + TM_XQ;
 #pragma unroll
         for (int k = 0; k < 8; ++k) mma_ts(d, tmem + TM_H + k * 8, ph + (k & 3) * 2, id, 1);
 #pragma unroll
@@ -743,27 +758,32 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tc_commit(&sm.empty[n & 1]);  // with the state's step the last to read this stage
       });
       wait_warp(&sm.s, par);
-      if (slow_prep || *(volatile int *)&sm.chain_bad == n + 1) {
-        wait_warp(&sm.o, par);  // its outputs are not wanted, and no product runs on
-        slow = true;
-        break;
-      }
-      pending = n;
-      out_scale = back_b;
-    }
-    if (slow) {
-      // The prep goes through the rest of its loop without waiting or touching
-      // anything.  All rows again, from the inputs and the state, which is not written
-      // before the end; as delta_rows.cu does it, the column's two threads exchanging
-      // their sums.
-      *abort_flag = 1;
-      float s[SD];
-      const float *from = p.s + (((int64_t)q.src * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+      if (!slow_prep && *(volatile int *)&sm.chain_bad != n + 1) {
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-      for (int d = 0; d < SD; ++d) s[d] = q.src >= 0 && have && d0 + d < p.Dk ? from[(int64_t)d * p.Dv] : 0.f;
+          for (int part = 0; part < SD; part += 16) {
+            uint32_t x[16];
+            tmem_ld16(me + TM_S + d0 + part, x);
+            tmem_wait_ld();
+            tie16(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s[part + i] = fmaf(s[part + i], end, BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_b);
+          }
+          tc_fence_before();
+        }
+        pending = n;
+        out_scale = back_b;
+        continue;
+      }
+      // The chunk row by row, from the inputs, as delta_rows.cu does it; the column's two
+      // threads exchange their sums.
+      wait_warp(&sm.o, par);  // its outputs are not wanted
+      const int rows = min(C, nn - n * C);
 #pragma unroll 1
-      for (int i = 0; i < nn; ++i) {
-        const int64_t tok = tok0 + i;
+      for (int i = 0; i < rows; ++i) {
+        const int64_t tok = tok0 + n * C + i;
         const uint4 *kr = reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride + hk * p.Dk);
         const uint4 *qr = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + hk * p.Dk);
         float fk = 1.f, fq = 1.f, x[8], y[8];
@@ -820,28 +840,13 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (have && half == 0)
           p.out[(tok * p.Hv + h) * p.Dv + col] = (uint16_t)pack2<T>(p.scale * fmaf(kq, u, decay * qs), 0.f);
       }
-      if (ok && q.dst >= 0 && have) {
-        float *to = p.s + (((int64_t)q.dst * p.Hv + h) * p.Dk + d0) * p.Dv + col;
+    }
+    put_outputs(false);
+    if (ok && q.ok && q.dst >= 0 && have) {
+      float *to = p.s + (((int64_t)q.dst * p.Hv + h) * p.Dk + d0) * p.Dv + col;
 #pragma unroll
-        for (int d = 0; d < SD; ++d)
-          if (d0 + d < p.Dk) to[(int64_t)d * p.Dv] = s[d];
-      }
-    } else {
-      put_outputs();
-      if (ok && q.ok && q.dst >= 0) {
-        float *to = p.s + (((int64_t)q.dst * p.Hv + h) * p.Dk + d0) * p.Dv + col;
-        tc_fence_after();
-#pragma unroll 1
-        for (int d = 0; d < SD; d += 16) {
-          uint32_t x[16];
-          tmem_ld16(me + TM_S + d0 + d, x);
-          tmem_wait_ld();
-          tie16(x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (have && d0 + d + e < p.Dk) to[(int64_t)(d + e) * p.Dv] = __uint_as_float(x[e]) * back;
-        }
-      }
+      for (int d = 0; d < SD; ++d)
+        if (d0 + d < p.Dk) to[(int64_t)d * p.Dv] = s[d];
     }
   }
   // no product runs on when tensor memory is given back
@@ -868,6 +873,10 @@ cudaError_t launch_type(const DeltaArgs &A, cudaStream_t stream) {
   if (dev > 63 || !((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
     if ((e = cudaFuncSetAttribute(delta_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) != cudaSuccess)
       return e;
+    // the roles' exchange of registers waits for what a block is launched with
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, delta_chunk_kernel<T>)) != cudaSuccess) return e;
+    if ((at.numRegs + 7) / 8 * 8 != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
     if (dev < 64) ready.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
   }
   const int slices = (A.Dv + LANES - 1) / LANES;
