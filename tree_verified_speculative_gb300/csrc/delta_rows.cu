@@ -70,6 +70,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
     for (int t = 0; t < PER; ++t)
       S[t] = ok && src >= 0 && have && t < per ? *reinterpret_cast<const float4 *>(from + (int64_t)t * p.Dv) : make_float4(0, 0, 0, 0);
   }
+  if (per < PER) {  // narrower keys leave elements between the groups': zeros, like the state's rows there
+    for (int i = tid; i < BATCH * MAX_DK; i += WARPS * 32) reinterpret_cast<float *>(k_s)[i] = 0.f;
+    for (int i = tid; i < (MODE == COMMIT ? 1 : BATCH) * MAX_DK; i += WARPS * 32) reinterpret_cast<float *>(q_s)[i] = 0.f;
+    block_sync();
+  }
   const int64_t tok0 = (int64_t)r * p.N;
   int rows = nn;
   if (MODE == COMMIT) {
@@ -97,6 +102,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
       *reinterpret_cast<uint2 *>(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col) = make_uint2(0, 0);
   if (!ok) return;
 
+  // The state is S times `kept`, the product of the decays since it was last multiplied
+  // out: a row then costs two products an element, not three.
+  float kept = 1.f;
   for (int first = 0; first < rows; first += BATCH) {
     const int n = min(BATCH, rows - first);
     if (first) block_sync();
@@ -155,37 +163,41 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
       float4 a = make_float4(0, 0, 0, 0), b = a;
       const float4 *kv = k_s[i] + group * (PER / 4), *qv = q_s[MODE == COMMIT ? 0 : i] + group * (PER / 4);
 #pragma unroll
-      for (int t = 0; t < PER; t += 4)
-        if (t < per) {
-          const float4 k = kv[t / 4];
-          a = fma4(k.x, S[t], a);
-          if (t + 1 < per) a = fma4(k.y, S[t + 1], a);
-          if (t + 2 < per) a = fma4(k.z, S[t + 2], a);
-          if (t + 3 < per) a = fma4(k.w, S[t + 3], a);
-          if (MODE != COMMIT) {
-            const float4 q = qv[t / 4];
-            b = fma4(q.x, S[t], b);
-            if (t + 1 < per) b = fma4(q.y, S[t + 1], b);
-            if (t + 2 < per) b = fma4(q.z, S[t + 2], b);
-            if (t + 3 < per) b = fma4(q.w, S[t + 3], b);
-          }
+      for (int t = 0; t < PER; t += 4) {
+        const float4 k = kv[t / 4];
+        a = fma4(k.x, S[t], a);
+        a = fma4(k.y, S[t + 1], a);
+        a = fma4(k.z, S[t + 2], a);
+        a = fma4(k.w, S[t + 3], a);
+        if (MODE != COMMIT) {
+          const float4 q = qv[t / 4];
+          b = fma4(q.x, S[t], b);
+          b = fma4(q.y, S[t + 1], b);
+          b = fma4(q.z, S[t + 2], b);
+          b = fma4(q.w, S[t + 3], b);
         }
+      }
       a = group_sum(a);
       if (MODE != COMMIT) b = group_sum(b);
-      const float d = decay_s[i], beta = beta_s[i];
+      const float d = decay_s[i] * kept, beta = beta_s[i];
       const float4 u = make_float4(beta * fmaf(-d, a.x, v.x), beta * fmaf(-d, a.y, v.y), beta * fmaf(-d, a.z, v.z),
                                    beta * fmaf(-d, a.w, v.w));
+      kept = d;
+      if (!(d > 0x1p-40f && d < 0x1p40f)) {  // too small to divide by, or NaN
 #pragma unroll
-      for (int t = 0; t < PER; t += 4)
-        if (t < per) {
-          const float4 k = kv[t / 4];
-          const float kk[4] = {k.x, k.y, k.z, k.w};
+        for (int t = 0; t < PER; ++t) S[t] = make_float4(d * S[t].x, d * S[t].y, d * S[t].z, d * S[t].w);
+        kept = 1.f;
+      }
+      const float up = 1.f / kept;
+      const float4 w = make_float4(u.x * up, u.y * up, u.z * up, u.w * up);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (t + e < per)
-              S[t + e] = make_float4(fmaf(kk[e], u.x, d * S[t + e].x), fmaf(kk[e], u.y, d * S[t + e].y), fmaf(kk[e], u.z, d * S[t + e].z),
-                                     fmaf(kk[e], u.w, d * S[t + e].w));
-        }
+      for (int t = 0; t < PER; t += 4) {
+        const float4 k = kv[t / 4];
+        S[t] = fma4(k.x, w, S[t]);
+        S[t + 1] = fma4(k.y, w, S[t + 1]);
+        S[t + 2] = fma4(k.z, w, S[t + 2]);
+        S[t + 3] = fma4(k.w, w, S[t + 3]);
+      }
       if (MODE != COMMIT && group == 0 && have) {
         const float qk = qk_s[i];
         *reinterpret_cast<uint2 *>(p.out + ((tok0 + first + i) * p.Hv + h) * p.Dv + col) =
@@ -198,7 +210,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
     float *to = p.s + (((int64_t)dst * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
 #pragma unroll
     for (int t = 0; t < PER; ++t)
-      if (t < per) *reinterpret_cast<float4 *>(to + (int64_t)t * p.Dv) = S[t];
+      if (t < per)
+        *reinterpret_cast<float4 *>(to + (int64_t)t * p.Dv) = make_float4(kept * S[t].x, kept * S[t].y, kept * S[t].z, kept * S[t].w);
   }
 }
 
