@@ -34,7 +34,7 @@ constexpr int DELTA_MAX_DEPTH = 16;   // of a tree's nodes, the root's being 0
 constexpr int DELTA_MAX_NODES = 513;
 
 // Rows from which the chunked form is the faster one.
-constexpr int DELTA_CHUNK_FROM = 24;
+constexpr int DELTA_CHUNK_FROM = 18;
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaArgs &A, cudaStream_t stream);
 cudaError_t launch_delta_commit(const DeltaArgs &A, int n_sm, cudaStream_t stream);

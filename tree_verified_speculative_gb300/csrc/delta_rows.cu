@@ -11,9 +11,10 @@
 //   u = beta (v - e^g kS),  o = scale (e^g qS + (q . k) u),
 //
 // three exchanges between the groups serve a row, and warps do not wait for each
-// other: a block's warps share the rows' vectors, BATCH of them at a time.  (With
-// the groups in different warps and a barrier for each row, 32 accepted paths took
-// 48 us.)
+// other: a block's warps share the rows' vectors.  A block walks (request, head,
+// slice) items.  While it works on one, the next one's path is read, then its
+// rows' vectors go to shared memory and its state to L2, so that only the state's
+// way from there is waited for.
 #include "delta.h"
 #include "kvcache.h"
 #include "mfd_device.cuh"
@@ -22,7 +23,8 @@ namespace mfd {
 namespace {
 
 constexpr int COLS = 16;     // of a warp
-constexpr int BATCH = 17;    // rows whose vectors are in shared memory at once: all of a path
+constexpr int BATCH = DELTA_MAX_DEPTH + 1;  // rows at most: all of a path
+static_assert(BATCH >= DELTA_CHUNK_FROM - 1, "rows of the rule");
 constexpr int MAX_DK = 128;
 constexpr int PER = MAX_DK / 8;  // rows of the state a lane holds
 
@@ -43,85 +45,118 @@ __device__ __forceinline__ float4 group_sum(float4 v) {
   return v;
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <typename T, int WARPS, int MODE>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(const DeltaArgs p, int slices) {
-  constexpr int W = WARPS * COLS;
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(const DeltaArgs p, int slices, int items) {
+  constexpr int W = WARPS * COLS, THREADS = WARPS * 32, VECS = MODE == COMMIT ? 1 : 2;
   __shared__ float4 k_s[BATCH][MAX_DK / 4], q_s[MODE == COMMIT ? 1 : BATCH][MAX_DK / 4];
-  __shared__ uint4 v_s[BATCH][W / 8];
-  __shared__ float decay_s[BATCH], beta_s[BATCH], qk_s[BATCH];
-  __shared__ int row_s[BATCH], bad_s;
+  __shared__ uint4 raw_s[2][BATCH][VECS][MAX_DK / 8], v_s[2][BATCH][W / 8];  // as they are, of this item and the next
+  __shared__ float g_s[2][BATCH], b_s[2][BATCH], decay_s[BATCH], beta_s[BATCH], qk_s[BATCH];
+  __shared__ int row_s[2][BATCH], bad_s[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.Hv, r = blockIdx.x / slices / p.Hv;
-  const int group = lane >> 2, col = slice * W + warp * COLS + (lane & 3) * 4;
-  const bool have = col < p.Dv;
-  const int hk = h / (p.Hv / p.Hk), per = p.Dk / 8;  // rows of a group: even
+  const int group = lane >> 2, per = p.Dk / 8;  // rows of a group
   pdl_launch_dependents();
   pdl_wait();
-
-  // lengths and slots; a request whose numbers are wrong has no rows and keeps no state
-  int nn = p.n_nodes ? __ldg(p.n_nodes + r) : p.N;
-  const int src = p.src ? __ldg(p.src + r) : r;
-  const int dst = p.dst ? __ldg(p.dst + r) : src;
-  bool ok = nn >= 0 && nn <= p.N && src >= -1 && src < p.n_slots && dst >= -1 && dst < p.n_slots;
-  float4 S[PER];
-  {
-    const float *from = p.s + (((int64_t)src * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
-#pragma unroll
-    for (int t = 0; t < PER; ++t)
-      S[t] = ok && src >= 0 && have && t < per ? *reinterpret_cast<const float4 *>(from + (int64_t)t * p.Dv) : make_float4(0, 0, 0, 0);
-  }
+  if (tid < 2) bad_s[tid] = 0;
   if (per < PER) {  // narrower keys leave elements between the groups': zeros, like the state's rows there
-    for (int i = tid; i < BATCH * MAX_DK; i += WARPS * 32) reinterpret_cast<float *>(k_s)[i] = 0.f;
-    for (int i = tid; i < (MODE == COMMIT ? 1 : BATCH) * MAX_DK; i += WARPS * 32) reinterpret_cast<float *>(q_s)[i] = 0.f;
-    block_sync();
+    for (int i = tid; i < BATCH * MAX_DK; i += THREADS) reinterpret_cast<float *>(k_s)[i] = 0.f;
+    for (int i = tid; i < (MODE == COMMIT ? 1 : BATCH) * MAX_DK; i += THREADS) reinterpret_cast<float *>(q_s)[i] = 0.f;
   }
-  const int64_t tok0 = (int64_t)r * p.N;
-  int rows = nn;
-  if (MODE == COMMIT) {
-    if (tid == 0) bad_s = 0;
-    block_sync();
-    rows = ok ? __ldg(p.accept_len + r) + 1 : 0;
-    if (rows < 1 || rows > p.L + 1) ok = false;
-    const int32_t *path = p.path + (int64_t)r * (p.L + 1);
-    if (ok && tid < rows) {
-      const int node = __ldg(path + tid);
-      const bool good = node < nn && (tid == 0 ? node == 0 : node > __ldg(path + tid - 1));
-      if (!good) bad_s = 1;
-      row_s[tid] = node;
+  struct Item {
+    int slice, h, r, nn, src, dst, rows;
+    int node;  // of the path, thread's
+  };
+  // What a request says of itself, not looked at yet.
+  auto read = [&](int item) {
+    Item x;
+    x.slice = item % slices;
+    x.h = item / slices % p.Hv;
+    x.r = item / slices / p.Hv;
+    x.nn = p.n_nodes ? __ldg(p.n_nodes + x.r) : p.N;
+    x.src = p.src ? __ldg(p.src + x.r) : x.r;
+    x.dst = p.dst ? __ldg(p.dst + x.r) : x.src;
+    x.rows = MODE == COMMIT ? __ldg(p.accept_len + x.r) : 0;
+    x.node = MODE == COMMIT && tid <= p.L ? __ldg(p.path + (int64_t)x.r * (p.L + 1) + tid) : 0;
+    return x;
+  };
+  // Looks at it, by all threads: false where numbers are wrong; the path's nodes are
+  // judged by their threads, and known after a barrier.
+  auto check = [&](Item &x, int buf) {
+    const bool ok = x.nn >= 0 && x.nn <= p.N && x.src >= -1 && x.src < p.n_slots && x.dst >= -1 && x.dst < p.n_slots &&
+                    (MODE == RULE || (x.rows >= 0 && x.rows <= p.L));
+    x.rows = !ok ? -1 : MODE == COMMIT ? x.rows + 1 : x.nn;
+    if (MODE == COMMIT && tid < 32) {
+      const int before = __shfl_up_sync(0xffffffffu, x.node, 1);
+      if (tid < x.rows) {
+        if (x.node >= x.nn || (tid == 0 ? x.node != 0 : x.node <= before)) bad_s[buf] = 1;
+        row_s[buf][tid] = x.node;
+      }
     }
-    block_sync();
-    if (bad_s) ok = false;
-  }
-  if (!ok) {
-    if (tid == 0) report(p.status, MFD_ERR_INPUT);
-    rows = nn = 0;
-  }
-  // rows that are not live
-  if (MODE == RULE && have)
-    for (int i = nn + group; i < p.N; i += 8)
-      *reinterpret_cast<uint2 *>(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col) = make_uint2(0, 0);
-  if (!ok) return;
+  };
+  // Its rows' vectors on their way to buffer `buf`, its state's to L2.
+  auto fetch = [&](const Item &x, int buf, bool state) {
+    const int hk = x.h / (p.Hv / p.Hk), n = x.rows, at0 = x.slice * W;
+    const int64_t tok0 = (int64_t)x.r * p.N;
+    auto token = [&](int i) { return tok0 + (MODE == COMMIT ? row_s[buf][i] : i); };
+    for (int i = tid; i < n * VECS * (MAX_DK / 8); i += THREADS) {
+      const int c = i % (MAX_DK / 8), vec = i / (MAX_DK / 8) % VECS, row = i / (MAX_DK / 8) / VECS;
+      if (c * 8 < p.Dk)
+        cp_async16(&raw_s[buf][row][vec][c], (vec ? p.q + token(row) * p.q_stride : p.k + token(row) * p.k_stride) + hk * p.Dk + c * 8);
+    }
+    for (int i = tid; i < n * (W / 8); i += THREADS) {
+      const int row = i / (W / 8), c = i % (W / 8);
+      if (at0 + c * 8 < p.Dv) cp_async16(&v_s[buf][row][c], p.v + token(row) * p.v_stride + x.h * p.Dv + at0 + c * 8);
+    }
+    if (tid < n) {
+      cp_async4(&g_s[buf][tid], p.g + token(tid) * p.Hv + x.h);
+      cp_async4(&b_s[buf][tid], p.beta + token(tid) * p.Hv + x.h);
+    }
+    if (state && x.src >= 0)
+      for (int i = tid; i < p.Dk; i += THREADS)
+        bulk_prefetch_l2(p.s + (((int64_t)x.src * p.Hv + x.h) * p.Dk + i) * p.Dv + at0, (uint32_t)min(W, p.Dv - at0) * 4);
+  };
 
-  // The state is S times `kept`, the product of the decays since it was last multiplied
-  // out: a row then costs two products an element, not three.
-  float kept = 1.f;
-  for (int first = 0; first < rows; first += BATCH) {
-    const int n = min(BATCH, rows - first);
-    if (first) block_sync();
-    for (int i = tid; i < n * (W / 8); i += WARPS * 32) {
-      const int row = i / (W / 8), c = i % (W / 8), at = slice * W + c * 8;
-      const int64_t tok = tok0 + (MODE == COMMIT ? row_s[row] : first + row);
-      if (at < p.Dv) v_s[row][c] = __ldg(reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride + h * p.Dv + at));
+  int buf = 0;
+  Item x = read(blockIdx.x);
+  block_sync();
+  check(x, 0);
+  block_sync();
+  if (bad_s[0]) x.rows = -1;
+  if (x.rows > 0) fetch(x, 0, false);
+  for (int item = blockIdx.x; item < items; buf ^= 1) {
+    const int n = max(x.rows, 0), h = x.h, slice = x.slice;
+    const int col = slice * W + warp * COLS + (lane & 3) * 4;
+    const bool have = col < p.Dv;
+    const int64_t tok0 = (int64_t)x.r * p.N;
+    float4 S[PER];
+    {
+      const float *from = p.s + (((int64_t)x.src * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
+#pragma unroll
+      for (int t = 0; t < PER; ++t)
+        S[t] = x.rows >= 0 && x.src >= 0 && have && t < per ? *reinterpret_cast<const float4 *>(from + (int64_t)t * p.Dv)
+                                                            : make_float4(0, 0, 0, 0);
     }
+    const int next = item + gridDim.x;
+    Item y = x;
+    if (next < items) y = read(next);
+    if (x.rows < 0 && tid == 0) report(p.status, MFD_ERR_INPUT);
+    // rows that are not live
+    if (MODE == RULE && have)
+      for (int i = n + group; i < p.N; i += 8)
+        *reinterpret_cast<uint2 *>(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col) = make_uint2(0, 0);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    block_sync();
     // half a warp for a key, half for a query
     for (int i = warp; i < n; i += WARPS) {
-      const int64_t tok = tok0 + (MODE == COMMIT ? row_s[i] : first + i);
-      const int c = lane & 15;
-      const bool is_q = lane >= 16;
+      const int c = lane & 15, vec = lane >> 4;
       uint4 raw = make_uint4(0, 0, 0, 0);
-      if (c * 8 < p.Dk && (!is_q || MODE != COMMIT))
-        raw = __ldg(reinterpret_cast<const uint4 *>((is_q ? p.q + tok * p.q_stride : p.k + tok * p.k_stride) + hk * p.Dk + c * 8));
-      const float g = __ldg(p.g + tok * p.Hv + h), b = __ldg(p.beta + tok * p.Hv + h);
+      if (c * 8 < p.Dk && vec < VECS) raw = raw_s[buf][i][vec & (VECS - 1)][c];
       float x[8], ss = 0.f, qk = 0.f;
       unpack8<T>(raw, x);
 #pragma unroll
@@ -139,25 +174,40 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) qk += __shfl_xor_sync(0xffffffffu, qk, o);
       }
-      if (!is_q || MODE != COMMIT) {
+      if (vec < VECS) {
         // element e of the vector is element e % per of group e / per; rows of groups are
         // PER floats apart in shared memory, whatever Dk is
-        float *to = reinterpret_cast<float *>(is_q ? q_s[i] : k_s[i]);
+        float *to = reinterpret_cast<float *>(vec ? q_s[MODE == COMMIT ? 0 : i] : k_s[i]);
+        if (per == PER) {
+          *reinterpret_cast<float4 *>(to + c * 8) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4 *>(to + c * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const int at = c * 8 + e;
-          if (at < p.Dk) *reinterpret_cast<float2 *>(to + at / per * PER + at % per) = make_float2(x[e], x[e + 1]);
+          for (int e = 0; e < 8; e += 2) {
+            const int at = c * 8 + e;
+            if (at < p.Dk) *reinterpret_cast<float2 *>(to + at / per * PER + at % per) = make_float2(x[e], x[e + 1]);
+          }
         }
       }
       if (lane == 0) {
-        decay_s[i] = expf(g);
-        beta_s[i] = b;
+        decay_s[i] = expf(g_s[buf][i]);
+        beta_s[i] = b_s[buf][i];
         qk_s[i] = qk;
       }
     }
+    if (tid == 0) bad_s[buf] = 0;  // looked at; the next but one's
+    if (next < items) check(y, buf ^ 1);
     block_sync();
+    if (next < items) {
+      if (bad_s[buf ^ 1]) y.rows = -1;
+      if (y.rows > 0) fetch(y, buf ^ 1, true);
+    }
+
+    // The state is S times `kept`, the product of the decays since it was last multiplied
+    // out: a row then costs two products an element, not three.
+    float kept = 1.f;
     for (int i = 0; i < n; ++i) {
-      const uint2 raw = reinterpret_cast<const uint2 *>(v_s[i])[warp * (COLS / 4) + (lane & 3)];
+      const uint2 raw = reinterpret_cast<const uint2 *>(v_s[buf][i])[warp * (COLS / 4) + (lane & 3)];
       const float2 v0 = unpack2<T>(raw.x), v1 = unpack2<T>(raw.y);
       const float4 v = make_float4(v0.x, v0.y, v1.x, v1.y);
       float4 a = make_float4(0, 0, 0, 0), b = a;
@@ -200,34 +250,37 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
       }
       if (MODE != COMMIT && group == 0 && have) {
         const float qk = qk_s[i];
-        *reinterpret_cast<uint2 *>(p.out + ((tok0 + first + i) * p.Hv + h) * p.Dv + col) =
+        *reinterpret_cast<uint2 *>(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + col) =
             make_uint2(pack2<T>(p.scale * fmaf(qk, u.x, d * b.x), p.scale * fmaf(qk, u.y, d * b.y)),
                        pack2<T>(p.scale * fmaf(qk, u.z, d * b.z), p.scale * fmaf(qk, u.w, d * b.w)));
       }
     }
-  }
-  if (dst >= 0 && have) {
-    float *to = p.s + (((int64_t)dst * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
+    if (x.rows >= 0 && x.dst >= 0 && have) {
+      float *to = p.s + (((int64_t)x.dst * p.Hv + h) * p.Dk + group * per) * p.Dv + col;
 #pragma unroll
-    for (int t = 0; t < PER; ++t)
-      if (t < per)
-        *reinterpret_cast<float4 *>(to + (int64_t)t * p.Dv) = make_float4(kept * S[t].x, kept * S[t].y, kept * S[t].z, kept * S[t].w);
+      for (int t = 0; t < PER; ++t)
+        if (t < per)
+          *reinterpret_cast<float4 *>(to + (int64_t)t * p.Dv) = make_float4(kept * S[t].x, kept * S[t].y, kept * S[t].z, kept * S[t].w);
+    }
+    x = y;
+    item = next;
   }
 }
 
 template <typename T, int WARPS, int MODE>
-cudaError_t launch_width(const DeltaArgs &A, cudaStream_t stream) {
+cudaError_t launch_width(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
   const int slices = (A.Dv + WARPS * COLS - 1) / (WARPS * COLS);
+  const int64_t items = (int64_t)A.n_req * A.Hv * slices, resident = (int64_t)n_sm * (16 / WARPS);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)((int64_t)A.n_req * A.Hv * slices));
+  cfg.gridDim = dim3((unsigned)(items < resident ? items : resident));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_rows_kernel<T, WARPS, MODE>, A, slices);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, delta_rows_kernel<T, WARPS, MODE>, A, slices, (int)items);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -235,8 +288,8 @@ template <typename T, int MODE>
 cudaError_t launch_mode(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
   // narrower slices where heads alone leave SMs without work
   const int64_t heads = (int64_t)A.n_req * A.Hv;
-  if (heads * ((A.Dv + 63) / 64) <= n_sm) return launch_width<T, 2, MODE>(A, stream);
-  return launch_width<T, 4, MODE>(A, stream);
+  if (heads * ((A.Dv + 63) / 64) <= n_sm) return launch_width<T, 2, MODE>(A, n_sm, stream);
+  return launch_width<T, 4, MODE>(A, n_sm, stream);
 }
 template <int MODE>
 cudaError_t launch_type(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
