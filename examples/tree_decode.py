@@ -8,10 +8,15 @@ accepts a path (mfd_verify); each layer keeps that path's entries
 (mfd_kv_commit).  The prompt goes through the same two calls, causally, and so
 does the one-token decoding that the result is compared with.
 
+With --hybrid every other layer is recurrent: its state takes the prompt and single
+tokens (mfd_delta_rule), scores the tree (mfd_delta_tree) and moves along the
+accepted path (mfd_delta_commit); its output goes through mfd_gated_norm, and all
+blocks end in mfd_residual_norm.
+
 The drafter is a stand-in: it knows the target's continuation and gets each
 position of each mode wrong with some probability.
 
-    python examples/tree_decode.py [--cache e4m3]
+    python examples/tree_decode.py [--cache e4m3] [--hybrid]
 """
 from __future__ import annotations
 
@@ -28,9 +33,10 @@ EPS, THETA = 1e-6, 1.0e4
 
 
 class Target:
-    """A random decoder with grouped-query attention over paged caches."""
+    """A random decoder with grouped-query attention over paged caches and, if
+    hybrid, recurrent layers in between."""
 
-    def __init__(self, n_req, max_len, cache_dtype, layers=2, H=256, Hq=8, Hk=2, D=64, V=1000, page_size=16, seed=0):
+    def __init__(self, n_req, max_len, cache_dtype, layers=2, H=256, Hq=8, Hk=2, D=64, V=1000, page_size=16, seed=0, hybrid=False):
         g = torch.Generator("cuda").manual_seed(seed)
 
         def weight(*shape):
@@ -46,19 +52,24 @@ class Target:
             c = mfd.KVCache(n_req * pages, page_size, Hk, D, n_req, pages, cache_dtype)
             c.block_table.copy_(torch.randperm(n_req * pages, generator=torch.Generator().manual_seed(seed)).view(n_req, pages))
             self.caches.append(c)
+        self.recurrent = [_Recurrent(n_req, H, weight) for _ in range(layers if hybrid else 0)]
+        self.ones = torch.ones(H, dtype=torch.bfloat16, device="cuda")
         self.phase = mfd.rope_phases(THETA, D)
         self.ctx = torch.zeros(n_req, dtype=torch.int32, device="cuda")
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.ws = {}
 
-    def forward(self, tokens, pos, n_nodes=None, mask=None):
-        """Logits [n_req, N, V] of N rows per request behind the context."""
+    def forward(self, tokens, pos, n_nodes=None, mask=None, parent=None):
+        """Logits [n_req, N, V] of N rows per request behind the context: a
+        tree's nodes with its mask and parents, or rows in a line."""
         R, N = tokens.shape
         if N not in self.ws:
             n = mfd.mfd_tree_attention_workspace_bytes(R, N, self.Hq, self.Hk, self.D)
             self.ws[N] = torch.empty(n, dtype=torch.uint8, device="cuda")
         x = self.embed[tokens.clamp_min(0).long()]
-        for w, cache in zip(self.layers, self.caches):
+        for i, (w, cache) in enumerate(zip(self.layers, self.caches)):
+            if self.recurrent:
+                x = self.recurrent[i].forward(x, _norm(x), n_nodes, parent, self.ones, self.status)
             qkv = (_norm(x) @ w["qkv"].T).view(R, N, self.Hq + 2 * self.Hk, self.D)
             q, k, v = qkv.split([self.Hq, self.Hk, self.Hk], dim=2)
             q_out = torch.empty((R, N, self.Hq, self.D), dtype=x.dtype, device="cuda")
@@ -75,6 +86,8 @@ class Target:
         new = torch.empty_like(self.ctx)
         for cache in self.caches:
             mfd.mfd_kv_commit(cache, self.ctx, accept_len, path_nodes, n_nodes, new, self.status)
+        for layer in self.recurrent:
+            layer.keep(accept_len, path_nodes, n_nodes, self.status)
         self.ctx = new
 
     def prompt(self, tokens):
@@ -84,6 +97,40 @@ class Target:
         self.forward(tokens[:, :n], pos)
         self.ctx += n
         return tokens[:, n].to(torch.int32)
+
+
+class _Recurrent:
+    """A layer with the gated delta rule."""
+
+    def __init__(self, n_req, H, weight, Hk=2, Hv=4, Dk=64, Dv=64):
+        self.sizes = Hk * Dk, Hk * Dk, Hv * Dv, Hv * Dv
+        self.Hk, self.Hv, self.Dk, self.Dv = Hk, Hv, Dk, Dv
+        self.proj, self.gates, self.o = weight(sum(self.sizes), H), weight(2 * Hv, H), weight(H, Hv * Dv)
+        self.w = 1 + 0.1 * weight(Dv)
+        self.state = mfd.DeltaState(n_req, Hv, Dk, Dv)
+        self.rows = None
+
+    def forward(self, residual, x, n_nodes, parent, ones, status):
+        R, N, _ = x.shape
+        q, k, v, z = (x @ self.proj.T).split(self.sizes, dim=-1)
+        q, k = (torch.nn.functional.silu(t).unflatten(2, (self.Hk, self.Dk)) for t in (q, k))
+        v, z = torch.nn.functional.silu(v).unflatten(2, (self.Hv, self.Dv)), z.unflatten(2, (self.Hv, self.Dv))
+        decay, beta = (x @ self.gates.T).float().split(self.Hv, dim=-1)
+        g, beta = -0.2 * torch.nn.functional.softplus(decay), torch.sigmoid(beta)
+        out = torch.empty((R, N, self.Hv, self.Dv), dtype=x.dtype, device="cuda")
+        if parent is None:
+            mfd.mfd_delta_rule(q, k, v, g, beta, EPS, self.Dk ** -0.5, n_nodes, out, self.state, None, None, status)
+        else:
+            mfd.mfd_delta_tree(q, k, v, g, beta, EPS, self.Dk ** -0.5, parent, n_nodes, out, self.state, None, status)
+            self.rows = k, v, g, beta
+        mfd.mfd_gated_norm(out, z, self.w, EPS, "silu", out)
+        y = (out.view(R, N, -1) @ self.o.T).contiguous()
+        mfd.mfd_residual_norm(y, residual.contiguous(), ones, None, "none", 1.0, None, EPS, y, None)
+        return y
+
+    def keep(self, accept_len, path_nodes, n_nodes, status):
+        k, v, g, beta = self.rows
+        mfd.mfd_delta_commit(k, v, g, beta, EPS, accept_len, path_nodes, n_nodes, self.state, None, None, status)
 
 
 def _norm(x):
@@ -121,7 +168,7 @@ def decode_trees(target, prompt, n, future, K=4, L=7, topk=8, B=31, wrong=0.25, 
         rd.base_pos.copy_(target.ctx)
         rd.logits_topk(draft.view(R * K * L, V))
         rd.build_tree()
-        logits = target.forward(rd.token, rd.pos, rd.n_nodes, rd.mask)
+        logits = target.forward(rd.token, rd.pos, rd.n_nodes, rd.mask, rd.parent)
         rd.verify(logits.contiguous(), temperature, seeds)
         target.keep(rd.accept_len, rd.path_nodes, rd.n_nodes)
         accept = rd.accept_len.tolist()
@@ -137,16 +184,17 @@ def decode_trees(target, prompt, n, future, K=4, L=7, topk=8, B=31, wrong=0.25, 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--hybrid", action="store_true")
     ap.add_argument("--requests", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=64)
     a = ap.parse_args(argv)
     dtype = torch.bfloat16 if a.cache == "bf16" else torch.float8_e4m3fn
     prompt = torch.randint(0, 1000, (a.requests, 37), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
     size = prompt.shape[1] + a.tokens + 64
-    one = decode_one_by_one(Target(a.requests, size, dtype), prompt, a.tokens + 8)
-    tree, rounds = decode_trees(Target(a.requests, size, dtype), prompt, a.tokens, one)
+    one = decode_one_by_one(Target(a.requests, size, dtype, hybrid=a.hybrid), prompt, a.tokens + 8)
+    tree, rounds = decode_trees(Target(a.requests, size, dtype, hybrid=a.hybrid), prompt, a.tokens, one)
     same = (tree == one[:, :a.tokens]).float().mean().item()
-    print(f"{a.tokens} tokens for {a.requests} requests in {rounds} passes ({a.cache} cache); "
+    print(f"{a.tokens} tokens for {a.requests} requests in {rounds} passes ({a.cache} cache{', hybrid' if a.hybrid else ''}); "
           f"{100 * same:.1f}% as decoded one by one")
     return tree, one, rounds, prompt
 
