@@ -66,35 +66,43 @@ struct Fixed {
 };
 // The rest of shared memory, by the number of nodes.
 struct Layout {
-  int kc, w, a, u, node, above, par, depth, pos, fixed, total;
+  int blocks, kc, v, w, a, u, node, above, par, depth, pos, fixed, total;
 };
+constexpr int MOST_SMEM = 232448;
 __host__ __device__ inline Layout layout(int N, int lanes) {
   const int n = N > 1 ? N - 1 : 1;
   Layout y;
-  int at = 2 * HALF;  // keys' 64 rows, then queries', later S^T Q^T
-  y.kc = at;          // another block's keys, later the values
-  at += C * 256;
-  y.w = at;  // P, then W, of the block; and the root's sums
-  at += C * DEPTH * 4;
-  y.a = at;
-  at += n * DEPTH * 4;
-  y.u = at;  // b
-  at += n * lanes * 4;
-  y.node = at;
-  at += n * (int)sizeof(Node);
-  y.above = (at + 15) / 16 * 16;
-  at = y.above + n * DEPTH * 2;
-  y.par = at;
-  at += (N * 2 + 15) / 16 * 16;
-  y.pos = at;
-  at += (N * 2 + 15) / 16 * 16;
-  y.depth = at;
-  at += (N + 15) / 16 * 16;
-  y.fixed = (at + 15) / 16 * 16;
-  y.total = y.fixed + (int)sizeof(Fixed) + 1024;  // and to a 1024-byte border
-  return y;
+  // Two blocks are loaded whole where they fit beside the rest: keys' 64 rows, then
+  // queries', later S^T Q^T; the first one's keys again; values.  Else one block at a
+  // time, and the values over the other block's keys.
+  const int most = (n + C - 1) / C;
+  for (y.blocks = most <= 2 ? most : 1;; --y.blocks) {
+    int at = y.blocks * 2 * HALF;
+    y.kc = at;
+    at += C * 256;
+    y.v = y.blocks == most ? at : y.kc;
+    at += y.blocks == most ? y.blocks * C * lanes * 2 : 0;
+    y.w = at;  // P, then W, of the block; and the root's sums
+    at += C * DEPTH * 4;
+    y.a = at;
+    at += n * DEPTH * 4;
+    y.u = at;  // b
+    at += n * lanes * 4;
+    y.node = at;
+    at += n * (int)sizeof(Node);
+    y.above = (at + 15) / 16 * 16;
+    at = y.above + n * DEPTH * 2;
+    y.par = at;
+    at += (N * 2 + 15) / 16 * 16;
+    y.pos = at;
+    at += (N * 2 + 15) / 16 * 16;
+    y.depth = at;
+    at += (N + 15) / 16 * 16;
+    y.fixed = (at + 15) / 16 * 16;
+    y.total = y.fixed + (int)sizeof(Fixed) + 1024;  // and to a 1024-byte border
+    if (y.total <= MOST_SMEM || y.blocks == 1) return y;
+  }
 }
-constexpr int MOST_SMEM = 232448;
 
 template <typename T, int LN>  // LN: columns a lane has in the sums
 __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs p, int slices) {
@@ -105,10 +113,10 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
   uint8_t *sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   const Layout y = layout(p.N, LANES);
   Fixed &fx = *reinterpret_cast<Fixed *>(sm + y.fixed);
-  uint8_t *tile = sm, *kc = sm + y.kc;
-  float *xq = reinterpret_cast<float *>(sm), *w_s = reinterpret_cast<float *>(sm + y.w), *a_s = reinterpret_cast<float *>(sm + y.a);
+  uint8_t *kc = sm + y.kc;
+  const bool whole = y.v != y.kc;  // all blocks are in shared memory at once
+  float *w_s = reinterpret_cast<float *>(sm + y.w), *a_s = reinterpret_cast<float *>(sm + y.a);
   float *u_s = reinterpret_cast<float *>(sm + y.u);
-  uint16_t *v_s = reinterpret_cast<uint16_t *>(kc);
   Node *node_s = reinterpret_cast<Node *>(sm + y.node);
   uint16_t *above = reinterpret_cast<uint16_t *>(sm + y.above), *pos_s = reinterpret_cast<uint16_t *>(sm + y.pos);
   int16_t *par = reinterpret_cast<int16_t *>(sm + y.par);
@@ -158,7 +166,8 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
     if (elect_one()) {
       constexpr uint32_t id = idesc_16<T>(128, C, false), id2 = idesc_16<T>(128, 128, false);
       const int steps = p.Dk / 16;
-      const uint32_t a = desc_lo(smem_u32(tile), 16), b = desc_lo(smem_u32(kc), 16);
+      const uint32_t tile0 = desc_lo(smem_u32(sm), 16), b = desc_lo(smem_u32(kc), 16);
+      uint32_t a = tile0;
       for (uint32_t n_go = 0;; ++n_go) {
         wait(&fx.go, n_go & 1u);
         const int order = *(volatile int *)&fx.order;
@@ -173,6 +182,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
           tc_commit(&fx.dot[order - KEYS]);
           continue;
         }
+        a = tile0 + (order == NEXT && whole ? 2 * HALF >> 4 : 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k)  // with the block's own
           if (k < steps) {
@@ -322,6 +332,12 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
     if (nn == 0) continue;
 
     // --------------------------------------------------------- the head
+    float own_g = 0.f, own_beta = 0.f;  // of the node that this thread looks after
+    if (tid < n) {
+      const int64_t at = (tok0 + (node_s[tid].at & 0xFFFF)) * p.Hv + h;
+      own_g = __ldg(p.g + at);
+      own_beta = __ldg(p.beta + at);
+    }
     float s[32];
     {
       const float *from = p.s + (((int64_t)q.src * p.Hv + h) * p.Dk + d0) * p.Dv + col;
@@ -331,33 +347,43 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
       if (tid == 0 && q.src >= 0 && slice == slices - 1 && h + 1 < p.Hv && item + 1 < item1)  // the next one, to L2
         bulk_prefetch_l2(p.s + ((int64_t)q.src * p.Hv + h + 1) * p.Dk * p.Dv, (uint32_t)(p.Dk * p.Dv * 4));
     }
-    // 64 rows of keys or queries from sorted place `first` on, swizzled, to rows `row0` on
-    // of blocks of `rows` rows
-    auto load_rows = [&](const uint16_t *from, int64_t stride, int first, uint8_t *to, int row0, int rows) {
-      for (int i = tid; i < C * 16; i += WORKERS) {
-        const int row = i >> 4, ch = i & 15;
-        uint8_t *dst = to + (ch >> 3) * (rows * 128) + (row0 + row) * 128 + (((ch & 7) ^ (row & 7)) << 4);
-        if (first + row < n && ch * 8 < p.Dk)
-          cp_async16(smem_u32(dst), from + (tok0 + (node_s[first + row].at & 0xFFFF)) * stride + hk * p.Dk + ch * 8);
-        else
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+    // A thread loads chunk `ch` of rows row16, row16 + 32 of a block: of its keys and
+    // queries to `to`, of the values to `tv`, of the keys alone to `tk` (each may be NULL).
+    const int ch = tid & 15, row16 = tid >> 4;
+    auto load = [&](int first, uint8_t *to, uint16_t *tv, uint8_t *tk) {
+      const uint32_t swizzle = ((ch & 7) ^ (row16 & 7)) << 4;
+      const bool dk = ch * 8 < p.Dk, dv = ch * 8 < LANES && slice * LANES + ch * 8 < p.Dv;
+#pragma unroll
+      for (int row = row16; row < C; row += 32) {
+        const bool there = first + row < n;
+        const int64_t tok = tok0 + (there ? node_s[first + row].at & 0xFFFF : 0);
+        const uint16_t *kr = p.k + tok * p.k_stride + hk * p.Dk + ch * 8;
+        uint8_t *kq = to + (ch >> 3) * HALF + row * 128 + swizzle, *k1 = tk + (ch >> 3) * (C * 128) + row * 128 + swizzle;
+        if (there && dk) {
+          if (to) cp_async16(smem_u32(kq), kr);
+          if (to) cp_async16(smem_u32(kq + C * 128), p.q + tok * p.q_stride + hk * p.Dk + ch * 8);
+          if (tk) cp_async16(smem_u32(k1), kr);
+        } else {
+          if (to) *reinterpret_cast<uint4 *>(kq) = *reinterpret_cast<uint4 *>(kq + C * 128) = make_uint4(0, 0, 0, 0);
+          if (tk) *reinterpret_cast<uint4 *>(k1) = make_uint4(0, 0, 0, 0);
+        }
+        if (tv && there && dv)
+          cp_async16(smem_u32(tv + row * LANES + ch * 8), p.v + tok * p.v_stride + h * p.Dv + slice * LANES + ch * 8);
       }
     };
-    if (n > 0) {
-      load_rows(p.k, p.k_stride, 0, tile, 0, 128);
-      load_rows(p.q, p.q_stride, 0, tile, 64, 128);
-    }
-    for (int i = tid; i < n; i += WORKERS) {
-      const int64_t at = (tok0 + (node_s[i].at & 0xFFFF)) * p.Hv + h;
-      const float g = __ldg(p.g + at);
-      g_s[i] = g < LEAST_LOG ? LEAST_LOG : g;
-      node_s[i].beta = __ldg(p.beta + at);
-      node_s[i].rk = node_s[i].rq = 1.f;
+    uint16_t *const v0_s = reinterpret_cast<uint16_t *>(sm + y.v);
+    for (int b0 = 0; b0 < (whole ? n : n > 0 ? 1 : 0); b0 += C)
+      load(b0, sm + b0 / C * (2 * HALF), whole ? v0_s + b0 * LANES : nullptr, whole && b0 == 0 ? kc : nullptr);
+    if (tid < n) {
+      g_s[tid] = own_g < LEAST_LOG ? LEAST_LOG : own_g;
+      node_s[tid].beta = own_beta;
+      node_s[tid].rk = node_s[tid].rq = 1.f;
     }
     // the root's key and query
     if (warp == WARPS - 1) {
       float a[4], b[4], kk = 0.f, qq = 0.f, kq = 0.f;
       uint2 kr = make_uint2(0, 0), qr = kr;
+      const float g0 = __ldg(p.g + tok0 * p.Hv + h), beta0 = __ldg(p.beta + tok0 * p.Hv + h);
       if (lane * 4 < p.Dk) {
         kr = *reinterpret_cast<const uint2 *>(p.k + tok0 * p.k_stride + hk * p.Dk + lane * 4);
         qr = *reinterpret_cast<const uint2 *>(p.q + tok0 * p.q_stride + hk * p.Dk + lane * 4);
@@ -380,8 +406,8 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
       }
       kq = warp_sum(kq);
       if (lane == 0) {
-        fx.root[0] = expf(__ldg(p.g + tok0 * p.Hv + h));
-        fx.root[1] = __ldg(p.beta + tok0 * p.Hv + h);
+        fx.root[0] = expf(g0);
+        fx.root[1] = beta0;
         fx.root[2] = kq;
       }
     }
@@ -399,8 +425,18 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
     }
     for (int i = tid; i < n; i += WORKERS) {  // sums of log2 decays from below the root, as two floats
       const int d = node_s[i].at >> 16;
+      const uint4 j0 = *reinterpret_cast<const uint4 *>(above + i * DEPTH), j1 = *reinterpret_cast<const uint4 *>(above + i * DEPTH + 8);
+      const uint32_t js[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};
+      // the sum of the high parts, and what each addition to it and each product lost
       Two c = two_product(g_s[i], LOG2E_HI, LOG2E_LO);
-      for (int e = 0; e < d - 1; ++e) c = two_sum(c, two_product(g_s[above[i * DEPTH + e]], LOG2E_HI, LOG2E_LO));
+#pragma unroll
+      for (int e = 0; e < DEPTH - 1; ++e) {
+        const Two x = two_product(e < d - 1 ? g_s[(js[e >> 1] >> (16 * (e & 1))) & 0xFFFFu] : 0.f, LOG2E_HI, LOG2E_LO);
+        const Two t = two_sum(c.hi, x.hi);
+        c.hi = t.hi;
+        c.lo += t.lo + x.lo;
+      }
+      c = two_sum(c.hi, c.lo);
       node_s[i].chi = c.hi;
       node_s[i].clo = c.lo;
     }
@@ -455,11 +491,14 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
       // ------------------------------------------------------- a block
       const int live = min(C, n - b0);
       uint32_t *vis_b = vis + (size_t)b0 * LANES;
-      if (b0) {
+      uint8_t *tile = sm + (whole ? b0 / C * (2 * HALF) : 0);
+      float *xq = reinterpret_cast<float *>(tile);
+      uint16_t *v_s = v0_s + (whole ? b0 * LANES : 0);
+      if (b0 && whole) sync();
+      if (b0 && !whole) {
         sync();  // the block before is done with
-        load_rows(p.k, p.k_stride, b0, tile, 0, 128);
-        load_rows(p.q, p.q_stride, b0, tile, 64, 128);
-        load_rows(p.k, p.k_stride, b0 - C, kc, 0, C);
+        load(b0, tile, nullptr, nullptr);
+        load(b0 - C, nullptr, nullptr, kc);
       }
       // meanwhile the nodes above as bits over sorted places: four threads a row, 128
       // places each
@@ -509,7 +548,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
       for (int b1 = b0; b1 >= 0; b1 -= C) {
         if (b0 - b1 >= 2 * C) {
           sync();  // the keys before have been used, the dot products before last read
-          load_rows(p.k, p.k_stride, b1, kc, 0, C);
+          load(b1, nullptr, nullptr, kc);
           cp_async_wait();
           go(KEYS + ((b0 - b1) & C ? 1 : 0));
         }
@@ -535,13 +574,8 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
         tc_fence_before();
       }
       sync();
-      // the values come in over the keys; factors
-      for (int i = tid; i < C * (LANES / 8); i += WORKERS) {
-        const int row = i / (LANES / 8), ch = i % (LANES / 8), c = slice * LANES + ch * 8;
-        if (row < live && c < p.Dv)
-          cp_async16(smem_u32(v_s + row * LANES + ch * 8),
-                     p.v + (tok0 + (node_s[b0 + row].at & 0xFFFF)) * p.v_stride + h * p.Dv + c);
-      }
+      if (!whole) load(b0, nullptr, v_s, nullptr);  // over the keys
+      // factors
 #pragma unroll
       for (int i = tid; i < C * DEPTH; i += WORKERS) {
         const int row = i >> 4, e = i & 15;
@@ -608,56 +642,66 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
       }
       tc_fence_before();
       sync();
-      // outputs, a node a warp
-      for (int row = warp; row < live; row += WARPS) {
-        const int i = b0 + row, at = node_s[i].at, d = at >> 16;
+      // outputs, a node half a warp: a lane has columns from c and from c + 16 LN on
+      for (int row = row16; row < live; row += 32) {
+        const int i = b0 + row, at = node_s[i].at, d = at >> 16, c = ch * LN;
         const float2 f = fx.out[row];
         const float *mine = w_s + row * DEPTH;
         const uint16_t *up = above + i * DEPTH;
-        float o[LN], b[LN];
-        auto take = [&](const float *from, float (&x)[LN]) {
-          if (LN == 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(from + lane * LN);
-            x[0] = y.x, x[LN > 1 ? 1 : 0] = y.y, x[LN > 2 ? 2 : 0] = y.z, x[LN - 1] = y.w;
-          } else if (LN == 2) {
-            const float2 y = *reinterpret_cast<const float2 *>(from + lane * LN);
-            x[0] = y.x, x[LN - 1] = y.y;
-          } else {
-            x[0] = from[lane];
+        float o[2 * LN];
+        auto take = [&](const float *from, float (&x)[2 * LN]) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float *at = from + c + e * 16 * LN;
+            if (LN == 4) {
+              const float4 y = *reinterpret_cast<const float4 *>(at);
+              x[e * LN] = y.x, x[e * LN + (LN > 1 ? 1 : 0)] = y.y, x[e * LN + (LN > 2 ? 2 : 0)] = y.z, x[e * LN + LN - 1] = y.w;
+            } else if (LN == 2) {
+              const float2 y = *reinterpret_cast<const float2 *>(at);
+              x[e * LN] = y.x, x[e * LN + LN - 1] = y.y;
+            } else {
+              x[e * LN] = *at;
+            }
           }
         };
         take(xq + row * LANES, o);
-        take(u_s + i * LANES, b);
-        const float self = mine[d - 1];
+        {
+          float b[2 * LN];
+          take(u_s + i * LANES, b);
+          const float self = mine[d - 1];
 #pragma unroll
-        for (int k = 0; k < LN; ++k) o[k] = fmaf(self, b[k], f.x * o[k]);
-        int t = 0;
-        for (; t + 4 <= d - 1; t += 4) {
-          const float4 w = *reinterpret_cast<const float4 *>(mine + t);
-          const uint2 j = *reinterpret_cast<const uint2 *>(up + t);
-          float x[4][LN];
-          take(u_s + (j.x & 0xFFFFu) * LANES, x[0]);
-          take(u_s + (j.x >> 16) * LANES, x[1]);
-          take(u_s + (j.y & 0xFFFFu) * LANES, x[2]);
-          take(u_s + (j.y >> 16) * LANES, x[3]);
-#pragma unroll
-          for (int k = 0; k < LN; ++k)
-            o[k] = fmaf(w.w, x[3][k], fmaf(w.z, x[2][k], fmaf(w.y, x[1][k], fmaf(w.x, x[0][k], o[k]))));
+          for (int k = 0; k < 2 * LN; ++k) o[k] = fmaf(self, b[k], f.x * o[k]);
         }
-        for (; t < d - 1; ++t) {
-          take(u_s + up[t] * LANES, b);
+        int t = 0;
+        for (; t + 2 <= d - 1; t += 2) {
+          const float2 w = *reinterpret_cast<const float2 *>(mine + t);
+          const uint32_t j = *reinterpret_cast<const uint32_t *>(up + t);
+          float x[2 * LN], z[2 * LN];
+          take(u_s + (j & 0xFFFFu) * LANES, x);
+          take(u_s + (j >> 16) * LANES, z);
+#pragma unroll
+          for (int k = 0; k < 2 * LN; ++k) o[k] = fmaf(w.y, z[k], fmaf(w.x, x[k], o[k]));
+        }
+        if (t < d - 1) {
+          float x[2 * LN];
+          take(u_s + up[t] * LANES, x);
           const float w = mine[t];
 #pragma unroll
-          for (int k = 0; k < LN; ++k) o[k] = fmaf(w, b[k], o[k]);
+          for (int k = 0; k < 2 * LN; ++k) o[k] = fmaf(w, x[k], o[k]);
         }
-        if (c0 < p.Dv && ok) {
-          uint16_t *to = p.out + ((tok0 + (at & 0xFFFF)) * p.Hv + h) * p.Dv + c0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int cc = slice * LANES + c + e * 16 * LN;
+          const float *y = o + e * LN;
+          uint16_t *to = p.out + ((tok0 + (at & 0xFFFF)) * p.Hv + h) * p.Dv + cc;
+          if (cc >= p.Dv || !ok) continue;
           if (LN == 4)
-            *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(f.y * o[0], f.y * o[LN > 1 ? 1 : 0]), pack2<T>(f.y * o[LN > 2 ? 2 : 0], f.y * o[LN - 1]));
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(pack2<T>(f.y * y[0], f.y * y[LN > 1 ? 1 : 0]), pack2<T>(f.y * y[LN > 2 ? 2 : 0], f.y * y[LN - 1]));
           else if (LN == 2)
-            *reinterpret_cast<uint32_t *>(to) = pack2<T>(f.y * o[0], f.y * o[LN - 1]);
+            *reinterpret_cast<uint32_t *>(to) = pack2<T>(f.y * y[0], f.y * y[LN - 1]);
           else
-            *to = (uint16_t)pack2<T>(f.y * o[0], 0.f);
+            *to = (uint16_t)pack2<T>(f.y * y[0], 0.f);
         }
       }
     }
