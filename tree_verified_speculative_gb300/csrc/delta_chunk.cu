@@ -538,6 +538,20 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       named_sync(5 + (warp & 3), 64);
       return max_nan(x, sm.top[which][half ^ 1][l], 0.f);
     };
+    // Whether any thread of the chain says so.
+    auto any = [&](bool x) {
+      uint32_t y;
+      __syncwarp();
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 p, %1, 0;\n\t"
+          "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(y)
+          : "r"((uint32_t)x), "n"(CHAIN)
+          : "memory");
+      return y != 0;
+    };
     constexpr uint32_t id = idesc_16<__half>(128, C, false), id_t = idesc_16<T>(128, C, false), id_kd = idesc_16<T>(128, 128, true);
     const int steps = p.Dk / 16;
     // Products: one lane of warp `who` issues them once all of the chain's warps have
@@ -758,7 +772,8 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         tc_commit(&sm.empty[n & 1]);  // with the state's step the last to read this stage
       });
       wait_warp(&sm.s, par);
-      if (!slow_prep && *(volatile int *)&sm.chain_bad != n + 1) {
+      // one decision for all of the chain, whose threads meet at barriers on either way
+      if (!any(slow_prep || *(volatile int *)&sm.chain_bad == n + 1)) {
         if (ok) {
           tc_fence_after();
 #pragma unroll
