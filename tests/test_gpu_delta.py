@@ -277,6 +277,38 @@ def test_commit(R, N, Hk, Hv, Dk, Dv, dt, norm, L):
         x.check_state(x.state.s[R + r], S, size, len(rows))
 
 
+@pytest.mark.parametrize("R,Hv", [(45, 16), (300, 4)])
+@pytest.mark.parametrize("form", ["rule", "commit"])
+def test_more_heads_than_blocks(form, R, Hv):
+    """Blocks walk several heads, of requests of unlike lengths; a request that is
+    refused in between leaves the others as they are."""
+    gen = torch.Generator().manual_seed(R)
+    N = 7
+    x = Rows(R, N, 2, Hv, 32, 48, "bf16", True, seed=R)
+    before = x.state.s.clone()
+    rows = torch.randint(0 if form == "rule" else 1, N + 1, (R,), generator=gen).tolist()
+    wrong = R // 3
+    dst = i32([R + r for r in range(R)])
+    if form == "rule":
+        live = list(rows)
+        live[wrong] = N + 1
+        x.rule(i32(live), None, dst)
+    else:
+        accept = [n - 1 for n in rows]
+        accept[wrong] = N
+        x.commit(i32(accept), torch.arange(N, dtype=torch.int32).repeat(R, 1).cuda(), None, None, dst)
+    torch.cuda.synchronize()
+    assert int(x.st.item()) == mfd.MFD_ERR_INPUT and torch.equal(x.state.s[:R], before[:R])
+    for r in range(R):
+        if r == wrong:
+            assert torch.equal(x.state.s[R + r], before[R + r]) and (form == "commit" or bool((x.out[r] == 0).all()))
+            continue
+        out, S, size = x.want(r, rows[r], before[r])
+        if form == "rule":
+            x.check_out(r, rows[r], out, size)
+        x.check_state(x.state.s[R + r], S, size, rows[r])
+
+
 def test_device_refusals():
     """Lengths, slots, parents and paths that are none: the status is set, the
     request's outputs are zero, its state stays, and the others' are right."""

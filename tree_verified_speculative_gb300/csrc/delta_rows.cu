@@ -27,6 +27,7 @@ constexpr int BATCH = DELTA_MAX_DEPTH + 1;  // rows at most: all of a path
 static_assert(BATCH >= DELTA_CHUNK_FROM - 1, "rows of the rule");
 constexpr int MAX_DK = 128;
 constexpr int PER = MAX_DK / 8;  // rows of the state a lane holds
+constexpr int ORDERED = 256;     // requests at most that a block puts in order
 
 enum { RULE = 0, COMMIT = 1 };
 
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
   __shared__ float4 k_s[BATCH][MAX_DK / 4], q_s[MODE == COMMIT ? 1 : BATCH][MAX_DK / 4];
   __shared__ uint4 raw_s[2][BATCH][VECS][MAX_DK / 8], v_s[2][BATCH][W / 8];  // as they are, of this item and the next
   __shared__ float g_s[2][BATCH], b_s[2][BATCH], decay_s[BATCH], beta_s[BATCH], qk_s[BATCH];
-  __shared__ int row_s[2][BATCH], bad_s[2];
+  __shared__ int row_s[2][BATCH], bad_s[2], length_s[ORDERED], order_s[ORDERED];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = lane >> 2, per = p.Dk / 8;  // rows of a group
   pdl_launch_dependents();
@@ -68,6 +69,21 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
     for (int i = tid; i < BATCH * MAX_DK; i += THREADS) reinterpret_cast<float *>(k_s)[i] = 0.f;
     for (int i = tid; i < (MODE == COMMIT ? 1 : BATCH) * MAX_DK; i += THREADS) reinterpret_cast<float *>(q_s)[i] = 0.f;
   }
+  // Blocks that walk several items get them longest first, and every second round in
+  // reverse: their sums of rows differ by little then.
+  const bool ordered = (int)gridDim.x < items && p.n_req <= ORDERED && (MODE == COMMIT || (p.n_nodes && p.N > 1));
+  if (ordered) {
+    for (int i = tid; i < p.n_req; i += THREADS) length_s[i] = __ldg((MODE == COMMIT ? p.accept_len : p.n_nodes) + i);
+    block_sync();
+    for (int i = tid; i < p.n_req; i += THREADS) {
+      const int own = length_s[i];
+      int place = 0;
+      for (int j = 0; j < p.n_req; ++j) place += length_s[j] > own || (length_s[j] == own && j < i);
+      order_s[place] = i;
+    }
+    block_sync();
+  }
+  auto item_of = [&](int round) { return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); };
   struct Item {
     int slice, h, r, nn, src, dst, rows;
     int node;  // of the path, thread's
@@ -78,6 +94,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
     x.slice = item % slices;
     x.h = item / slices % p.Hv;
     x.r = item / slices / p.Hv;
+    if (ordered) x.r = order_s[x.r];
     x.nn = p.n_nodes ? __ldg(p.n_nodes + x.r) : p.N;
     x.src = p.src ? __ldg(p.src + x.r) : x.r;
     x.dst = p.dst ? __ldg(p.dst + x.r) : x.src;
@@ -129,7 +146,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
   block_sync();
   if (bad_s[0]) x.rows = -1;
   if (x.rows > 0) fetch(x, 0, false);
-  for (int item = blockIdx.x; item < items; buf ^= 1) {
+  for (int round = 0, item = blockIdx.x; item < items; buf ^= 1) {
     const int n = max(x.rows, 0), h = x.h, slice = x.slice;
     const int col = slice * W + warp * COLS + (lane & 3) * 4;
     const bool have = col < p.Dv;
@@ -142,7 +159,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
         S[t] = x.rows >= 0 && x.src >= 0 && have && t < per ? *reinterpret_cast<const float4 *>(from + (int64_t)t * p.Dv)
                                                             : make_float4(0, 0, 0, 0);
     }
-    const int next = item + gridDim.x;
+    const int next = item_of(++round);
     Item y = x;
     if (next < items) y = read(next);
     if (x.rows < 0 && tid == 0) report(p.status, MFD_ERR_INPUT);
