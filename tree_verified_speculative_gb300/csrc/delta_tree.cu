@@ -27,6 +27,13 @@
 // Keys and queries go to the tensor cores as they are.  The state goes in as a
 // sum of numbers of their type: three of bf16, each the front of what is left
 // (24 bits), or two of fp16 after a power of two for each column (22 bits).
+//
+// 32 trees of 129 nodes and 32 heads of 128 x 128 take 132 us, a head some 36,000
+// cycles of an SM: a third until its state and rows have come and the root is done,
+// the rest phases of 1,000 to 1,500 cycles, each as long as its loads from shared
+// memory and its exchanges take, with a barrier of 16 warps after it.  The tensor cores
+// work 11% of the time.  (Fetching the next head's state during a head's outputs cost
+// more in registers than it hid: 154 us.)
 #include <atomic>
 #include <type_traits>
 
@@ -742,7 +749,9 @@ cudaError_t launch_lanes(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch_type(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
-  // as many columns as fit beside all nodes, fewer where heads alone leave SMs without work
+  // As many columns as fit beside all nodes, fewer where heads alone leave SMs without
+  // work: a tree of 257 nodes and 32 heads takes 39 us in slices of 32 columns, 42 in
+  // slices of 128; four trees of 129 take 64 and 21.
   const int64_t heads = (int64_t)A.n_req * A.Hv;
   const auto slices = [&](int lanes) { return heads * ((A.Dv + lanes - 1) / lanes); };
   if (layout(A.N, 128).total <= MOST_SMEM && slices(64) > n_sm) return launch_lanes<T, 4>(A, n_sm, stream);
