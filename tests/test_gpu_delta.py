@@ -277,6 +277,35 @@ def test_commit(R, N, Hk, Hv, Dk, Dv, dt, norm, L):
         x.check_state(x.state.s[R + r], S, size, len(rows))
 
 
+@pytest.mark.parametrize("N", [5, 64, 200])
+@pytest.mark.parametrize("what", ["alike", "in turn", "zero"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_keys_that_repeat(N, what, dt):
+    """One key over and over, two in turn, none: what a row takes back is what the
+    rows before it put there."""
+    gen = torch.Generator().manual_seed(N)
+    x = Rows(1, N, 1, 2, 128, 64, dt, True, seed=N, slots=2)
+    if what == "zero":
+        x.k.zero_()
+    else:
+        period = 1 if what == "alike" else 2
+        x.k.copy_(x.k[:, torch.arange(N, device="cuda") % period].clone())
+    x.g.mul_(0.01)
+    x.beta.copy_(1 - x.beta * 0.01)
+    before = x.state.s.clone()
+    x.rule(None, i32([0]), i32([1]))
+    torch.cuda.synchronize()
+    out, S, size = x.want(0, N, before[0])
+    x.check_out(0, N, out, size)
+    x.check_state(x.state.s[1], S, size, N)
+    par = random_tree(N, gen)
+    x.tree(i32([par]), None, i32([0]))
+    torch.cuda.synchronize()
+    out, _, size = x.want(0, N, before[0], par)
+    x.check_out(0, N, out, size)
+    assert int(x.st.item()) == 0
+
+
 @pytest.mark.parametrize("R,Hv", [(45, 16), (300, 4)])
 @pytest.mark.parametrize("form", ["rule", "commit"])
 def test_more_heads_than_blocks(form, R, Hv):

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (!finite(len2)) bad = true;
         if (part == 0) {
           sm.n2[row] = len2;
-          if (row < C) sm.cc[row].z = __uint_as_float((uint32_t)(127 - (((int)(__float_as_uint(len2) >> 23) - 127) >> 1)) << 23);
+          if (row < C) sm.cc[row].z = __uint_as_float((uint32_t)(127 - (((int)(__float_as_uint(len2 > 0.f ? len2 : 1.f) >> 23) - 127) >> 1)) << 23);
         }
       }
       named_sync(2, PREP);
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       const bool is_q = (t & 127) >= C;
       const float4 ci = sm.cc[row];
       const float len2 = row0 + row < nn ? sm.n2[t & 127] : 1.f;
-      const int half_e = ((int)(__float_as_uint(len2) >> 23) - 127) >> 1;  // floor(log2 of the length)
+      // floor(log2 of the length); of a key of zeros, which no power makes longer, 0
+      const int half_e = ((int)(__float_as_uint(len2 > 0.f ? len2 : 1.f) >> 23) - 127) >> 1;
       const float left = (p.normalize ? rsqrtf(len2 + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
       const float power = __uint_as_float((uint32_t)(127 - half_e) << 23);
       const float br = sm.beta[row] * left, brr = br * left;
