@@ -21,7 +21,9 @@ namespace {
 
 __device__ __forceinline__ float activate(float x, int act) {
   if (act == MFD_ACT_NONE) return x;
-  const float s = __fdividef(1.f, 1.f + __expf(-x));  // to 0 for x far below 0
+  float e, s;  // s to 0 for x far below 0
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
   return act == MFD_ACT_SIGMOID ? s : x * s;          // silu of -inf is NaN, as -inf / (1 + inf) is
 }
 
