@@ -103,7 +103,7 @@ __device__ __forceinline__ float block_sum(float x, float *buf) {
 // A block walks tokens, CH chunks of 8 elements a thread, with the next token's
 // loads in flight and the weights in registers.
 template <typename T, int CH>
-__global__ void __launch_bounds__(512) residual_norm_kernel(const ResidualNormArgs p) {
+__global__ void __launch_bounds__(512, CH == 1 ? 2 : 1) residual_norm_kernel(const ResidualNormArgs p) {
   __shared__ float sum_s[2][2][16];  // [token mod 2][norm]
   pdl_launch_dependents();
   pdl_wait();
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(512) residual_norm_kernel(const ResidualNormAr
 template <typename T, int CH>
 cudaError_t launch_chunks(const ResidualNormArgs &A, int n_sm, cudaLaunchConfig_t &cfg) {
   const int threads = (A.H / 8 + CH * 32 - 1) / (CH * 32) * 32;
-  // as many blocks as are resident: their threads times 64 registers, or 96 with more chunks
-  const int fit = 65536 / (threads * (CH == 1 ? 64 : CH == 2 ? 96 : 128)), blocks = n_sm * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
+  // as many blocks as are resident: their threads times 64 registers, or 128 with more chunks
+  const int fit = 65536 / (threads * (CH == 1 ? 64 : 128)), blocks = n_sm * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.gridDim = dim3((unsigned)(A.T < blocks ? A.T : blocks));
   return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, CH>, A);
