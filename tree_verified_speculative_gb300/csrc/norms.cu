@@ -102,8 +102,8 @@ __device__ __forceinline__ float block_sum(float x, float *buf) {
 
 // A block walks tokens, CH chunks of 8 elements a thread, with the next token's
 // loads in flight and the weights in registers.
-template <typename T, int CH>
-__global__ void __launch_bounds__(512, CH == 1 ? 2 : 1) residual_norm_kernel(const ResidualNormArgs p) {
+template <typename T, int CH, int REGS>
+__global__ void __maxnreg__(REGS) residual_norm_kernel(const ResidualNormArgs p) {
   __shared__ float sum_s[2][2][16];  // [token mod 2][norm]
   pdl_launch_dependents();
   pdl_wait();
@@ -188,21 +188,26 @@ __global__ void __launch_bounds__(512, CH == 1 ? 2 : 1) residual_norm_kernel(con
   }
 }
 
-template <typename T, int CH>
-cudaError_t launch_chunks(const ResidualNormArgs &A, int n_sm, cudaLaunchConfig_t &cfg) {
-  const int threads = (A.H / 8 + CH * 32 - 1) / (CH * 32) * 32;
-  // as many blocks as are resident: their threads times 64 registers, or 128 with more chunks
-  const int fit = 65536 / (threads * (CH == 1 ? 64 : 128)), blocks = n_sm * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
+template <typename T, int CH, int REGS>
+cudaError_t launch_chunks(const ResidualNormArgs &A, int threads, int n_sm, cudaLaunchConfig_t &cfg) {
+  // as many blocks as are resident
+  const int fit = 65536 / (threads * REGS), blocks = n_sm * (fit < 1 ? 1 : fit > 32 ? 32 : fit);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.gridDim = dim3((unsigned)(A.T < blocks ? A.T : blocks));
-  return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, CH>, A);
+  return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, CH, REGS>, A);
 }
+// Two chunks a thread where 512 threads have a row so: a block of few warps waits less
+// for its sums, and more blocks are resident (rows of 2560 at 6.1 TB/s, with one chunk a
+// thread 5.7; of 4096 5.5 and 5.6).  80 registers a thread, which spill a little, where
+// they let a second block in: rows of 6144 at 5.5 TB/s, 4.3 with 96; of 8192 4.5 and 4.9.
 template <typename T>
 cudaError_t launch_residual(const ResidualNormArgs &A, int n_sm, cudaLaunchConfig_t &cfg) {
   const int chunks = A.H / 8;
-  if (chunks <= 512) return launch_chunks<T, 1>(A, n_sm, cfg);
-  if (chunks <= 1024) return launch_chunks<T, 2>(A, n_sm, cfg);
-  return launch_chunks<T, 4>(A, n_sm, cfg);
+  const auto threads = [&](int ch) { return (chunks + ch * 32 - 1) / (ch * 32) * 32; };
+  if (chunks > 1024) return launch_chunks<T, 4, 128>(A, threads(4), n_sm, cfg);
+  const int t = threads(2);
+  if (2 * t * 96 > 65536 && 2 * t * 80 <= 65536) return launch_chunks<T, 2, 80>(A, t, n_sm, cfg);
+  return launch_chunks<T, 2, 96>(A, t, n_sm, cfg);
 }
 
 cudaError_t done(cudaError_t e) { return e != cudaSuccess ? e : cudaGetLastError(); }
