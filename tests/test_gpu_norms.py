@@ -84,7 +84,10 @@ def test_gated_at_the_ends():
 
 CASES = [(1, 8, "bf16", "none", None, True, True), (1, 2560, "bf16", "none", None, True, True), (5, 264, "fp16", "sigmoid", "rows", False, True),
          (3, 4096, "bf16", "silu", "one", True, False), (9, 4104, "bf16", "none", "rows", True, True), (2, 8200, "fp16", "sigmoid", "one", True, True),
-         (4, 16384, "bf16", "silu", "rows", True, True), (300, 1024, "fp16", "none", None, False, False), (33, 256, "bf16", "sigmoid", "rows", True, True)]
+         (4, 16384, "bf16", "silu", "rows", True, True), (300, 1024, "fp16", "none", None, False, False), (33, 256, "bf16", "sigmoid", "rows", True, True),
+         # more rows than blocks are resident
+         (700, 5600, "bf16", "silu", "rows", True, True), (701, 6400, "fp16", "sigmoid", "one", True, True),
+         (403, 8320, "fp16", "none", "rows", True, True), (5000, 264, "bf16", "silu", None, True, True)]
 
 
 @pytest.mark.parametrize("i", range(len(CASES)))
