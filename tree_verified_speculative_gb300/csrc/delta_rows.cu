@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) delta_rows_kernel(cons
       const float4 u = make_float4(beta * fmaf(-d, a.x, v.x), beta * fmaf(-d, a.y, v.y), beta * fmaf(-d, a.z, v.z),
                                    beta * fmaf(-d, a.w, v.w));
       kept = d;
-      if (!(d > 0x1p-40f && d < 0x1p40f)) {  // too small to divide by, or NaN
+      // A decay too small to divide by, or NaN; or a step that divided by it would leave
+      // fp32 (the state itself, undivided, holds it).  A column's lanes have the same sums.
+      const float most = fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w)));
+      if (!(d > 0x1p-40f && d < 0x1p40f) || most > d * 0x1p100f) {
 #pragma unroll
         for (int t = 0; t < PER; ++t) S[t] = make_float4(d * S[t].x, d * S[t].y, d * S[t].z, d * S[t].w);
         kept = 1.f;
