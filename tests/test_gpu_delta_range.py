@@ -1,5 +1,7 @@
 """GPU tests of the gated delta rule where rows differ in size by many orders:
 each row is held to its own size, which no later row enters."""
+import math
+
 import pytest
 import torch
 
@@ -59,7 +61,7 @@ def check(x, want, lim, S=None, lim_S=None, got=None, r=0):
         assert err <= 1, err
 
 
-@pytest.mark.parametrize("N", [1, 4, 17])
+@pytest.mark.parametrize("N", [1, 4, 17, 18, 70])
 @pytest.mark.parametrize("top", [1e30, 1e33])
 @pytest.mark.parametrize("Dk", [16, 128])
 def test_large_values_and_short_memories(N, top, Dk):
@@ -79,3 +81,83 @@ def test_large_values_and_short_memories(N, top, Dk):
     for r in range(2):
         _, _, S, lim_S = sized(x, r, len(path), None if r == 0 else before[0])
         check(x, None, None, S, lim_S, x.state.s[2 + r])
+
+
+def one_request(x, src=-1):
+    """The rule from slot src to slot 1, checked."""
+    before = None if src < 0 else x.state.s[src].clone()
+    x.rule(None, i32([src]), i32([1]))
+    out, lim, S, lim_S = sized(x, 0, x.N, before)
+    check(x, out, lim, S, lim_S, x.state.s[1])
+
+
+@pytest.mark.parametrize("N,at", [(16, 12), (64, 60), (64, 1), (200, 130)])
+@pytest.mark.parametrize("dt,size,top", [("bf16", 1.0, 1e6), ("bf16", 1.0, 1e10), ("bf16", 1.0, 1e20), ("bf16", 1e-3, 1e30),
+                                         ("fp16", 1e-3, 6e4)])
+def test_a_large_row_takes_nothing_from_the_others(N, at, dt, size, top):
+    """Rows before it keep what they have, rows behind it what its decay leaves them."""
+    x = Rows(1, N, 1, 2, 64, 64, dt, True, seed=N)
+    x.v.mul_(size / x.v.float().std().item())
+    x.v[0, at] = (x.v[0, at].float().sign() * top).to(x.dtype)
+    x.g.clamp_(max=-0.1)
+    x.g[0, at + 1:at + 3] = -20.0
+    one_request(x)
+    x.state.s[0].mul_(size)
+    one_request(x, 0)
+
+
+@pytest.mark.parametrize("N", [17, 64, 200])
+@pytest.mark.parametrize("dt,size", [("bf16", 1.0), ("bf16", 1e-10), ("fp16", 1e-2)])
+def test_a_large_row_that_is_forgotten(N, dt, size):
+    """Nothing of it is left where the next row's decay is 0: not in the outputs, not in
+    the state."""
+    x = Rows(1, N, 1, 2, 64, 64, dt, True, seed=N + 1)
+    x.v.mul_(size)
+    x.v[0, N // 2] = 6e4
+    x.g.clamp_(max=-0.1)
+    x.g[0, N // 2 + 1] = -math.inf
+    one_request(x)
+
+
+@pytest.mark.parametrize("N", [17, 64])
+@pytest.mark.parametrize("step", [1e3, 1e5, 1e7])
+def test_a_large_step_takes_nothing_from_the_others(N, step):
+    x = Rows(1, N, 1, 2, 64, 64, "bf16", True, seed=N + 2)
+    x.g.clamp_(max=-0.1)
+    x.beta[0, N // 2] = step
+    x.g[0, N // 2 + 1] = -30.0
+    one_request(x)
+
+
+@pytest.mark.parametrize("N", [1, 17, 64, 130])
+@pytest.mark.parametrize("size", [1e-12, 1e-24, 1e-30])
+def test_small_values(N, size):
+    """From the zero state, and from one of their size."""
+    x = Rows(1, N, 1, 2, 64, 64, "bf16", True, seed=N + 3)
+    x.v.mul_(size)
+    one_request(x)
+    x.state.s[0].mul_(size)
+    one_request(x, 0)
+
+
+@pytest.mark.parametrize("dt,length", [("fp16", 1e-4), ("fp16", 3e-3), ("fp16", 50.0), ("bf16", 1e-8), ("bf16", 1e8)])
+def test_keys_and_queries_of_any_length(dt, length):
+    """Some rows' keys and queries far shorter or longer than the others', brought to one."""
+    N = 130
+    x = Rows(1, N, 1, 2, 128, 64, dt, True, seed=7)
+    x.k[0, 3::5].mul_(length)
+    x.q[0, 4::7].mul_(length)
+    x.g.clamp_(max=-0.1)
+    one_request(x, 0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("N", [17, 64, 100])
+def test_little_is_left_of_a_stretch(N, dt):
+    """The last row's decay takes all rows' parts of the state down by 2^-20: what is left
+    is as exact as before."""
+    x = Rows(1, N, 1, 2, 128, 64, dt, True, seed=N + 4)
+    x.g.clamp_(max=-0.1)
+    x.g[0, -1] = -14.0
+    x.beta[0, -1] = 0.0
+    one_request(x, 0)

@@ -20,11 +20,15 @@
 // takes of the updates, go in as sums of numbers of their type: three of bf16,
 // each the front of what is left (24 bits), or two of fp16 after a power of two
 // for each column (22 bits).  What meets no key or query (the right sides, the
-// system's inverse, the updates) is two fp16 numbers, 22 bits, under a power of
-// two for each column.  So results are fp32's: products of two low halves are
-// left out (2^-22).  The state itself stays in fp32 registers: the tensor cores' sums
-// cut off what they cannot hold, and a step added to it there, sixteen rows at a time,
-// left slow heads' states 3e-6 off after some thousand rows.
+// system's inverse, P, the updates) is three bf16 numbers, each row's as exact as
+// if it were alone: rows of a chunk differ in size by whatever their values, steps
+// and decays do, and two fp16 numbers under a power of two for a column took from
+// the small ones what the largest, a later one too, left no room for.  Six of the
+// nine products of two such sums are made, smallest first; what the others leave
+// out is 2^-24 of a term on average, and below 2^-21.  So results are fp32's.  The
+// state itself stays in fp32 registers: the tensor cores' sums cut off what they
+// cannot hold, and a step added to it there, sixteen rows at a time, left slow heads'
+// states 3e-6 off after some thousand rows.
 //
 // A block has one head's state, transposed: a column of the state is a lane of
 // tensor memory, which two threads of the chain share, half of the column and
@@ -36,12 +40,13 @@
 //
 // Columns of a state do not mix, but rows of a chunk do: 0 times what a later
 // row holds is no zero where that is a NaN or an infinity.  A chunk in which
-// anything is not finite, or leaves fp16's range, is done over row by row from
-// the inputs, in fp32, by the chain's threads.
+// anything is not finite, or grows as no working layer's does, is done over row
+// by row from the inputs, in fp32, by the chain's threads.
 //
-// A prompt of 4001 rows and 32 heads of 128 x 128 takes 417 us: 12,900 cycles a chunk,
+// A prompt of 4001 rows and 32 heads of 128 x 128 takes 432 us: 13,300 cycles a chunk,
 // which prep and chain both need, each a line of phases that wait for one another, and
-// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 369 us.
+// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 388 us.  (With two fp16
+// numbers for the right sides, the inverse and the updates 416 and 367 us.)
 #include <atomic>
 #include <type_traits>
 
@@ -54,7 +59,11 @@ constexpr int C = 64;         // rows of a chunk
 constexpr int MAX_DK = 128;
 constexpr int LANES = 128;    // columns of a state in a block
 constexpr int CHAIN = 256, PREP = 256, THREADS = CHAIN + PREP;
-constexpr float MAX_HALF = 65504.f;
+// Largest elements of a chunk, past which it goes row by row: of the inverse and of P (unit
+// keys and steps up to 1 leave 1), of S^T K^T and the right sides (past it what a product
+// of decays below fp32's smallest takes with it may count), and of the updates' factors in
+// the step.  Within them all that follows is finite.
+constexpr float MOST = 0x1p16f, MOST_SUM = 0x1p60f, MOST_UNTIL = 0x1p40f;
 // Registers of the two roles' threads: what the one gives up the other takes.
 constexpr int LAUNCH_REGS = 128, PREP_REGS = 96, CHAIN_REGS = 160;
 static_assert(PREP * PREP_REGS + CHAIN * CHAIN_REGS == THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS == 65536, "registers of an SM");
@@ -68,12 +77,13 @@ struct Coef {                              // of a chunk's rows
 };
 struct alignas(1024) Stage {
   uint8_t kq[2 * BLOCK];  // keys' 64 rows, then queries': [64-column block][row][128 bytes, swizzled]
-  uint8_t th[TRI], tl[TRI], ph[TRI], pl[TRI];
+  uint8_t p3[3][TRI];     // P's parts
   uint16_t v[C * LANES];
-  Coef c;
 };
 struct Smem {
   Stage st[2];
+  uint8_t t3[3][TRI];                      // the inverse's parts, of one chunk
+  Coef c[2];
   float At[C * PAD], T[C * PAD];           // A transposed; the inverse
   uint16_t out[C * LANES];
   float n2[2 * C];                         // squared lengths
@@ -90,8 +100,8 @@ static_assert(SMEM <= 232448, "shared memory of one CTA");
 
 // Tensor memory, columns.  What is written over what has been read by then.
 constexpr int TM_S = 0;      // the state's step
-constexpr int TM_H = 128;    // the state's parts (64 each); right sides' halves (32 + 32), then the updates'
-constexpr int TM_Z = 192;    // the parts of the updates times their decays (32 each)
+constexpr int TM_H = 128;    // the state's parts (64 each); right sides' parts (32 each), then the updates'
+constexpr int TM_Z = 224;    // the parts of the updates times their decays (32 each)
 constexpr int TM_XK = 320;   // S^T K^T; the updates
 constexpr int TM_XQ = 384;   // S^T Q^T, then outputs
 constexpr int TM_G = 448;    // [K; Q] K^T
@@ -194,6 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
     for (int i = t; i < C * PAD; i += PREP) sm.T[i] = 0.f;  // above its diagonal blocks it stays so
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
+      Coef &cf = sm.c[n & 1];
       const int row0 = n * C;
       wait_warp(&sm.empty[n & 1], ((n >> 1) & 1u) ^ 1u);
       float most = 0.f;  // largest magnitude, NaN where there is one
@@ -304,12 +315,12 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (!is_q) {
           const float4 end = sm.cc[C - 1];
           const float until = ex2((end.x - ci.x) + (end.y - ci.y)) * power;
-          st.c.rhs[row] = make_float2(br, -brr * ec * power);
-          st.c.until[row] = until;
-          if (row == C - 1) st.c.end = ec;
-          if (!finite(br) || !finite(brr * ec * power) || !finite(until)) bad = true;
+          cf.rhs[row] = make_float2(br, -brr * ec * power);
+          cf.until[row] = until;
+          if (row == C - 1) cf.end = ec;
+          if (!finite(br) || !finite(brr * ec * power) || !(until <= MOST_UNTIL)) bad = true;
         } else {
-          st.c.eq[row] = ec * power;
+          cf.eq[row] = ec * power;
           sm.fq[n % 3][row] = left * p.scale;
           if (!finite(left) || !finite(ec)) bad = true;
         }
@@ -334,13 +345,13 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (is_q) {
 #pragma unroll
           for (int k8 = 0; k8 < 4; ++k8) {
-            uint32_t hi[4], lo[4];
+            uint32_t y[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              halves(__uint_as_float(x[k8 * 8 + 2 * e]), __uint_as_float(x[k8 * 8 + 2 * e + 1]), hi[e], lo[e]);
+              thirds(__uint_as_float(x[k8 * 8 + 2 * e]), __uint_as_float(x[k8 * 8 + 2 * e + 1]), y[0][e], y[1][e], y[2][e]);
             const int at = row * 128 + ((((j1 >> 3) + k8) ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4 *>(st.ph + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(st.pl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(st.p3[e] + at) = make_uint4(y[e][0], y[e][1], y[e][2], y[e][3]);
           }
         } else {
 #pragma unroll
@@ -440,8 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         *reinterpret_cast<float4 *>(&sm.T[(i + 1) * PAD + j]) = acc[1];
       }
       named_sync(2, PREP);
+      if (n) wait_warp(&sm.u, (n - 1) & 1u);  // the chunk before is done with its own
       {
-        // its halves: a quarter of a row a thread
+        // its parts: a quarter of a row a thread
         const int i = t >> 2, j1 = (t & 3) * 16;
 #pragma unroll
         for (int k8 = 0; k8 < 2; ++k8) {
@@ -452,19 +464,20 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           most = max_nan(most, a.z, a.w);
           most = max_nan(most, b.x, b.y);
           most = max_nan(most, b.z, b.w);
-          uint4 hi, lo;
-          halves(a.x, a.y, hi.x, lo.x);
-          halves(a.z, a.w, hi.y, lo.y);
-          halves(b.x, b.y, hi.z, lo.z);
-          halves(b.z, b.w, hi.w, lo.w);
+          uint4 x, y, z;
+          thirds(a.x, a.y, x.x, y.x, z.x);
+          thirds(a.z, a.w, x.y, y.y, z.y);
+          thirds(b.x, b.y, x.z, y.z, z.z);
+          thirds(b.z, b.w, x.w, y.w, z.w);
           const int at = i * 128 + (((j0 >> 3) ^ (i & 7)) << 4);
           if (ok) {
-            *reinterpret_cast<uint4 *>(st.th + at) = hi;
-            *reinterpret_cast<uint4 *>(st.tl + at) = lo;
+            *reinterpret_cast<uint4 *>(sm.t3[0] + at) = x;
+            *reinterpret_cast<uint4 *>(sm.t3[1] + at) = y;
+            *reinterpret_cast<uint4 *>(sm.t3[2] + at) = z;
           }
         }
       }
-      if (bad || !(most < MAX_HALF)) sm.bad[n & 1] = 1;
+      if (bad || !(most < MOST)) sm.bad[n & 1] = 1;
       fence_async_smem();
       named_sync(2, PREP);
       if (t == 0 && ok) mbar_arrive(&sm.full[n & 1]);
@@ -494,7 +507,6 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           st_global16(p.out + ((tok0 + i) * p.Hv + h) * p.Dv + slice * LANES + ch * 8, make_uint4(0, 0, 0, 0));
     }
     int pending = -1;  // chunk whose outputs wait in tensor memory
-    float out_scale = 0.f;
     auto arrive = [&](uint64_t *bar) {
       tmem_wait_st();
       tc_fence_before();
@@ -520,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (next) arrive(&sm.pq);
         // all that is read before all that is written: a load does not pass a store
 #pragma unroll
-        for (int i = 0; i < SC; ++i) x[i] = pack2<T>(__uint_as_float(x[i]) * out_scale * fq[i0 + i], 0.f);
+        for (int i = 0; i < SC; ++i) x[i] = pack2<T>(__uint_as_float(x[i]) * fq[i0 + i], 0.f);
 #pragma unroll
         for (int i = 0; i < SC; ++i) sm.out[(i0 + i) * LANES + l] = (uint16_t)x[i];
       }
@@ -557,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           : "memory");
       return y != 0;
     };
-    constexpr uint32_t id = idesc_16<__half>(128, C, false), id_t = idesc_16<T>(128, C, false), id_kd = idesc_16<T>(128, 128, true);
+    constexpr uint32_t id_t = idesc_16<T>(128, C, false), id_kd = idesc_16<T>(128, 128, true);
     const int steps = p.Dk / 16;
     // Products: one lane of warp `who` issues them once all of the chain's warps have
     // arrived; a warp for each kind, so that none is held up for long.
@@ -571,12 +583,27 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       __syncwarp();
     };
 
+    // D (+)= A B^T of two sums of three bf16 numbers, rows of A in tensor memory (TM_H), B
+    // lower triangular: places 16 k .. have nothing for the rows before 16 k.
+    auto triangle = [&](uint32_t d, const uint8_t (&b3)[3][TRI], bool add) {
+      constexpr int A[6] = {0, 1, 2, 0, 1, 0}, B[6] = {2, 1, 0, 1, 0, 0};  // smallest first
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        const uint32_t b = desc_lo(smem_u32(b3[B[i]]), 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ts(tmem + d + k * 16, tmem + TM_H + A[i] * 32 + k * 8, b + (k * 16 * 128 >> 4) + k * 2,
+                 idesc_16<__nv_bfloat16>(128, C - k * 16, false), add || i != 0 || k != 0);
+      }
+    };
+
     for (int n = 0; n < n_chunk; ++n) {
       Stage &st = sm.st[n & 1];
+      const Coef &cf = sm.c[n & 1];
       const uint32_t xq = me + TM_XQ + i0;
       const uint32_t par = n & 1u;
       bool bad = false;
-      // the state's halves; the updates' of the chunk before, which they go over, have
+      // the state's parts; the updates' of the chunk before, which they go over, have
       // been read with its outputs
       if (pending >= 0) wait_warp(&sm.o, pending & 1u);
       tc_fence_after();
@@ -647,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float2 f = st.c.rhs[i0 + part + i];
+          const float2 f = cf.rhs[i0 + part + i];
           const float v = to_float<T>(st.v[(i0 + part + i) * LANES + l]);
           b[part + i] = fmaf(f.y, BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_s, f.x * v);
         }
@@ -657,46 +684,36 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       top = 0.f;
 #pragma unroll
       for (int i = 0; i < SC; i += 2) top = max_nan(top, b[i], b[i + 1]);
-      // A column of the state that is not finite has nothing more to lose; one that leaves
-      // the outputs' common scale no room goes row by row too.
-      const bool had = finite(x_top);
-      if (had && (!finite(top) || x_top * back_s > 0x1p60f)) bad = true;
-      top = of_both(1, top);
-      float back_b;
-      float up_b = power_for(top, 11, back_b);
-      if (back_b < back_s * 0x1p-60f) {  // nothing to add: the outputs' common scale stays near the state's
-        back_b = back_s * 0x1p-60f;
-        up_b = 1.f / back_b;  // a power of two
+      // A column of the state that is not finite has nothing more to lose.
+      bool lost = false;
+      if (!(top <= MOST_SUM) || !(x_top * back_s <= MOST_SUM)) {
+        float most = 0.f;
+#pragma unroll
+        for (int d = 0; d < SD; d += 2) most = max_nan(most, s[d], s[d + 1]);
+        lost = !finite(most);
+        bad = !lost;
       }
-      wait_warp(&sm.xq, par);  // the state's halves have been read
+      wait_warp(&sm.xq, par);  // the state's parts have been read
       tc_fence_after();
-      {
-        const uint64_t up = pair(up_b, up_b);
 #pragma unroll
-        for (int i = 0; i < SC; i += 16) {
-          uint32_t hi[8], lo[8];
+      for (int i = 0; i < SC; i += 16) {
+        uint32_t x[8], y[8], z[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) halves_at(pair(b[i + 2 * e], b[i + 2 * e + 1]), up, hi[e], lo[e]);
-          if (ok) {
-            tmem_st8(me + TM_H + (i0 + i) / 2, hi);
-            tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
-          }
+        for (int e = 0; e < 8; ++e) thirds(b[i + 2 * e], b[i + 2 * e + 1], x[e], y[e], z[e]);
+        if (ok) {
+          tmem_st8(me + TM_H + (i0 + i) / 2, x);
+          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, y);
+          tmem_st8(me + TM_H + 64 + (i0 + i) / 2, z);
         }
       }
       arrive(&sm.pb);
       products(1, &sm.pb, par, [&]() {
-        const uint32_t th = desc_lo(smem_u32(st.th), 16), tl = desc_lo(smem_u32(st.tl), 16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, th + (k & 3) * 2, id, k != 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ts(tmem + TM_XK, tmem + TM_H + k * 8, tl + k * 2, id, 1);
+        triangle(TM_XK, sm.t3, false);
         tc_commit(&sm.u);
       });
-      // meanwhile the outputs' first part, to the updates' scale (2^3 less than the right sides')
-      up_b *= 0.125f;
-      back_b *= 8.f;
+      // meanwhile the outputs' first part
+      float most = 0.f;
       if (ok) {
-        const float f = up_b * back_s;
 #pragma unroll
         for (int part = 0; part < SC; part += 16) {
           uint32_t x[16];
@@ -704,8 +721,11 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           tmem_wait_ld();
           tie16(x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * (f * st.c.eq[i0 + part + i]));
+          for (int i = 0; i < 16; ++i)
+            x[i] = __float_as_uint((BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_s) * cf.eq[i0 + part + i]);
           tmem_st16(xq + part, x);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) most = max_nan(most, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
         }
       }
       // the updates
@@ -719,24 +739,31 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           tmem_wait_ld();
           tie16(x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) b[part + i] = __uint_as_float(x[i]) * 0.125f;
+          for (int i = 0; i < 16; ++i) b[part + i] = __uint_as_float(x[i]);
         }
       }
-      float most = 0.f;
+      float up_z = 1.f, back_z = 1.f;  // of what the state's step takes of them
+      if (!BF16) {
+        top = 0.f;
 #pragma unroll
-      for (int e = 0; e < SC; e += 2) most = max_nan(most, b[e], b[e + 1]);
+        for (int i = 0; i < SC; i += 2) {
+          const float2 f = *reinterpret_cast<const float2 *>(&cf.until[i0 + i]);
+          top = max_nan(top, b[i] * f.x, b[i + 1] * f.y);
+        }
+        top = of_both(1, top);
+        up_z = power_for(top, 14, back_z);
+      }
 #pragma unroll
       for (int i = 0; i < SC; i += 16) {
         uint32_t x[8], y[8], z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 f = *reinterpret_cast<const float2 *>(&st.c.until[i0 + i + 2 * e]);
+          const float2 f = *reinterpret_cast<const float2 *>(&cf.until[i0 + i + 2 * e]);
+          const float z0 = b[i + 2 * e] * f.x, z1 = b[i + 2 * e + 1] * f.y;
           if (BF16) {
-            thirds(b[i + 2 * e] * back_b * f.x, b[i + 2 * e + 1] * back_b * f.y, x[e], y[e], z[e]);
+            thirds(z0, z1, x[e], y[e], z[e]);
           } else {
-            const float z0 = b[i + 2 * e] * f.x, z1 = b[i + 2 * e + 1] * f.y;
-            most = max_nan(most, z0, z1);
-            halves(z0, z1, x[e], y[e]);
+            halves(z0 * up_z, z1 * up_z, x[e], y[e]);
           }
         }
         if (ok) {
@@ -745,7 +772,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
           if (BF16) tmem_st8(me + TM_Z + 64 + (i0 + i) / 2, z);
         }
       }
-      if (bad || (had && !(most < MAX_HALF))) *(volatile int *)&sm.chain_bad = n + 1;
+      if (bad || (!lost && !finite(most))) *(volatile int *)&sm.chain_bad = n + 1;
       arrive(&sm.pz);
       products(2, &sm.pz, par, [&]() {
         const uint32_t kd = desc_lo(smem_u32(st.kq), BLOCK);
@@ -756,23 +783,20 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       });
 #pragma unroll
       for (int i = 0; i < SC; i += 16) {
-        uint32_t hi[8], lo[8];
+        uint32_t x[8], y[8], z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) halves(b[i + 2 * e], b[i + 2 * e + 1], hi[e], lo[e]);
+        for (int e = 0; e < 8; ++e) thirds(b[i + 2 * e], b[i + 2 * e + 1], x[e], y[e], z[e]);
         if (ok) {
-          tmem_st8(me + TM_H + (i0 + i) / 2, hi);
-          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, lo);
+          tmem_st8(me + TM_H + (i0 + i) / 2, x);
+          tmem_st8(me + TM_H + 32 + (i0 + i) / 2, y);
+          tmem_st8(me + TM_H + 64 + (i0 + i) / 2, z);
         }
       }
       const bool slow_prep = *(volatile int *)&sm.bad[n & 1] != 0;
-      const float end = st.c.end;
+      const float end = cf.end;
       arrive(&sm.py);
       products(3, &sm.py, par, [&]() {
-        const uint32_t ph = desc_lo(smem_u32(st.ph), 16), pl = desc_lo(smem_u32(st.pl), 16), d = tmem + TM_XQ;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_ts(d, tmem + TM_H + k * 8, ph + (k & 3) * 2, id, 1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ts(d, tmem + TM_H + k * 8, pl + k * 2, id, 1);
+        triangle(TM_XQ, st.p3, true);
         tc_commit(&sm.o);
         tc_commit(&sm.empty[n & 1]);  // with the state's step the last to read this stage
       });
@@ -789,12 +813,11 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
             tie16(x);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              s[part + i] = fmaf(s[part + i], end, BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_b);
+              s[part + i] = fmaf(s[part + i], end, BF16 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back_z);
           }
           tc_fence_before();
         }
         pending = n;
-        out_scale = back_b;
         continue;
       }
       // The chunk row by row, from the inputs, as delta_rows.cu does it; the column's two
