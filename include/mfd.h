@@ -501,8 +501,10 @@ typedef struct {
  *            k and v
  *   src, dst int32 [n_req] or NULL, see above
  * Sums and the state are fp32, products too or of operands that keep 22 bits of
- * each factor.  Results do not change from run to run.  What a row holds reaches
- * no row before it, infinities and NaN included.
+ * each factor; but with MFD_FP16, from 18 rows on and in trees, an element of the
+ * state is known to 2^-39 of its column's largest at best.  A product of decays
+ * below 2^-126 is 0.  Results do not change from run to run.  What a row holds
+ * reaches no row before it, infinities and NaN included.
  * normalize: 0 or 1; eps >= 0; scale finite.
  * Limits: as for the state; n_req * N < 2^31, n_req * Hv * 8 < 2^31.  Device
  * errors (MFD_ERR_INPUT): n_nodes outside [0, N], a slot outside [-1, n_slots);

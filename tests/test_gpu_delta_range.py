@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from delta_helpers import Rows, i32, unit
+from delta_helpers import Rows, i32, random_tree, unit
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +161,34 @@ def test_little_is_left_of_a_stretch(N, dt):
     x.g[0, -1] = -14.0
     x.beta[0, -1] = 0.0
     one_request(x, 0)
+
+
+@pytest.mark.parametrize("N", [17, 64, 100])
+@pytest.mark.parametrize("dt,size", [("bf16", 1e-6), ("fp16", 0.05), ("fp16", 1e-3)])
+def test_a_state_of_unlike_rows(N, dt, size):
+    """A row of the state that no key and no query meets, far larger than the rest: what
+    meets it not is as it would be without it, but for 2^-39 of it with fp16."""
+    x = Rows(1, N, 1, 2, 64, 64, dt, True, seed=N + 5)
+    for t in (x.q, x.k):
+        t[..., 0] = 0
+    x.v.mul_(size)
+    x.g.clamp_(max=-0.1)
+    x.state.s.mul_(size)
+    rest = x.state.s[0].clone()
+    rest[:, 0] = 0
+    x.state.s[0, :, 0] = 6e4
+    par = random_tree(N, torch.Generator().manual_seed(N), back=9)
+    # a row takes in Dk elements of the state that are off by that, and its keys and queries
+    # are of length one; a step by each row before (17 nodes of a path) adds to what is off
+    floor = 0 if dt == "bf16" else 2.0 ** -39 * 6e4 * 64 ** 0.5
+    for form in ("rule", "tree"):
+        if form == "rule":
+            x.rule(None, i32([0]), i32([1]))
+        else:
+            x.tree(i32([par]), None, i32([0]))
+        out, lim, S, lim_S = sized(x, 0, N, rest, par if form == "tree" else None)
+        passed = torch.cumsum(torch.exp(torch.cumsum(x.g[0].double(), 0)), 0)[..., None] if form == "rule" else torch.full((1, 1, 1), 17.0, device="cuda")
+        lim = lim + abs(x.scale) * floor * (1 + passed)
+        check(x, out, lim)
+        if form == "rule":
+            check(x, None, None, S[:, 1:], lim_S + floor * (1 + passed[-1]), x.state.s[1, :, 1:])

@@ -19,7 +19,8 @@
 // they are; their powers are in the other factors.  The state, and what its step
 // takes of the updates, go in as sums of numbers of their type: three of bf16,
 // each the front of what is left (24 bits), or two of fp16 after a power of two
-// for each column (22 bits).  What meets no key or query (the right sides, the
+// for each column, which brings its largest to [2^14, 2^15) (22 bits of what is at
+// least 2^-17 of that; 2^-39 of the largest below).  What meets no key or query (the right sides, the
 // system's inverse, P, the updates) is three bf16 numbers, each row's as exact as
 // if it were alone: rows of a chunk differ in size by whatever their values, steps
 // and decays do, and two fp16 numbers under a power of two for a column took from
@@ -45,7 +46,7 @@
 //
 // A prompt of 4001 rows and 32 heads of 128 x 128 takes 432 us: 13,300 cycles a chunk,
 // which prep and chain both need, each a line of phases that wait for one another, and
-// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 388 us.  (With two fp16
+// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 388 us, 437 and 366 in fp16.  (With two fp16
 // numbers for the right sides, the inverse and the updates 416 and 367 us.)
 #include <atomic>
 #include <type_traits>
@@ -106,17 +107,6 @@ constexpr int TM_XK = 320;   // S^T K^T; the updates
 constexpr int TM_XQ = 384;   // S^T Q^T, then outputs
 constexpr int TM_G = 448;    // [K; Q] K^T
 
-// Halves of x times a power of two that brings the column's largest to [2^11,
-// 2^12): hi is x to the nearest even number, 11 bits at most, lo what is left, to
-// 2^-12 of 1.  The two roundings by 1.5 * 2^24 cost no conversions back.
-__device__ __forceinline__ void halves_at(uint64_t x, uint64_t up, uint32_t &hi, uint32_t &lo) {
-  const uint64_t grid = pair(0x1.8p24f, 0x1.8p24f), back = pair(-0x1.8p24f, -0x1.8p24f), minus = pair(-1.f, -1.f);
-  const uint64_t a = add2(fma2(x, up, grid), back);
-  const float2 h = unpair(a), l = unpair(fma2(x, up, fma2(a, minus, pair(0.f, 0.f))));
-  const __half2 hh = __floats2half2_rn(h.x, h.y), ll = __floats2half2_rn(l.x, l.y);
-  hi = *reinterpret_cast<const uint32_t *>(&hh);
-  lo = *reinterpret_cast<const uint32_t *>(&ll);
-}
 // Three bf16 numbers of two floats: each the front of what is left.
 __device__ __forceinline__ void thirds(float a, float b, uint32_t &x, uint32_t &y, uint32_t &z) {
   x = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
@@ -624,13 +614,12 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
 #pragma unroll
         for (int d = 0; d < SD; d += 2) top = max_nan(top, s[d], s[d + 1]);
         top = of_both(0, top);
-        const float up = power_for(top, 11, back_s);
-        const uint64_t up2 = pair(up, up);
+        const float up = power_for(top, 14, back_s);
 #pragma unroll
         for (int d = 0; d < SD; d += 16) {
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) halves_at(pair(s[d + 2 * e], s[d + 2 * e + 1]), up2, hi[e], lo[e]);
+          for (int e = 0; e < 8; ++e) halves(s[d + 2 * e] * up, s[d + 2 * e + 1] * up, hi[e], lo[e]);
           if (ok) {
             tmem_st8(me + TM_H + (d0 + d) / 2, hi);
             tmem_st8(me + TM_H + 64 + (d0 + d) / 2, lo);

@@ -26,7 +26,9 @@
 //
 // Keys and queries go to the tensor cores as they are.  The state goes in as a
 // sum of numbers of their type: three of bf16, each the front of what is left
-// (24 bits), or two of fp16 after a power of two for each column (22 bits).
+// (24 bits), or two of fp16 after a power of two for each column, which brings its
+// largest to [2^14, 2^15) (22 bits of what is at least 2^-17 of that; 2^-39 of the
+// largest below).
 //
 // 32 trees of 129 nodes and 32 heads of 128 x 128 take 132 us, a head some 36,000
 // cycles of an SM: a third until its state and rows have come and the root is done,
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_tree_kernel(const DeltaArgs 
         red[(tid >> 7) * 128 + l] = top;
         sync();
         top = max_nan(max_nan(red[l], red[128 + l], red[256 + l]), red[384 + l], 0.f);
-        const float up = power_for(top, 11, back);
+        const float up = power_for(top, 14, back);
         uint32_t lo[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) halves(s[2 * e] * up, s[2 * e + 1] * up, part[e], lo[e]);
