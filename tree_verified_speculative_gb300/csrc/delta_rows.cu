@@ -311,11 +311,13 @@ cudaError_t launch_width(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
 
 template <typename T, int MODE>
 cudaError_t launch_mode(const DeltaArgs &A, int n_sm, cudaStream_t stream) {
-  // Narrower slices where few heads leave SMs without work: one token of 4 requests of 32
-  // heads takes 5.9 us so, 6.6 with four warps; of 8 requests 9.1 and 7.4.  A path's
-  // blocks have more to do in turn: 6.0 and 5.6 us for one request.
+  // Narrower slices where few heads leave SMs without work, for one token: of 4 requests of
+  // 32 heads it takes 5.9 us so, 6.6 with four warps; of 8 requests 9.1 and 7.4.  Blocks
+  // that have rows to do in turn, or a path, are no faster so: 6.0 and 5.6 us for one
+  // request's path; 17 rows of one request 21.1 and 19.1 us, of 4 requests 23.2 and 21.1
+  // (a call by events, the L2 cache flushed before it).
   const int64_t heads = (int64_t)A.n_req * A.Hv;
-  if (MODE == RULE && heads * ((A.Dv + 63) / 64) <= 2 * n_sm) return launch_width<T, 2, RULE>(A, n_sm, stream);
+  if (MODE == RULE && A.N == 1 && heads * ((A.Dv + 63) / 64) <= 2 * n_sm) return launch_width<T, 2, RULE>(A, n_sm, stream);
   return launch_width<T, 4, MODE>(A, n_sm, stream);
 }
 template <int MODE>
