@@ -135,3 +135,24 @@ def test_residual_keeps_rows_apart():
     for a, b in zip(*outs):
         assert torch.equal(a[keep], b[keep])
     assert bool(torch.isnan(outs[1][0][2]).all()) and bool(torch.isnan(outs[1][1][2]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gates_far_below_zero(dt, act):
+    """Down to where the type's smallest number ends, and up to where a sigmoid is 1."""
+    dtype = DT[dt]
+    z = torch.cat([torch.arange(-110, -80, 0.125), torch.arange(-20, 100, 0.5)]).to(dtype).cuda()
+    z = z[:z.numel() // 8 * 8].view(-1, 1, 8).contiguous()
+    x, w, out = torch.ones_like(z), torch.ones(8, dtype=dtype, device="cuda"), torch.empty_like(z)
+    mfd.mfd_gated_norm(x, z, w, 0.0, act, out)
+    rows = z.flatten().expand(2, -1).contiguous()
+    y, r = torch.ones_like(rows), torch.empty_like(rows)
+    mfd.mfd_residual_norm(y, torch.zeros_like(y), None, rows, act, 1.0, None, EPS, r, None)
+    torch.cuda.synchronize()
+    want = act64(z, act)
+    # the exponential's argument, 1.45 |z| + 32 at most, is rounded to 2^-24 of itself
+    lim = off(want, 8, dtype) + (1.45 * z.double().abs() + 32) * 2.0 ** -24 * want.abs()
+    assert bool(((out.double() - want).abs() <= lim).all())
+    assert bool(((r.double() - want.flatten()).abs() <= lim.flatten()).all())
+    assert dt == "fp16" or float(out[z == -88.5].double().abs().max()) > 0
