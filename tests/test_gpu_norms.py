@@ -156,3 +156,55 @@ def test_gates_far_below_zero(dt, act):
     assert bool(((out.double() - want).abs() <= lim).all())
     assert bool(((r.double() - want.flatten()).abs() <= lim.flatten()).all())
     assert dt == "fp16" or float(out[z == -88.5].double().abs().max()) > 0
+
+
+@pytest.mark.parametrize("T,H,dt", [(1, 2560, "bf16"), (5, 264, "fp16"), (300, 1024, "fp16"), (5000, 264, "bf16"), (2500, 2560, "bf16"),
+                                    (701, 6400, "bf16"), (403, 8320, "bf16"), (403, 16384, "fp16")])
+def test_residual_and_the_next_norm(T, H, dt):
+    """The plain end of a block, without a norm of its output and without a gate: one sum
+    a row, for rows that all are resident and for more."""
+    g = torch.Generator("cuda").manual_seed(T)
+    dtype = DT[dt]
+    y, r = normal(g, T, H).to(dtype), (3 * normal(g, T, H)).to(dtype)
+    w = (1 + 0.3 * normal(g, H)).to(dtype)
+    ro, xo = torch.empty_like(y), torch.empty_like(y)
+    mfd.mfd_residual_norm(y, r, None, None, "none", 1.0, w, EPS, ro, xo)
+    torch.cuda.synchronize()
+    want = r.double() + y.double()
+    fp32 = 2.0 ** -24 * want.abs()  # the sum, rounded once
+    assert bool(((ro.double() - want).abs() <= fp32 + off(want, 0, dtype)).all())
+    x = norm64(want, w)
+    # a row's sum of squares carries twice the relative error of its terms, its root once
+    assert bool(((xo.double() - x).abs() <= off(x, H, dtype) + 2.0 ** -22 * x.abs()).all())
+    for over in ("residual", "y"):  # in place: the sum over one input, the normed row over the other
+        a, b = y.clone(), r.clone()
+        sum_to, x_to = (b, a) if over == "residual" else (a, b)
+        mfd.mfd_residual_norm(a, b, None, None, "none", 1.0, w, EPS, sum_to, x_to)
+        torch.cuda.synchronize()
+        assert torch.equal(sum_to, ro) and torch.equal(x_to, xo)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_rows_of_the_largest_numbers(dt):
+    """Their squares are summed in fp32: past its largest number (bf16 only) a row's norm
+    is 0; rows beside it are as without it."""
+    dtype = DT[dt]
+    top = torch.finfo(dtype).max
+    x = torch.ones((4, 2, 64), dtype=dtype, device="cuda")
+    x[1] = top
+    x[2, 0, ::2] = -top
+    w, out = torch.ones(64, dtype=dtype, device="cuda"), torch.empty_like(x)
+    mfd.mfd_gated_norm(x, torch.ones_like(x), w, EPS, "none", out)
+    y, w2 = x.flatten(1), torch.ones(128, dtype=dtype, device="cuda")
+    ro, xo = torch.empty_like(y), torch.empty_like(y)
+    mfd.mfd_residual_norm(y, torch.ones_like(y), w2, None, "none", 1.0, w2, EPS, ro, xo)
+    torch.cuda.synchronize()
+    want = norm64(x, w)
+    want_y = norm64(y, w2)
+    if dt == "bf16":
+        want[1] = want[2, 0] = want_y[1] = want_y[2] = 0
+    assert bool(((out.double() - want).abs() <= off(want, 64, dtype)).all())
+    want_r = 1 + want_y
+    assert bool(((ro.double() - want_r).abs() <= off(want_r, 128, dtype) + off(want_y, 128, torch.float32)).all())
+    want_x = norm64(want_r, w2)
+    assert bool(((xo.double() - want_x).abs() <= off(want_x, 128, dtype) + off(want_y, 128, torch.float32).abs() * 4).all())
