@@ -519,7 +519,10 @@ int mfd_delta_rule(const void *q, int64_t q_stride, const void *k, int64_t k_str
  * from the request's state, which stays as it is.  Arguments as above, and
  *   parent  int32 [n_req][N] from mfd_build_tree: -1 for node 0, else a node
  *           before it; no node more than 16 below the root
- * What a node holds reaches only nodes below it.  N <= 513.  Device errors
+ * What a node holds reaches only nodes below it.  A node's products of the state
+ * with its query and key, and of these with other nodes' keys, are made before the
+ * division by their lengths, and have to stay inside fp32 as such; so does e to the
+ * sum of g along a path.  N <= 513.  Device errors
  * (MFD_ERR_INPUT): as above, and parents that are none; that request's outputs
  * are zero. */
 int mfd_delta_tree(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -544,7 +547,8 @@ int mfd_delta_commit(const void *k, int64_t k_stride, const void *v, int64_t v_s
 enum { MFD_ACT_NONE = 0, MFD_ACT_SIGMOID = 1, MFD_ACT_SILU = 2 };
 
 /* Norm of each head's row times its gate, the end of a recurrent layer:
- *   out = x / sqrt(mean(x^2) + eps) * w * act(gate)   (fp32, one rounding)
+ *   out = x / sqrt(mean(x^2) + eps) * w * act(gate)   (fp32, one rounding; a row
+ *         whose squares' sum passes fp32's largest number gives 0)
  *   x, gate  [T] tokens of [heads][D], x_stride and gate_stride elements apart (a
  *            multiple of 8, at least heads * D), heads contiguous, `dtype`
  *            MFD_BF16 or MFD_FP16, 16-byte aligned
@@ -555,7 +559,8 @@ enum { MFD_ACT_NONE = 0, MFD_ACT_SIGMOID = 1, MFD_ACT_SILU = 2 };
 int mfd_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, int dtype, int T, int heads,
                    int D, const void *w, float eps, int act, void *out, mfd_stream_t stream);
 
-/* A block's end and the next one's start:
+/* A block's end and the next one's start (fp32, one rounding for each output; sums
+ * of squares as above):
  *   y' = y / sqrt(mean(y^2) + eps) * w_post   (w_post NULL: y)
  *   r  = residual + scale * act(gate) * y'    (gate NULL: 1)
  *   x  = r / sqrt(mean(r^2) + eps) * w_pre    (w_pre NULL: no x), from the r that

@@ -192,3 +192,54 @@ def test_a_state_of_unlike_rows(N, dt, size):
         check(x, out, lim)
         if form == "rule":
             check(x, None, None, S[:, 1:], lim_S + floor * (1 + passed[-1]), x.state.s[1, :, 1:])
+
+
+@pytest.mark.parametrize("N", [1, 3, 17, 64, 100])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_what_is_no_number_in_the_formula_is_none(N, what, bad):
+    """A NaN or an infinity in row i: outputs and state are finite where the 64-bit form's
+    are, and nowhere else."""
+    i = N // 2
+    x = Rows(1, N, 2, 2, 64, 64, seed=N)
+    t = getattr(x, what)
+    if what in ("g", "beta"):
+        t[0, i, 1] = bad
+    else:
+        t[0, i, 1, 5] = bad
+    par = random_tree(N, torch.Generator().manual_seed(N), back=5)
+    before = x.state.s[0].clone()
+    x.rule(None, i32([0]), i32([1]))
+    torch.cuda.synchronize()
+    out, S, _ = x.want(0, N, before)
+    assert torch.equal(torch.isfinite(x.out[0]), torch.isfinite(out))
+    assert torch.equal(torch.isfinite(x.state.s[1]), torch.isfinite(S))
+    x.tree(i32([par]), None, i32([0]))
+    torch.cuda.synchronize()
+    out, _, _ = x.want(0, N, before, par)
+    assert torch.equal(torch.isfinite(x.out[0]), torch.isfinite(out))
+    assert int(x.st.item()) == 0
+
+
+@pytest.mark.parametrize("N", [1, 17, 64, 100])
+@pytest.mark.parametrize("length", [1.0, 1e15])
+def test_a_state_far_up(N, length):
+    """A state of 1e25 and, of every fifth row, keys and queries so long that their products
+    with it pass fp32 before they are divided by their length; in a column of it a NaN."""
+    x = Rows(1, N, 1, 2, 64, 64, "bf16", True, seed=N + 6)
+    x.k[0, ::5].mul_(length)
+    x.q[0, ::5].mul_(length)
+    x.g.clamp_(max=-0.1)
+    x.state.s[0].mul_(1e25)
+    x.state.s[0, 1, 3, 7] = math.nan
+    x.rule(None, i32([0]), i32([1]))
+    before = x.state.s[0].clone()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(x.out[0, :, 1, 7]).all()) and bool(torch.isnan(x.state.s[1, 1, :, 7]).all())
+    before[1, :, 7] = 0
+    x.out[0, :, 1, 7] = 0
+    x.state.s[1, 1, :, 7] = 0
+    out, lim, S, lim_S = sized(x, 0, N, before)
+    out[:, 1, 7] = 0
+    S[1, :, 7] = 0
+    check(x, out, lim, S, lim_S, x.state.s[1])
