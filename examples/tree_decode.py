@@ -10,8 +10,8 @@ does the one-token decoding that the result is compared with.
 
 With --hybrid every other layer is recurrent: its state takes the prompt and single
 tokens (mfd_delta_rule), scores the tree (mfd_delta_tree) and moves along the
-accepted path (mfd_delta_commit); its output goes through mfd_gated_norm, and all
-blocks end in mfd_residual_norm.
+accepted path (mfd_delta_commit); its output goes through mfd_gated_norm, and its
+block ends in mfd_residual_norm with the norm that the attention after it starts with.
 
 The drafter is a stand-in: it knows the target's continuation and gets each
 position of each mode wrong with some probability.
@@ -68,9 +68,10 @@ class Target:
             self.ws[N] = torch.empty(n, dtype=torch.uint8, device="cuda")
         x = self.embed[tokens.clamp_min(0).long()]
         for i, (w, cache) in enumerate(zip(self.layers, self.caches)):
+            normed = _norm(x)
             if self.recurrent:
-                x = self.recurrent[i].forward(x, _norm(x), n_nodes, parent, self.ones, self.status)
-            qkv = (_norm(x) @ w["qkv"].T).view(R, N, self.Hq + 2 * self.Hk, self.D)
+                x, normed = self.recurrent[i].forward(x, normed, n_nodes, parent, self.ones, self.status)
+            qkv = (normed @ w["qkv"].T).view(R, N, self.Hq + 2 * self.Hk, self.D)
             q, k, v = qkv.split([self.Hq, self.Hk, self.Hk], dim=2)
             q_out = torch.empty((R, N, self.Hq, self.D), dtype=x.dtype, device="cuda")
             mfd.mfd_kv_append(q, k, v, w["q_w"], w["k_w"], EPS, self.phase, self.D, False, pos, self.ctx, n_nodes, q_out,
@@ -125,8 +126,9 @@ class _Recurrent:
             self.rows = k, v, g, beta
         mfd.mfd_gated_norm(out, z, self.w, EPS, "silu", out)
         y = (out.view(R, N, -1) @ self.o.T).contiguous()
-        mfd.mfd_residual_norm(y, residual.contiguous(), ones, None, "none", 1.0, None, EPS, y, None)
-        return y
+        normed = torch.empty_like(y)
+        mfd.mfd_residual_norm(y, residual.contiguous(), ones, None, "none", 1.0, ones, EPS, y, normed)
+        return y, normed
 
     def keep(self, accept_len, path_nodes, n_nodes, status):
         k, v, g, beta = self.rows
