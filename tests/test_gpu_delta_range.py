@@ -106,6 +106,22 @@ def test_a_large_row_takes_nothing_from_the_others(N, at, dt, size, top):
     one_request(x, 0)
 
 
+@pytest.mark.parametrize("N", [20, 129, 300])
+@pytest.mark.parametrize("dt,size,top", [("bf16", 1.0, 1e10), ("bf16", 1e-3, 1e30), ("fp16", 1e-3, 6e4)])
+def test_a_large_node_takes_nothing_from_the_others(N, dt, size, top):
+    """The same in a tree: large nodes among others, and below them, behind short memories."""
+    x = Rows(1, N, 1, 2, 64, 64, dt, True, seed=N)
+    x.v.mul_(size / x.v.float().std().item())
+    x.v[0, 5::11] = (x.v[0, 5::11].float().sign() * top).to(x.dtype)
+    x.g.clamp_(max=-0.1)
+    x.g[0, 2::3] = -20.0
+    x.state.s[0].mul_(size)
+    par = random_tree(N, torch.Generator().manual_seed(N), back=9)
+    x.tree(i32([par]), None, i32([0]))
+    out, lim, _, _ = sized(x, 0, N, x.state.s[0], par)
+    check(x, out, lim)
+
+
 @pytest.mark.parametrize("N", [17, 64, 200])
 @pytest.mark.parametrize("dt,size", [("bf16", 1.0), ("bf16", 1e-10), ("fp16", 1e-2)])
 def test_a_large_row_that_is_forgotten(N, dt, size):

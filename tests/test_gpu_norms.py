@@ -208,3 +208,25 @@ def test_rows_of_the_largest_numbers(dt):
     assert bool(((ro.double() - want_r).abs() <= off(want_r, 128, dtype) + off(want_y, 128, torch.float32)).all())
     want_x = norm64(want_r, w2)
     assert bool(((xo.double() - want_x).abs() <= off(want_x, 128, dtype) + off(want_y, 128, torch.float32).abs() * 4).all())
+
+
+def test_more_elements_than_32_bits_count():
+    """The last rows of 2^31 elements and more."""
+    T, H = 135000, 16384
+    g = torch.Generator("cuda").manual_seed(2)
+    dtype = torch.bfloat16
+    y, r = (torch.zeros((T, H), dtype=dtype, device="cuda") for _ in range(2))
+    last = slice(T - 3, T)
+    y[last], r[last] = normal(g, 3, H).to(dtype), normal(g, 3, H).to(dtype)
+    w = (1 + 0.3 * normal(g, H)).to(dtype)
+    small = [torch.empty((3, H), dtype=dtype, device="cuda") for _ in range(2)]
+    mfd.mfd_residual_norm(y[last].clone(), r[last].clone(), w, y[last].clone(), "sigmoid", 1.0, w, EPS, *small)
+    x = y.clone()
+    mfd.mfd_residual_norm(y, r, w, x, "sigmoid", 1.0, w, EPS, r, y)
+    torch.cuda.synchronize()
+    assert torch.equal(r[last], small[0]) and torch.equal(y[last], small[1]) and not bool(r[:T - 3].any()) and not bool(y[:T - 3].any())
+    heads = x.view(T, 64, 256)
+    mfd.mfd_gated_norm(heads[last].clone(), heads[last].clone(), w[:256], EPS, "silu", small[0].view(3, 64, 256))
+    mfd.mfd_gated_norm(heads, heads, w[:256], EPS, "silu", y.view(T, 64, 256))
+    torch.cuda.synchronize()
+    assert torch.equal(y[last], small[0]) and not bool(y[:T - 3].any())
