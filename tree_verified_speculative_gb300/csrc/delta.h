@@ -34,8 +34,8 @@ constexpr int DELTA_MAX_DEPTH = 16;   // of a tree's nodes, the root's being 0
 constexpr int DELTA_MAX_NODES = 513;
 
 // Rows from which the rule goes by chunks: what the row form has shared memory for.
-// 17 rows of 32 heads there and 18 here take 15.8 and 15.5 us for one request, 24 and 31
-// for 8, 161 and 227 for 64; a row more costs the row form 0.9, 1.1 and 8 us.
+// 17 rows of 32 heads there and 18 here take 13.5 and 15.9 us for one request, 24 and 33
+// for 8, 159 and 236 for 64; a row more costs the row form 0.6, 1.1 and 8 us.
 constexpr int DELTA_CHUNK_FROM = 18;
 cudaError_t launch_delta_rows(const DeltaArgs &A, int n_sm, cudaStream_t stream);
 cudaError_t launch_delta_chunk(const DeltaArgs &A, cudaStream_t stream);

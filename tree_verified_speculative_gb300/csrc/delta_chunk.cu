@@ -46,7 +46,7 @@
 //
 // A prompt of 4001 rows and 32 heads of 128 x 128 takes 432 us: 13,300 cycles a chunk,
 // which prep and chain both need, each a line of phases that wait for one another, and
-// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 388 us.  (In fp16 437
+// 32 of the SMs have work.  Eight prompts of 975 to 2000 rows take 386 us.  (In fp16 437
 // and 366; with two fp16 numbers for the right sides, the inverse and the updates 416 and
 // 367 in bf16.)
 #include <atomic>

@@ -30,7 +30,7 @@
 // largest to [2^14, 2^15) (22 bits of what is at least 2^-17 of that; 2^-39 of the
 // largest below).
 //
-// 32 trees of 129 nodes and 32 heads of 128 x 128 take 132 us, a head some 36,000
+// 32 trees of 129 nodes and 32 heads of 128 x 128 take 134 us, a head some 36,000
 // cycles of an SM: a third until its state and rows have come and the root is done,
 // the rest phases of 1,000 to 1,500 cycles, each as long as its loads from shared
 // memory and its exchanges take, with a barrier of 16 warps after it.  The tensor cores
