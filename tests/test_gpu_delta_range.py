@@ -156,7 +156,7 @@ def test_small_values(N, size):
     one_request(x, 0)
 
 
-@pytest.mark.parametrize("dt,length", [("fp16", 1e-4), ("fp16", 3e-3), ("fp16", 50.0), ("bf16", 1e-8), ("bf16", 1e8)])
+@pytest.mark.parametrize("dt,length", [("fp16", 1e-4), ("fp16", 3e-3), ("fp16", 50.0), ("bf16", 1e-8), ("bf16", 1e-15), ("bf16", 1e-25), ("bf16", 1e8)])
 def test_keys_and_queries_of_any_length(dt, length):
     """Some rows' keys and queries far shorter or longer than the others', brought to one."""
     N = 130

@@ -13,7 +13,7 @@
 //   S  <- e^(c_end) S + sum_j e^(c_end - c_j) k_j y_j^T
 //
 // where k_j and q_i are taken times a power of two that gives them lengths in
-// [1, 2), and r_i, s_i are what is left of their factors (the norm's among them).
+// [1, 2) (2^40 at most), and r_i, s_i are what is left of their factors (the norm's among them).
 //
 // Operands.  The tensor cores take 16-bit factors.  Keys and queries go in as
 // they are; their powers are in the other factors.  The state, and what its step
@@ -117,6 +117,12 @@ __device__ __forceinline__ void thirds(float a, float b, uint32_t &x, uint32_t &
   a -= __uint_as_float(y << 16);
   b -= __uint_as_float(y & 0xFFFF0000u);
   z = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+// floor(log2 of the length) from its square, at least -40: of a key that short the powers
+// would leave MOST_UNTIL.  Of a key of zeros, which no power makes longer, 0.
+__device__ __forceinline__ int length_exponent(float len2) {
+  return max(((int)(__float_as_uint(len2 > 0.f ? len2 : 1.f) >> 23) - 127) >> 1, -40);
 }
 
 template <typename T>
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
         if (!finite(len2)) bad = true;
         if (part == 0) {
           sm.n2[row] = len2;
-          if (row < C) sm.cc[row].z = __uint_as_float((uint32_t)(127 - (((int)(__float_as_uint(len2 > 0.f ? len2 : 1.f) >> 23) - 127) >> 1)) << 23);
+          if (row < C) sm.cc[row].z = __uint_as_float((uint32_t)(127 - length_exponent(len2)) << 23);
         }
       }
       named_sync(2, PREP);
@@ -296,8 +302,7 @@ __global__ void __launch_bounds__(THREADS, 1) delta_chunk_kernel(const DeltaArgs
       const bool is_q = (t & 127) >= C;
       const float4 ci = sm.cc[row];
       const float len2 = row0 + row < nn ? sm.n2[t & 127] : 1.f;
-      // floor(log2 of the length); of a key of zeros, which no power makes longer, 0
-      const int half_e = ((int)(__float_as_uint(len2 > 0.f ? len2 : 1.f) >> 23) - 127) >> 1;
+      const int half_e = length_exponent(len2);
       const float left = (p.normalize ? rsqrtf(len2 + p.eps) : 1.f) * __uint_as_float((uint32_t)(127 + half_e) << 23);
       const float power = __uint_as_float((uint32_t)(127 - half_e) << 23);
       const float br = sm.beta[row] * left, brr = br * left;
